@@ -65,7 +65,10 @@
 extern "C" {
 #endif
 
-/* 6: msr_set_exchange; 5: MSR_FLAG_FUSED (4: msr_workspace_bytes, msr_chunkwise_noalloc; strong-decay routing; 3: MSR_FLAG_DECAY_ROWNORM,
+/* The entry points of the layer around retention (msr_add_rmsnorm and what
+ * follows it) came after 6 and left the number as it was: they change nothing
+ * that a caller of 6 uses, and a caller of theirs finds them by name.
+ * 6: msr_set_exchange; 5: MSR_FLAG_FUSED (4: msr_workspace_bytes, msr_chunkwise_noalloc; strong-decay routing; 3: MSR_FLAG_DECAY_ROWNORM,
  * msr_qkv_projection, msr_qkv_chunkwise; 2: pos_rows) */
 #define MSR_ABI_VERSION 6
 #define MSR_MAX_HEADS 128 /* H limit (per-head constants travel by value) */
@@ -327,6 +330,102 @@ void msr_set_kernel_events(void *start, void *stop);
  */
 typedef enum { MSR_EXCHANGE_AUTO = 0, MSR_EXCHANGE_OFF = 1, MSR_EXCHANGE_NO_WAIT = 2 } msr_exchange_mode;
 msr_status msr_set_exchange(int32_t mode);
+
+/* ==== the layer around retention =============================================
+ * What a retention layer runs before and after the forms above: the
+ * residual's addition with a root-mean-square norm, and its projections in
+ * 8-bit floating point.  (jsqmd.com section 2: the layer input goes through
+ * linear layers to give Q, K and V; section 5: normalisation.)  They follow
+ * the conventions at the top of this file: device pointers, 16-byte aligned;
+ * row-major arrays; work enqueued on `hip_stream` without synchronising;
+ * everything checked before the first launch.
+ *
+ * 8-bit arrays hold e4m3 values (sign, 4 exponent bits, 3 fraction bits; the
+ * largest is 448, no infinity, NaN 0x7f / 0xff), one byte each, in rows that
+ * are padded with zeros to P(cols) = cols rounded up to a multiple of 128.
+ * Each block of 128 consecutive values of a row (or each square of 128 rows
+ * by 128 columns, see block_rows) has one fp32 scale and stands for
+ * scale * value.  The operators that write them choose
+ *   scale = max(largest magnitude / 448, 2^-126),
+ *   value = round-to-nearest-even(x * (1 / scale));
+ * a block that holds an infinity or a NaN stands for NaN.
+ */
+#define MSR_BLOCK 128
+#define MSR_MAX_NORM_DIM 32768 /* d limit of the norm: a row stays in registers */
+
+/*
+ * h = x + residual (residual NULL: h = x) and its root-mean-square norm
+ *   n = h / sqrt(mean(h^2) + eps) * weight,
+ * for `rows` rows of d values of type dtype (msr_dtype).  weight holds d
+ * values of type weight_dtype (NULL: ones).  n is taken from the unrounded
+ * fp32 h.  Any of the outputs may be NULL (not all of them):
+ *   sum      [rows][d] dtype         h; may be x or residual (in place)
+ *   y        [rows][d] dtype         n; may be x
+ *   q        [rows][P(d)] e4m3 and q_scale [rows][P(d) / 128] (both or
+ *            neither): n in 8 bits, taken from the unrounded n.
+ * Other overlaps of outputs with inputs or each other are not allowed.
+ * 1 <= d <= MSR_MAX_NORM_DIM.
+ */
+msr_status msr_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, const void *x, const void *residual,
+                           const void *weight, int32_t weight_dtype, float eps, void *sum, void *y, void *q,
+                           float *q_scale, void *hip_stream);
+
+/*
+ * Gradients of msr_add_rmsnorm.  h [rows][d] is the forward call's sum (x
+ * when it had no residual), dy = dL/dn (for the 8-bit output: the gradient of
+ * what it stands for, passed straight through the rounding), dsum = dL/dsum
+ * that arrives along the residual stream (NULL: zero), all of type dtype:
+ *   g = weight dy,  dx = rstd (g - h rstd^2 mean(g h)) + dsum
+ *   dweight = sum over the rows of dy h rstd      (fp32 [d]; NULL: skipped)
+ * dx (dtype) is the gradient of x and of the residual alike; it may be dy or
+ * dsum.  Nothing else from the forward call is needed.  The sums over rows
+ * run in a fixed order.  With a dweight it needs a workspace of
+ * msr_add_rmsnorm_backward_workspace(rows, d) bytes.
+ */
+msr_status msr_add_rmsnorm_backward(int64_t rows, int32_t d, int32_t dtype, const void *h, const void *weight,
+                                    int32_t weight_dtype, float eps, const void *dy, const void *dsum, void *dx,
+                                    float *dweight, void *ws, size_t ws_bytes, void *hip_stream);
+size_t msr_add_rmsnorm_backward_workspace(int64_t rows, int32_t d);
+
+/*
+ * x [rows][cols] (dtype) in 8 bits, in its own order, transposed, or both:
+ *   q  [rows][P(cols)] with scale,   qt [cols][P(rows)] with scale_t
+ * (an array and its scales: both or neither).  block_rows 1: a scale for
+ * each 128 values of a row of the array written,
+ *   scale [rows][P(cols) / 128],  scale_t [cols][P(rows) / 128]
+ * (activations and gradients; the transposed copy has blocks and values of
+ * its own, since they run along x's columns).  block_rows 128: a scale for
+ * each square of 128 x 128,
+ *   scale [P(rows) / 128][P(cols) / 128],  scale_t its transpose
+ * (weights; the transposed copy holds the same values).
+ * The outputs must not overlap x or each other.
+ */
+msr_status msr_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block_rows, const void *x, void *q,
+                        float *scale, void *qt, float *scale_t, void *hip_stream);
+
+/*
+ * out [m][n] = A B^T of 8-bit A [m][k] and B [n][k] with their blocks'
+ * scales, k a multiple of 128 (the padded width): a linear layer with the
+ * weight layout of msr_qkv_projection.
+ *   a_scale [m][k / 128];  b_scale [n][k / 128] when b_block_rows is 1,
+ *   [P(n) / 128][k / 128] when it is 128;
+ *   out of type out_dtype.
+ * Sums over the blocks are fp32.  Within a block, an MSR_F32 output keeps
+ * fp32's accuracy (the values are widened to bf16, which is exact, for the
+ * matrix cores); an MSR_BF16 output uses the 8-bit matrix instruction, which
+ * adds groups of 8 products aligned to the largest of them and drops their
+ * bits below 2^-13 of it.  The product of two scales is formed in fp32.
+ * The gradients of y = x w^T are products of the same kind:
+ *   dx = dy w    A = dy by rows, B = the weight's transposed copy
+ *   dw = dy^T x  A, B = the transposed copies of dy and x, b_block_rows 1
+ * m or n of 0 launches nothing, k of 0 writes zeros.  Needs a workspace of
+ * msr_scaled_matmul_workspace(m, n, k, out_dtype) bytes (0 for most sizes).
+ * out must not overlap an input.
+ */
+msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, const float *a_scale, const void *b,
+                             const float *b_scale, int32_t b_block_rows, int32_t out_dtype, void *out, void *ws,
+                             size_t ws_bytes, void *hip_stream);
+size_t msr_scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, int32_t out_dtype);
 
 #ifdef __cplusplus
 }

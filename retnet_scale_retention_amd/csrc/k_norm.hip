@@ -1,0 +1,280 @@
+// k_norm.hip -- the residual's addition with a root-mean-square norm, its
+// output in the input's type and / or in 8 bits with scales, and the
+// gradients.  Per row of d values:
+//   h = x + r,  rstd = 1 / sqrt(mean(h^2) + eps),  n = h rstd w
+//   g = w dn,   dx = rstd (g - h rstd^2 mean(g h)) + dh,  dw = sum_rows dn h rstd
+// Everything is fp32 between the loads and the stores; n is taken from the
+// unrounded h, so the stored sum's rounding does not reach it.
+//
+// A row is held in registers by W waves, V groups of 8 elements per lane:
+// group v of lane l of wave w starts at element 8 (64 (v W + w) + l), so a
+// wave reads contiguous kilobytes and a block of 128 is one row of 16 lanes
+// (its largest magnitude needs four lane-row rotations, no LDS).
+#include "msr_quant.hpp"
+
+namespace {
+
+using namespace msr;
+
+struct NormArgs {
+    const void *x, *r, *w;  // r, w may be NULL
+    void *sum, *y;          // may be NULL
+    uint8_t *q;             // may be NULL; [rows][dpad]
+    float *qs;              // [rows][dpad / 128]
+    int64_t rows;
+    int d, dpad, w_bf16;
+    float eps;
+};
+
+// the sum over the W waves that share a row (team `tm` of the workgroup)
+template <int W>
+__device__ __forceinline__ float team_sum(float x, float *red, int tm, int w) {
+    x = wave_sum(x);
+    if constexpr (W > 1) {
+        if ((threadIdx.x & 63) == 0) red[tm * W + w] = x;
+        __syncthreads();
+        x = 0.f;
+#pragma unroll
+        for (int i = 0; i < W; ++i) x += red[tm * W + i];
+    }
+    return x;
+}
+
+template <typename T, bool VEC, int W, int V>
+__global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormArgs a) {
+    constexpr int TEAMS = W < 4 ? 4 / W : 1;
+    __shared__ float red[TEAMS * W];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tm = wave / W, w = wave % W;
+    const int64_t row_raw = (int64_t)blockIdx.x * TEAMS + tm;
+    const bool live = row_raw < a.rows;
+    const int64_t row = live ? row_raw : a.rows - 1;  // a team past the end repeats the last row and stores nothing
+    const T *x = static_cast<const T *>(a.x) + row * a.d;
+    const T *r = a.r ? static_cast<const T *>(a.r) + row * a.d : nullptr;
+    float h[V][8];
+    float ss = 0.f;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 8 * (64 * (v * W + w) + lane);
+        load8<VEC>(x + e, a.d - e, h[v]);
+    }
+    if (r) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 8 * (64 * (v * W + w) + lane);
+            float t[8];
+            load8<VEC>(r + e, a.d - e, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[v][i] += t[i];
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(h[v][i], h[v][i], ss);
+    if (a.sum && live) {
+        T *s = static_cast<T *>(a.sum) + row * a.d;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 8 * (64 * (v * W + w) + lane);
+            store8<VEC>(s + e, a.d - e, h[v]);
+        }
+    }
+    const float rstd = 1.f / sqrtf(team_sum<W>(ss, red, tm, w) / (float)a.d + a.eps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = 8 * (64 * (v * W + w) + lane);
+        float g[8];
+        load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, g);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * rstd * g[i];
+        if (a.y && live) store8<VEC>(static_cast<T *>(a.y) + row * a.d + e, a.d - e, h[v]);
+        if (a.q) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, abs_bits(h[v][i]));
+            const float s = block_scale(row16_max(m)), inv = 1.f / s;
+            if (live && e < a.dpad) {
+                *reinterpret_cast<uint2 *>(a.q + row * a.dpad + e) = pack8(h[v], inv);
+                if ((lane & 15) == 0) a.qs[row * (a.dpad / kBlock) + e / kBlock] = s;
+            }
+        }
+    }
+}
+
+struct NormBackArgs {
+    const void *h, *w, *dy, *dsum;  // w, dsum may be NULL
+    void *dx;
+    float *part;                    // [gridDim.x * TEAMS][d], or NULL: no weight gradient
+    int64_t rows;
+    int d, w_bf16;
+    float eps;
+};
+
+// Each team walks over rows team, team + teams, ... and keeps the weight's
+// gradient over them in registers; the teams' sums go to `part` and are
+// added by column_sum_kernel in a fixed order (no atomics).
+template <typename T, bool VEC, int W, int V>
+__global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(NormBackArgs a) {
+    constexpr int TEAMS = W < 4 ? 4 / W : 1;
+    __shared__ float red[2][2 * TEAMS * W];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tm = wave / W, w = wave % W;
+    const int64_t team = (int64_t)blockIdx.x * TEAMS + tm, teams = (int64_t)gridDim.x * TEAMS;
+    const int64_t turns = (a.rows + teams - 1) / teams;  // the same for every team: the barriers match
+    float dw[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+    for (int64_t t = 0; t < turns; ++t) {
+        const int64_t row_raw = t * teams + team;
+        const bool live = row_raw < a.rows;
+        const int64_t row = live ? row_raw : a.rows - 1;
+        const T *hp = static_cast<const T *>(a.h) + row * a.d, *dyp = static_cast<const T *>(a.dy) + row * a.d;
+        float h[V][8], g[V][8];
+        float ss = 0.f, gh = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 8 * (64 * (v * W + w) + lane);
+            load8<VEC>(hp + e, a.d - e, h[v]);
+            load8<VEC>(dyp + e, a.d - e, g[v]);
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 8 * (64 * (v * W + w) + lane);
+            float wt[8];
+            load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                ss = fmaf(h[v][i], h[v][i], ss);
+                gh = fmaf(h[v][i], g[v][i] * wt[i], gh);
+            }
+        }
+        ss = wave_sum(ss);
+        gh = wave_sum(gh);
+        if constexpr (W > 1) {
+            float *rd = red[t & 1];  // two areas: one barrier per turn separates a turn's reads from its writes
+            if (lane == 0) {
+                rd[2 * (tm * W + w)] = ss;
+                rd[2 * (tm * W + w) + 1] = gh;
+            }
+            __syncthreads();
+            ss = gh = 0.f;
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                ss += rd[2 * (tm * W + i)];
+                gh += rd[2 * (tm * W + i) + 1];
+            }
+        }
+        const float rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
+        const float c = rstd * rstd * (gh / (float)a.d);
+        if (!live) continue;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 8 * (64 * (v * W + w) + lane);
+            float wt[8], ds[8];
+            load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt);
+            if (a.dsum) {
+                load8<VEC>(static_cast<const T *>(a.dsum) + row * a.d + e, a.d - e, ds);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ds[i] = 0.f;
+            }
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                o[i] = fmaf(rstd, g[v][i] * wt[i] - h[v][i] * c, ds[i]);
+                dw[v][i] = fmaf(g[v][i], h[v][i] * rstd, dw[v][i]);
+            }
+            store8<VEC>(static_cast<T *>(a.dx) + row * a.d + e, a.d - e, o);
+        }
+    }
+    if (a.part) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const int e = 8 * (64 * (v * W + w) + lane);
+            store8<VEC>(a.part + team * a.d + e, a.d - e, dw[v]);
+        }
+    }
+}
+
+// out[c] = sum_p part[p][c], p in order within each of 64 slices, the slices in order
+__global__ __launch_bounds__(256) void column_sum_kernel(const float *part, float *out, int parts, int d) {
+    __shared__ float red[64][17];
+    const int c = (int)blockIdx.x * 16 + 4 * (threadIdx.x & 3), sl = threadIdx.x >> 2;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int p = sl; p < parts; p += 64)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (c + i < d) s[i] += part[(size_t)p * d + c + i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[sl][4 * (threadIdx.x & 3) + i] = s[i];
+    __syncthreads();
+    if (threadIdx.x < 16) {
+        float t = 0.f;
+        for (int i = 0; i < 64; ++i) t += red[i][threadIdx.x];
+        const int o = (int)blockIdx.x * 16 + threadIdx.x;
+        if (o < d) out[o] = t;
+    }
+}
+
+template <typename F>
+hipError_t by_width(int d, F f) {
+    // (waves, groups per lane) that hold a row of d <= 512 W V values
+    if (d <= 512) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    if (d <= 1024) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 2>());
+    if (d <= 2048) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
+    if (d <= 4096) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
+    if (d <= 8192) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
+    if (d <= 16384) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
+    return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+}
+
+template <typename F>
+hipError_t by_type(int dtype, bool vec, F f) {
+    if (dtype == MSR_BF16) return vec ? f(uint16_t(), std::true_type()) : f(uint16_t(), std::false_type());
+    return vec ? f(float(), std::true_type()) : f(float(), std::false_type());
+}
+
+constexpr int kBackGroups = 512;  // workgroups of the backward pass at most
+
+int back_teams(int64_t rows, int d) {
+    const int per = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
+    const int64_t g = (rows + per - 1) / per;
+    return (int)(g < kBackGroups ? g : kBackGroups) * per;
+}
+
+}  // namespace
+
+hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, const void *r, const void *w, int w_dtype,
+                              float eps, void *sum, void *y, void *q, float *qs, hipStream_t st) {
+    const NormArgs a{x, r, w, sum, y, static_cast<uint8_t *>(q), qs, rows, d, (int)round128(d), w_dtype == MSR_BF16, eps};
+    return by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
+        return by_width(d, [&](auto W, auto V) {
+            constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
+            hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(t), vec.value, W.value, V.value>),
+                               dim3((unsigned)((rows + teams - 1) / teams)), dim3(nt), 0, st, a);
+            return hipGetLastError();
+        });
+    });
+}
+
+size_t rmsnorm_backward_workspace(int64_t rows, int d) { return (size_t)back_teams(rows, d) * d * sizeof(float); }
+
+hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h, const void *w, int w_dtype, float eps,
+                                   const void *dy, const void *dsum, void *dx, float *dw, float *part, hipStream_t st) {
+    const int parts = back_teams(rows, d);
+    const NormBackArgs a{h, w, dy, dsum, dx, dw ? part : nullptr, rows, d, w_dtype == MSR_BF16, eps};
+    hipError_t e = parts == 0 ? hipSuccess : by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
+        return by_width(d, [&](auto W, auto V) {
+            constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
+            hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), vec.value, W.value, V.value>), dim3(parts / teams),
+                               dim3(nt), 0, st, a);
+            return hipGetLastError();
+        });
+    });
+    if (e == hipSuccess && dw) {
+        hipLaunchKernelGGL(column_sum_kernel, dim3((d + 15) / 16), dim3(256), 0, st, part, dw, parts, d);
+        e = hipGetLastError();
+    }
+    return e;
+}

@@ -1,0 +1,159 @@
+// k_quant.hip -- a matrix into 8 bits (e4m3) with one scale per block of
+// 128, in its own order, transposed, or both from one pass over it.  A block
+// is 128 values of a row (of a column for the transposed copy), or a square
+// of 128 x 128, in which case the transposed copy has the same scales and
+// bytes.  Scales, rounding and non-finite values: msr_quant.hpp.
+#include "msr_quant.hpp"
+
+namespace {
+
+using namespace msr;
+
+struct QuantArgs {
+    const void *x;
+    uint8_t *q, *qt;      // NULL: not wanted.  [R][Cp] and [C][Rp]
+    float *s, *st;
+    int64_t R, C, Cp, Rp;
+    int tiles_c;
+};
+
+// Own order, blocks within a row: 16 lanes take a block, 8 values each.
+template <typename T, bool VEC>
+__global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
+    const int64_t blocks = a.R * (a.Cp / kBlock), per = (int64_t)gridDim.x * 16;
+    for (int64_t b0 = (int64_t)blockIdx.x * 16; b0 < blocks; b0 += per) {
+        const int64_t b_raw = b0 + (threadIdx.x >> 4), b = b_raw < blocks ? b_raw : blocks - 1;
+        const int64_t row = b / (a.Cp / kBlock), c = (b % (a.Cp / kBlock)) * kBlock + 8 * (threadIdx.x & 15);
+        float v[8];
+        load8<VEC>(static_cast<const T *>(a.x) + row * a.C + c, (int)(a.C - c), v);
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
+        const float sc = block_scale(row16_max(m));
+        if (b_raw < blocks) {
+            *reinterpret_cast<uint2 *>(a.q + row * a.Cp + c) = pack8(v, 1.f / sc);
+            if ((threadIdx.x & 15) == 0) a.s[b] = sc;
+        }
+    }
+}
+
+// A workgroup takes a 128 x 128 tile: thread t holds the 8 x 8 values of rows
+// 8 (t / 16) .., columns 8 (t % 16) .. in registers, so both directions'
+// packs are register work; the transposed bytes pass through LDS to leave in
+// whole 128-byte rows.
+template <typename T, bool VEC, bool SQUARE>
+__global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
+    constexpr int LDT = 144;  // bytes between the rows of the transposed tile: 16-byte aligned, off the banks' period
+    __shared__ uint32_t cmax[4][128];
+    __shared__ uint32_t tmax[4];
+    __shared__ __attribute__((aligned(16))) uint8_t tr[128 * LDT];
+    const int64_t tr_i = blockIdx.x / a.tiles_c, tc = blockIdx.x % a.tiles_c;
+    const int64_t r0 = tr_i * 128, c0 = tc * 128;
+    const int rg = threadIdx.x >> 4, cg = threadIdx.x & 15, wave = threadIdx.x >> 6;
+    const int64_t c = c0 + 8 * cg;
+    float v[8][8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + 8 * rg + i;
+        load8<VEC>(static_cast<const T *>(a.x) + r * a.C + c, r < a.R ? (int)(a.C - c) : 0, v[i]);
+    }
+    uint32_t rm[8], cm[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) rm[i] = cm[i] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t m = abs_bits(v[i][j]);
+            rm[i] = max(rm[i], m);
+            cm[j] = max(cm[j], m);
+        }
+    float rs[8], cs[8];
+    if constexpr (SQUARE) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max(m, rm[i]);
+        m = row16_max(m);
+        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+        if ((threadIdx.x & 63) == 0) tmax[wave] = m;
+        __syncthreads();
+        const float s = block_scale(max(max(tmax[0], tmax[1]), max(tmax[2], tmax[3])));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rs[i] = cs[i] = s;
+        if (threadIdx.x == 0) {
+            if (a.q) a.s[tr_i * (a.Cp / kBlock) + tc] = s;
+            if (a.qt) a.st[tc * (a.Rp / kBlock) + tr_i] = s;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rs[i] = block_scale(row16_max(rm[i]));
+        if (a.qt) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                uint32_t m = cm[j];
+                m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+                m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+                if ((threadIdx.x & 48) == 0) cmax[wave][8 * cg + j] = m;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = 8 * cg + j;
+                cs[j] = block_scale(max(max(cmax[0][k], cmax[1][k]), max(cmax[2][k], cmax[3][k])));
+                if (rg == 0 && c + j < a.C) a.st[(c + j) * (a.Rp / kBlock) + tr_i] = cs[j];
+            }
+        }
+    }
+    if (a.q) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + 8 * rg + i;
+            if (r < a.R) {
+                *reinterpret_cast<uint2 *>(a.q + r * a.Cp + c) = pack8(v[i], 1.f / rs[i]);
+                if (!SQUARE && cg == 0) a.s[r * (a.Cp / kBlock) + tc] = rs[i];
+            }
+        }
+    }
+    if (a.qt) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float col[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
+            *reinterpret_cast<uint2 *>(tr + (8 * cg + j) * LDT + 8 * rg) = pack8(col, 1.f / cs[j]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int k = 32 * i + (int)(threadIdx.x >> 3), b = 16 * (threadIdx.x & 7);
+            if (c0 + k < a.C)
+                *reinterpret_cast<uint4 *>(a.qt + (c0 + k) * a.Rp + r0 + b) =
+                    *reinterpret_cast<const uint4 *>(tr + k * LDT + b);
+        }
+    }
+}
+
+template <typename T, bool VEC>
+hipError_t quantize(const QuantArgs &a, int block_rows, hipStream_t st) {
+    if (block_rows == 1 && !a.qt) {
+        const int64_t g = (a.R * (a.Cp / kBlock) + 15) / 16;
+        hipLaunchKernelGGL((quantize_rows_kernel<T, VEC>), dim3((unsigned)(g < 16384 ? g : 16384)), dim3(256), 0, st, a);
+    } else {
+        const unsigned tiles = (unsigned)(a.Rp / 128 * a.tiles_c);
+        if (block_rows == 1)
+            hipLaunchKernelGGL((quantize_tile_kernel<T, VEC, false>), dim3(tiles), dim3(256), 0, st, a);
+        else
+            hipLaunchKernelGGL((quantize_tile_kernel<T, VEC, true>), dim3(tiles), dim3(256), 0, st, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize(int64_t R, int64_t C, int dtype, int block_rows, const void *x, void *q, float *s, void *qt,
+                           float *s_t, hipStream_t st) {
+    const QuantArgs a{x, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt), s, s_t, R, C, round128(C), round128(R),
+                      (int)(round128(C) / 128)};
+    if (dtype == MSR_BF16)
+        return C % 8 == 0 ? quantize<uint16_t, true>(a, block_rows, st) : quantize<uint16_t, false>(a, block_rows, st);
+    return C % 8 == 0 ? quantize<float, true>(a, block_rows, st) : quantize<float, false>(a, block_rows, st);
+}

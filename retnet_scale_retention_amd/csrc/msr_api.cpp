@@ -516,6 +516,14 @@ void main_kernel_end(hipStream_t st) {
     if (g_ev_stop) (void)hipEventRecord(g_ev_stop, st);
 }
 
+msr_status set_error(msr_status s, const char *fmt, ...) {
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(g_err, sizeof(g_err), fmt, ap);
+    va_end(ap);
+    return s;
+}
+
 int exchange_mode() { return g_exchange.load(std::memory_order_relaxed); }
 
 hipEvent_t main_event_start() { return g_ev_start; }

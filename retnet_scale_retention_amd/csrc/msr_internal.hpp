@@ -89,6 +89,23 @@ hipError_t launch_accumulate(size_t n, const void *x, int in_dtype, float *y, in
 hipError_t launch_state_op(const MsrConst &c, int d1, int d2, const float *in, float *out, int transpose,
                            float power, int j0, int nj, hipStream_t st);
 
+// ---- the layer around retention (k_norm.hip, k_quant.hip, k_matmul.hip) ----
+// Sizes, alignment and aliasing are checked by msr_layer.cpp; r, w, sum, y,
+// dsum and dw may be NULL, q with qs and qt with s_t too.
+hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, const void *r, const void *w, int w_dtype,
+                              float eps, void *sum, void *y, void *q, float *qs, hipStream_t st);
+size_t rmsnorm_backward_workspace(int64_t rows, int d);
+hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h, const void *w, int w_dtype, float eps,
+                                   const void *dy, const void *dsum, void *dx, float *dw, float *part, hipStream_t st);
+hipError_t launch_quantize(int64_t R, int64_t C, int dtype, int block_rows, const void *x, void *q, float *s, void *qt,
+                           float *s_t, hipStream_t st);
+size_t scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, int out_dtype);
+hipError_t launch_scaled_matmul(int m, int n, int k, const void *A, const float *sa, const void *B, const float *sb,
+                                int b_rows, int out_dtype, void *out, void *ws, hipStream_t st);
+
+// Sets this thread's msr_last_error text and returns s.
+msr_status set_error(msr_status s, const char *fmt, ...);
+
 // The fixed scratch array of msr_chunkwise_noalloc (k_static.hip): this
 // device's copy, looked up once per device.
 constexpr size_t MSR_STATIC_SCRATCH_BYTES = MSR_NOALLOC_SCRATCH_BYTES;

@@ -1,0 +1,145 @@
+// msr_quant.hpp -- device helpers of the 8-bit operators: e4m3 values with
+// one fp32 scale for each block of 128, vector loads and stores of eight
+// elements, and reductions over a row of 16 lanes.
+//
+// A block's scale is s = max(amax / 448, 2^-126) (448 is e4m3's largest
+// value; the floor keeps 1 / s finite) and its values are rne(v * (1 / s)).
+// amax is taken on the bit patterns of |v|, which order as the numbers do,
+// with infinity above every number and NaN above infinity: a block that
+// holds one gets an infinite or NaN scale, and stands for NaN as a whole.
+#pragma once
+
+#include "msr_device.hpp"
+
+namespace msr {
+
+constexpr int kBlock = 128;
+constexpr float kF8Max = 448.f;
+constexpr float kScaleFloor = 1.17549435e-38f;  // 2^-126
+
+__host__ __device__ constexpr int64_t round128(int64_t n) { return (n + 127) / 128 * 128; }
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+__device__ __forceinline__ float block_scale(uint32_t amax_bits) {
+    const float s = __uint_as_float(amax_bits) / kF8Max;
+    return s < kScaleFloor ? kScaleFloor : s;
+}
+
+// eight values times inv as e4m3 bytes, in order (round to nearest even)
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], float inv) {
+    int a = 0, b = 0;
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, a, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, a, true);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, b, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, b, true);
+    return make_uint2((uint32_t)a, (uint32_t)b);
+}
+
+// lane l of a row of 16 reads lane (l + N) % 16 of it
+template <int N>
+__device__ __forceinline__ uint32_t row_ror(uint32_t x) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 | N, 0xf, 0xf, true);
+}
+
+__device__ __forceinline__ uint32_t row16_max(uint32_t x) {
+    x = max(x, row_ror<8>(x));
+    x = max(x, row_ror<4>(x));
+    x = max(x, row_ror<2>(x));
+    return max(x, row_ror<1>(x));
+}
+
+__device__ __forceinline__ float row16_sum(float x) {
+    x += __uint_as_float(row_ror<8>(__float_as_uint(x)));
+    x += __uint_as_float(row_ror<4>(__float_as_uint(x)));
+    x += __uint_as_float(row_ror<2>(__float_as_uint(x)));
+    return x + __uint_as_float(row_ror<1>(__float_as_uint(x)));
+}
+
+// Eight consecutive elements at p (16-byte aligned when VEC): elements from
+// index `left` on lie past the row's end, are not read and count as zero.
+template <bool VEC>
+__device__ __forceinline__ void load8(const uint16_t *p, int left, float (&v)[8]) {
+    if constexpr (VEC) {
+        if (left > 0) {
+            const uint4 u = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? bf16_to_f32(p[i]) : 0.f;
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const float *p, int left, float (&v)[8]) {
+    if constexpr (VEC) {
+        if (left > 0) {
+            const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.f;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.f;
+    }
+}
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const bf16x2_t p = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
+    return __builtin_bit_cast(uint32_t, p);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(uint16_t *p, int left, const float (&v)[8]) {
+    if constexpr (VEC) {
+        if (left > 0)
+            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
+                                                       pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = f32_to_bf16(v[i]);
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(float *p, int left, const float (&v)[8]) {
+    if constexpr (VEC) {
+        if (left > 0) {
+            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) p[i] = v[i];
+    }
+}
+
+// the same for a weight row whose type is known at run time only (NULL: ones)
+template <bool VEC>
+__device__ __forceinline__ void load_weight8(const void *w, int bf16, size_t i, int left, float (&v)[8]) {
+    if (!w) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = 1.f;
+    } else if (bf16) {
+        load8<VEC>(static_cast<const uint16_t *>(w) + i, left, v);
+    } else {
+        load8<VEC>(static_cast<const float *>(w) + i, left, v);
+    }
+}
+
+}  // namespace msr

@@ -8,6 +8,7 @@ fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 from pathlib import Path
 
 import numpy as np
@@ -26,7 +27,9 @@ STATUS = {0: "MSR_OK", -1: "MSR_ERR_INVALID_ARG", -2: "MSR_ERR_SHAPE", -3: "MSR_
 
 EXPORTS = ("msr_abi_version", "msr_last_error", "msr_workspace_size", "msr_workspace_bytes", "msr_parallel",
            "msr_chunkwise", "msr_chunkwise_noalloc", "msr_chunkwise_backward", "msr_qkv_projection", "msr_qkv_chunkwise",
-           "msr_recurrent_step", "msr_set_kernel_events", "msr_set_exchange")
+           "msr_recurrent_step", "msr_set_kernel_events", "msr_set_exchange",
+           "msr_add_rmsnorm", "msr_add_rmsnorm_backward", "msr_add_rmsnorm_backward_workspace", "msr_quantize",
+           "msr_scaled_matmul", "msr_scaled_matmul_workspace")
 
 
 class MsrError(RuntimeError):
@@ -85,6 +88,17 @@ def load():
     lib.msr_set_kernel_events.argtypes = [vp, vp]
     lib.msr_set_kernel_events.restype = None
     lib.msr_set_exchange.argtypes, lib.msr_set_exchange.restype = [ctypes.c_int32], ctypes.c_int
+    i32, i64, sz, f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
+    lib.msr_add_rmsnorm.argtypes = [i64, i32, i32, vp, vp, vp, i32, f32, vp, vp, vp, vp, vp]
+    lib.msr_add_rmsnorm.restype = ctypes.c_int
+    lib.msr_add_rmsnorm_backward.argtypes = [i64, i32, i32, vp, vp, i32, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.msr_add_rmsnorm_backward.restype = ctypes.c_int
+    lib.msr_add_rmsnorm_backward_workspace.argtypes, lib.msr_add_rmsnorm_backward_workspace.restype = [i64, i32], sz
+    lib.msr_quantize.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]
+    lib.msr_quantize.restype = ctypes.c_int
+    lib.msr_scaled_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp, sz, vp]
+    lib.msr_scaled_matmul.restype = ctypes.c_int
+    lib.msr_scaled_matmul_workspace.argtypes, lib.msr_scaled_matmul_workspace.restype = [i64, i64, i64, i32], sz
     del fp
     _lib = lib
     return lib
@@ -343,6 +357,162 @@ def msr_recurrent_step(q, k, v, state, gamma, pos, *, theta=None, scale=0.0, eps
         out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
     _check(load().msr_recurrent_step(d.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state),
                                      _stream(q, stream)))
+    return out
+
+
+# ------------------------------------------------- the layer around retention
+BLOCK = 128  # MSR_BLOCK
+
+
+def _padded(n: int) -> int:
+    return (n + BLOCK - 1) // BLOCK * BLOCK
+
+
+def _expect(name, t, shape, dtype, device):
+    """t, checked to be a contiguous tensor of this shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
+    return t
+
+
+def _like(name, t, shape, dtype, device):
+    """A new tensor of this shape, type and device, or t after the same checks."""
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=device)
+    return _expect(name, t, shape, dtype, device)
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(device, stream):
+    return (_torch().cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _matrix(name, x):
+    """(rows, d) of a contiguous device tensor [..., d]."""
+    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    *lead, d = x.shape
+    return math.prod(lead), d
+
+
+def _weight(weight, d, device):
+    if weight is None:
+        return None, MSR_F32
+    if weight.shape != (d,) or weight.device != device or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous [{d}] tensor on {device}")
+    return weight.data_ptr(), _dtype_code(weight)
+
+
+def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, want_q=False, out=None, stream=None):
+    """h = x + residual and its root-mean-square norm n = h / sqrt(mean(h^2) + eps) * weight over the last dimension.
+    x, residual: [..., d] float32 or bfloat16; weight: [d] of either type.  Returns (y, sum, q, scale), None where
+    not computed: y = n in x's type (want_y); sum = h in x's type (when a residual is given); q, scale (want_q) = n as
+    float8_e4m3fn [..., P(d)] (P: the next multiple of 128, zeros there) with a float32 scale per 128 values,
+    [..., P(d) / 128].  out: tensors to write, in the same order (sum may be x or residual, y may be x)."""
+    torch = _torch()
+    rows, d = _matrix("x", x)
+    code, dev = _dtype_code(x), x.device
+    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.device != dev
+                                 or not residual.is_contiguous()):
+        raise ValueError("residual must be a contiguous tensor of x's shape, type and device")
+    wp, wcode = _weight(weight, d, dev)
+    y, total, q, scale = (None, None, None, None) if out is None else out
+    lead, dp = x.shape[:-1], _padded(d)
+    y = _like("y", y, x.shape, x.dtype, dev) if want_y else None
+    total = _like("sum", total, x.shape, x.dtype, dev) if residual is not None else None
+    if want_q:
+        q = _like("q", q, (*lead, dp), torch.float8_e4m3fn, dev)
+        scale = _like("scale", scale, (*lead, dp // BLOCK), torch.float32, dev)
+    else:
+        q = scale = None
+    _check(load().msr_add_rmsnorm(rows, d, code, x.data_ptr(), _address(residual), wp, wcode, eps, _address(total),
+                                  _address(y), _address(q), _address(scale), _raw_stream(dev, stream)))
+    return y, total, q, scale
+
+
+def msr_add_rmsnorm_backward(h, weight, grad_y, *, grad_sum=None, eps=1e-6, want_weight_grad=True, out=None,
+                             workspace=None, stream=None):
+    """Gradients of msr_add_rmsnorm: h = the forward call's sum (x when it had no residual), grad_y = dL/dn, grad_sum =
+    dL/dsum or None, all [..., d] of one type.  Returns (dx, dweight or None): dx is the gradient of x and of the
+    residual, in h's type; dweight is float32 [d].  out: tensors to write, in the same order."""
+    torch = _torch()
+    rows, d = _matrix("h", h)
+    code, dev = _dtype_code(h), h.device
+    for name, t in (("grad_y", grad_y), ("grad_sum", grad_sum)):
+        if t is None and name == "grad_sum":
+            continue
+        if t.shape != h.shape or t.dtype != h.dtype or t.device != dev or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous tensor of h's shape, type and device")
+    wp, wcode = _weight(weight, d, dev)
+    dx, dw = (None, None) if out is None else out
+    dx = _like("dx", dx, h.shape, h.dtype, dev)
+    dw = _like("dweight", dw, (d,), torch.float32, dev) if want_weight_grad else None
+    lib, n = load(), 0
+    if want_weight_grad:
+        n = lib.msr_add_rmsnorm_backward_workspace(rows, d)
+        if n and (workspace is None or workspace.numel() < n):
+            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    _check(lib.msr_add_rmsnorm_backward(rows, d, code, h.data_ptr(), wp, wcode, eps, grad_y.data_ptr(),
+                                        _address(grad_sum), dx.data_ptr(), _address(dw),
+                                        _address(workspace) if n else None, n, _raw_stream(dev, stream)))
+    return dx, dw
+
+
+def msr_quantize(x, *, block_rows=1, want_rows=True, want_transposed=False, out=None, stream=None):
+    """x [rows, cols] (float32 or bfloat16) in 8 bits: (q, scale, qt, scale_t), None where not wanted.  q:
+    float8_e4m3fn [rows, P(cols)] (P: the next multiple of 128, zeros there), qt [cols, P(rows)] its transposed
+    counterpart.  block_rows 1: a float32 scale per 128 values of a row of the array written, scale [rows, P(cols) /
+    128], scale_t [cols, P(rows) / 128]; block_rows 128: a scale per 128 x 128 square, [P(rows) / 128, P(cols) / 128]
+    and its transpose.  out: tensors to write, in the same order."""
+    torch = _torch()
+    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
+        raise ValueError("x must be a contiguous device matrix")
+    R, C = x.shape
+    code, dev, square = _dtype_code(x), x.device, block_rows == BLOCK
+    q, s, qt, st = (None, None, None, None) if out is None else out
+    f8, f32, rp, cp = torch.float8_e4m3fn, torch.float32, _padded(R), _padded(C)
+    if want_rows:
+        q = _like("q", q, (R, cp), f8, dev)
+        s = _like("scale", s, (rp // BLOCK if square else R, cp // BLOCK), f32, dev)
+    else:
+        q = s = None
+    if want_transposed:
+        qt = _like("qt", qt, (C, rp), f8, dev)
+        st = _like("scale_t", st, (cp // BLOCK if square else C, rp // BLOCK), f32, dev)
+    else:
+        qt = st = None
+    _check(load().msr_quantize(R, C, code, block_rows, x.data_ptr(), _address(q), _address(s), _address(qt),
+                               _address(st), _raw_stream(dev, stream)))
+    return q, s, qt, st
+
+
+def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, workspace=None, stream=None):
+    """a b^T of 8-bit operands with a scale for each block of 128: a [..., K] float8_e4m3fn with a_scale [..., K /
+    128], b [N, K] with b_scale [N, K / 128] or, per 128 x 128 square, [P(N) / 128, K / 128] (float32; K a multiple
+    of 128).  Returns [..., N] of out_dtype: bfloat16 (default) or float32."""
+    torch = _torch()
+    m, k = _matrix("a", a)
+    if b.dim() != 2 or not b.is_contiguous() or b.device != a.device or b.shape[1] != k:
+        raise ValueError(f"b must be a contiguous [N, {k}] tensor on {a.device}")
+    if a.dtype != torch.float8_e4m3fn or b.dtype != torch.float8_e4m3fn:
+        raise TypeError("a and b must be float8_e4m3fn")
+    n, dev, kb = b.shape[0], a.device, k // BLOCK
+    _expect("a_scale", a_scale, (*a.shape[:-1], kb), torch.float32, dev)
+    rows = 1 if b_scale.shape[:1] == (n,) else BLOCK
+    _expect("b_scale", b_scale, (n if rows == 1 else _padded(n) // BLOCK, kb), torch.float32, dev)
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if out is None else out.dtype
+    out = _like("out", out, (*a.shape[:-1], n), out_dtype, dev)
+    code, lib = _dtype_code(out), load()
+    ws = lib.msr_scaled_matmul_workspace(m, n, k, code)
+    if ws and (workspace is None or workspace.numel() < ws):
+        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
+    _check(lib.msr_scaled_matmul(m, n, k, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), rows,
+                                 code, out.data_ptr(), _address(workspace) if ws else None, ws,
+                                 _raw_stream(dev, stream)))
     return out
 
 
