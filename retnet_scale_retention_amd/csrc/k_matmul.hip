@@ -36,6 +36,35 @@ struct MatArgs {
 
 constexpr int kUnitScale = 0x7f7f7f7f;  // the instruction's own block scales, all 2^0
 
+typedef __attribute__((address_space(3))) void lds_void;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), (short)0, (int)bytes, 0x00020000);
+}
+
+// 16 (or 4) bytes per lane from a buffer straight into LDS, lane l's at dst + 16 l (4 l; dst wave-uniform); past the
+// buffer's end zeros arrive
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, char *dst, int lane_off, int off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 16, lane_off, off, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, char *dst, int lane_off, int off) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void *)dst, 4, lane_off, off, 0, 0);
+}
+
+// vmcnt(N) and lgkmcnt(0), then a barrier
+template <int N>
+__device__ __forceinline__ void wait_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// a number that is the same for the whole wave, through the scalar cache
+__device__ __forceinline__ float uniform_load(const float *p) {
+    return *(const __attribute__((address_space(4))) float *)p;
+}
+
 struct Frag {  // 32 contraction bytes of one row per lane: a 16-row operand of one block
     i32x4 lo, hi;
 };
@@ -70,9 +99,37 @@ __device__ __forceinline__ f32x4 block_product(const WideFrag &x, const WideFrag
     return c;
 }
 
-__device__ __forceinline__ void load_lds16(const void *gptr, void *lds) {
-    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)gptr,
-                                     (__attribute__((address_space(3))) void *)lds, 16, 0, 0);
+template <typename OUT>
+using OperandOf = std::conditional_t<sizeof(OUT) == 4, WideFrag, Frag>;
+
+template <typename OUT>
+__device__ __forceinline__ OperandOf<OUT> operand(const Frag &f) {
+    if constexpr (sizeof(OUT) == 4) return widen(f);
+    else return f;
+}
+
+// Rows of a block in LDS are 128 bytes, their 16-byte chunks XOR-swizzled by
+// half the row number.  Lane (l16, g) of a 16-row operand takes chunks g and
+// g + 4 of row l16 (any split of the 128 will do that both operands share):
+// each quarter of the lanes that LDS serves together then touches all 64
+// banks once (no conflicts measured; keyed by the row number itself, half
+// the cycles were conflicts).
+struct LaneRow {
+    int lo, hi;
+    __device__ __forceinline__ explicit LaneRow(int lane) {
+        const int l16 = lane & 15, g = lane >> 4, key = l16 >> 1;
+        lo = l16 * 128 + ((g ^ key) << 4);
+        hi = l16 * 128 + (((g + 4) ^ key) << 4);
+    }
+    __device__ __forceinline__ Frag load(const char *rows) const {
+        return {*reinterpret_cast<const i32x4 *>(rows + lo), *reinterpret_cast<const i32x4 *>(rows + hi)};
+    }
+};
+
+// Where lane l of a 1 KiB load of rows 8 q .. 8 q + 7 (128 bytes each, K
+// apart) finds the bytes that the swizzle puts at its place.
+__device__ __forceinline__ int swizzled_source(int lane, int q, int K) {
+    return (lane >> 3) * K + 16 * ((lane & 7) ^ ((4 * (q & 1) + (lane >> 4)) & 7));
 }
 
 // Four consecutive output features of one token (n < N for the first).
@@ -90,54 +147,69 @@ __device__ __forceinline__ void store_row4(OUT *row, int n, int N, f32x4 v) {
     }
 }
 
-// A workgroup of WM x WN waves computes a tile of BM tokens by BN features.
+// Tile id -> (row tile, column tile).  Ids are dealt round-robin over the 8
+// XCDs; each takes a contiguous range of an order in which groups of 8 row
+// tiles sweep the column tiles, so what runs together on an XCD shares rows
+// of A and B in its L2.
+__device__ __forceinline__ bool tile_of(int block, int mt, int nt, int &tm, int &tn) {
+    const int total = mt * nt, per = (total + 7) / 8, id = block % 8 * per + block / 8;
+    if (block / 8 >= per || id >= total) return false;
+    const int grp = id / (8 * nt), in = id % (8 * nt), gm = min(8, mt - grp * 8);
+    tm = grp * 8 + in % gm;
+    tn = in / gm;
+    return true;
+}
+
+// A tile of BM tokens by BN features per workgroup of KG x WM x WN waves; the
+// KG groups share out the contraction's blocks and add up in LDS at the end.
 // B's rows are the instruction's first operand: lane (l16, g) of a 16 x 16
 // result holds token l16 and features 4 g .. 4 g + 3, so A's scale is one
 // number per lane and the four results are neighbours in the output row.
-// Each block's bytes go straight into LDS (direct 16-byte loads, one block
-// ahead into the other of two buffers); rows are 128 bytes, their 16-byte
-// chunks XOR-swizzled by row through the choice of each lane's source chunk.
-template <int BM, int BN, int WM, int WN, typename OUT, bool BROW>
-__global__ __launch_bounds__(64 * WM * WN) void matmul_tile_kernel(MatArgs a) {
+// Blocks go straight into a ring of ST LDS stages (16-byte direct loads),
+// ST - 1 blocks ahead, with one barrier per block.  The stages are separate
+// arrays: the compiler then knows that reads of one do not wait for the loads
+// into the others (in one array it drained every load before each block's
+// first read: 787 us against 645 for 16384 x 8192 x 4096).
+template <int BM, int BN, int KG, int WM, int WN, int ST, typename OUT, bool BROW>
+__device__ __forceinline__ void tile_body(const MatArgs &a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
-    constexpr bool WIDE = sizeof(OUT) == 4;
-    constexpr int LA = BM / 8 / NW, LB = BN / 8 / NW;  // 1 KiB loads per wave and block
-    __shared__ __attribute__((aligned(1024))) char As[2][BM * 128];
-    __shared__ __attribute__((aligned(1024))) char Bs[2][BN * 128];
+    constexpr int LA = BM / 8, L = (BM + BN) / 8 / NW;  // 1 KiB loads of a block's A, and of a wave
+    constexpr int SA = (BM + BN) * 128, SB = SA + (BM < 64 ? 64 : BM) * 4;
+    constexpr int STAGE = SB + (BROW ? (BN < 64 ? 64 : BN) * 4 : 0);
+    constexpr int NSA = (BM + 63) / 64, NS = NSA + (BROW ? (BN + 63) / 64 : 0);  // loads of 64 scales
+    static_assert((BM + BN) / 8 % NW == 0 && NS <= NW && ST >= 2 && ST <= 4, "");
+    __shared__ __attribute__((aligned(1024))) char S0[KG * STAGE];
+    __shared__ __attribute__((aligned(1024))) char S1[KG * STAGE];
+    __shared__ __attribute__((aligned(1024))) char S2[ST > 2 ? KG * STAGE : 16];
+    __shared__ __attribute__((aligned(1024))) char S3[ST > 3 ? KG * STAGE : 16];
 
-    const int total = a.mt * a.nt, per = (total + 7) / 8;
-    const int id = (int)(blockIdx.x % 8) * per + (int)(blockIdx.x / 8);
-    if ((int)(blockIdx.x / 8) >= per || id >= total) return;
-    const int grp = id / (8 * a.nt), in = id % (8 * a.nt), gm = min(8, a.mt - grp * 8);
-    const int m0 = (grp * 8 + in % gm) * BM, n0 = in / gm * BN;
+    int tm, tn;
+    if (!tile_of(blockIdx.x, a.mt, a.nt, tm, tn)) return;
+    const int m0 = tm * BM, n0 = tn * BN, K = a.K, nkb = a.nkb;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int kg = wave / NW, wv = wave % NW, l16 = lane & 15, g = lane >> 4;
+    const int ar = wv / WN * (BM / WM), br = wv % WN * (BN / WN);
+    const int steps = (nkb + KG - 1) / KG, k0 = kg * steps, k1 = min(k0 + steps, nkb);
 
-    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, g = lane >> 4, wm = wv / WN, wn = wv % WN;
-
-    const uint8_t *ag[LA], *bg[LB];
+    const auto ra = rsrc(a.a + (size_t)m0 * K, (uint32_t)(min(a.M - m0, BM) * K));
+    const auto rb = rsrc(a.b + (size_t)n0 * K, (uint32_t)(min(a.N - n0, BN) * K));
+    const int vo[2] = {swizzled_source(lane, wv * L, K), swizzled_source(lane, wv * L + 1, K)};
+    // every wave brings 64 scales (those past the last repeat the first), so that all wait for the same count
+    const int sw = wv < NS ? wv : 0, srow = sw < NSA ? 64 * sw : 64 * (sw - NSA);
+    const auto rs = sw < NSA ? rsrc(a.sa + (size_t)m0 * nkb, (uint32_t)(min(a.M - m0, BM) * nkb * 4))
+                             : rsrc(a.sb + (size_t)n0 * nkb, (uint32_t)(min(a.N - n0, BN) * nkb * 4));
+    const int so = (srow + lane) * nkb * 4, sdst = (sw < NSA ? SA : SB) + srow * 4;
+    auto issue = [&](int i, char *S) __attribute__((always_inline)) {
+        const int kb = min(k0 + i, nkb - 1);
 #pragma unroll
-    for (int i = 0; i < LA; ++i) {
-        const int r = 8 * (wv + NW * i) + (lane >> 3);
-        ag[i] = a.a + (size_t)min(m0 + r, a.M - 1) * a.K + 16 * ((lane & 7) ^ (r & 7));
-    }
-#pragma unroll
-    for (int i = 0; i < LB; ++i) {
-        const int r = 8 * (wv + NW * i) + (lane >> 3);
-        bg[i] = a.b + (size_t)min(n0 + r, a.N - 1) * a.K + 16 * ((lane & 7) ^ (r & 7));
-    }
-    auto issue = [&](int kb, int buf) {
-#pragma unroll
-        for (int i = 0; i < LA; ++i) load_lds16(ag[i] + (size_t)kb * 128, As[buf] + (wv + NW * i) * 1024);
-#pragma unroll
-        for (int i = 0; i < LB; ++i) load_lds16(bg[i] + (size_t)kb * 128, Bs[buf] + (wv + NW * i) * 1024);
+        for (int j = 0; j < L; ++j) {
+            const int q = wv * L + j;
+            load_lds16(q < LA ? ra : rb, S + kg * STAGE + q * 1024, vo[j & 1], (q < LA ? q : q - LA) * 8 * K + kb * 128);
+        }
+        load_lds4(rs, S + kg * STAGE + sdst, so, kb * 4);
     };
-    auto frag = [&](const char *base, int row) {
-        Frag f;
-        f.lo = *reinterpret_cast<const i32x4 *>(base + row * 128 + (((2 * g) ^ (row & 7)) << 4));
-        f.hi = *reinterpret_cast<const i32x4 *>(base + row * 128 + (((2 * g + 1) ^ (row & 7)) << 4));
-        return f;
-    };
-    const int mw = m0 + wm * (BM / WM), nw = n0 + wn * (BN / WN);  // the wave's corner
+    const LaneRow rows(lane);
+    const float *sb_square = BROW ? nullptr : a.sb + (size_t)(min(n0 + br, a.N - 1) >> 7) * nkb;
 
     f32x4 acc[TM][TN];
 #pragma unroll
@@ -145,64 +217,454 @@ __global__ __launch_bounds__(64 * WM * WN) void matmul_tile_kernel(MatArgs a) {
 #pragma unroll
         for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    if (a.nkb > 0) issue(0, 0);
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    for (int kb = 0; kb < a.nkb; ++kb) {
-        const int buf = kb & 1;
+    float sbn = 1.f;
+    if (nkb > 0) {
+        if (!BROW) sbn = uniform_load(sb_square + min(k0, nkb - 1));
+        issue(0, S0);
+        if (ST > 2) issue(1, S1);
+        if (ST > 3) issue(2, S2);
+    }
+    // block i of the group, in S; D is the stage that the block before it has left
+    auto step = [&](int i, const char *S, char *D) __attribute__((always_inline)) {
+        wait_barrier<(ST - 2) * (L + 1)>();  // this block has landed for every wave, and all are done with the last one
+        issue(i + ST - 1, D);
+        if (KG > 1 && k0 + i >= k1) return;  // a group that has one block less
+        S += kg * STAGE;
         float sa[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) sa[i] = a.sa[(size_t)min(mw + 16 * i + l16, a.M - 1) * a.nkb + kb];
-        if (kb + 1 < a.nkb) issue(kb + 1, buf ^ 1);
-        using F = std::conditional_t<WIDE, WideFrag, Frag>;
-        auto conv = [](const Frag &f) -> F {
-            if constexpr (WIDE) return widen(f);
-            else return f;
-        };
-        F fa[TM];
+        for (int r = 0; r < TM; ++r) sa[r] = *reinterpret_cast<const float *>(S + SA + 4 * (ar + 16 * r + l16)) * sbn;
+        if (!BROW) sbn = uniform_load(sb_square + min(k0 + i + 1, nkb - 1));
+        OperandOf<OUT> fa[TM];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) fa[i] = conv(frag(As[buf], wm * (BM / WM) + 16 * i + l16));
+        for (int r = 0; r < TM; ++r) fa[r] = operand<OUT>(rows.load(S + (ar + 16 * r) * 128));
+        f32x4 p[2][TM], sb[2];
 #pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const F fb = conv(frag(Bs[buf], wn * (BN / WN) + 16 * j + l16));
-            f32x4 sb;
-            if constexpr (BROW) {
+        for (int j = 0; j <= TN; ++j) {  // products one column tile ahead of the folds
+            if (j < TN) {
+                const OperandOf<OUT> fb = operand<OUT>(rows.load(S + (BM + br + 16 * j) * 128));
+                if constexpr (BROW) sb[j & 1] = *reinterpret_cast<const f32x4 *>(S + SB + 4 * (br + 16 * j + 4 * g));
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sb[r] = a.sb[(size_t)min(nw + 16 * j + 4 * g + r, a.N - 1) * a.nkb + kb];
-            } else {
-                const float s = a.sb[(size_t)(min(nw + 16 * j, a.N - 1) >> 7) * a.nkb + kb];
-                sb = f32x4{s, s, s, s};
+                for (int r = 0; r < TM; ++r) p[j & 1][r] = block_product(fb, fa[r]);
             }
+            if (j > 0) {
+                const int u = (j - 1) & 1;
 #pragma unroll
-            for (int i = 0; i < TM; ++i) {
-                const f32x4 p = block_product(fb, fa[i]);
+                for (int r = 0; r < TM; ++r)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(p[r], sa[i] * sb[r], acc[i][j][r]);
+                    for (int e = 0; e < 4; ++e)
+                        acc[r][j - 1][e] = fmaf(p[u][r][e], BROW ? sa[r] * sb[u][e] : sa[r], acc[r][j - 1][e]);
             }
         }
-        __builtin_amdgcn_s_waitcnt(0);  // the next block has landed
+    };
+    for (int i = 0; i < steps;) {
+        if constexpr (ST == 2) {
+            step(i, S0, S1);
+            if (++i == steps) break;
+            step(i, S1, S0);
+        } else if constexpr (ST == 3) {
+            step(i, S0, S2);
+            if (++i == steps) break;
+            step(i, S1, S0);
+            if (++i == steps) break;
+            step(i, S2, S1);
+        } else {
+            step(i, S0, S3);
+            if (++i == steps) break;
+            step(i, S1, S0);
+            if (++i == steps) break;
+            step(i, S2, S1);
+            if (++i == steps) break;
+            step(i, S3, S2);
+        }
+        ++i;
+    }
+    wait_barrier<0>();  // no load into LDS is under way any more
+    if constexpr (KG > 1) {
+        static_assert((KG - 1) * NW * TM * TN * 1024 <= KG * STAGE, "");
+        f32x4 *red = reinterpret_cast<f32x4 *>(S0);
+        if (kg > 0) {
+#pragma unroll
+            for (int t = 0; t < TM * TN; ++t) red[(((kg - 1) * NW + wv) * TM * TN + t) * 64 + lane] = acc[t / TN][t % TN];
+        }
         __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int q = 0; q < KG - 1; ++q)
+#pragma unroll
+            for (int t = 0; t < TM * TN; ++t) acc[t / TN][t % TN] += red[((q * NW + wv) * TM * TN + t) * 64 + lane];
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int m = mw + 16 * i + l16;
+        const int m = m0 + ar + 16 * i + l16;
         if (m >= a.M) continue;
         OUT *row = static_cast<OUT *>(a.out) + (size_t)m * a.N;
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
-            const int n = nw + 16 * j + 4 * g;
+            const int n = n0 + br + 16 * j + 4 * g;
             if (n < a.N) store_row4(row, n, a.N, acc[i][j]);
         }
     }
 }
 
-template <typename OUT, bool BROW>
-hipError_t matmul(MatArgs a, hipStream_t st) {
-    constexpr int BM = 128, BN = 128;
+template <int BM, int BN, int KG, int WM, int WN, int ST, typename OUT, bool BROW>
+__global__ __launch_bounds__(64 * KG * WM * WN) void matmul_tile_kernel(MatArgs a) {
+    tile_body<BM, BN, KG, WM, WN, ST, OUT, BROW>(a);
+}
+
+// A few tokens against all of B (a decode step): B is read once, straight into registers.  A workgroup of KW waves takes
+// 16 NT features and up to 16 MT tokens; the waves split the contraction's blocks and their sums meet in LDS.
+template <int MT, int NT, int KW, typename OUT, bool BROW>
+__device__ __forceinline__ void stream_body(const MatArgs &a) {
+    constexpr int COLS = 16 * NT, LD = COLS + 4;
+    __shared__ __attribute__((aligned(16))) float red[KW][16 * MT][LD];
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4;
+    const int n0 = blockIdx.x * COLS, m0 = blockIdx.y * 16 * MT;
+    const int k0 = (int)((int64_t)a.nkb * wv / KW), k1 = (int)((int64_t)a.nkb * (wv + 1) / KW);
+    const uint8_t *ap[MT], *bp[NT];
+    const float *sap[MT], *sbp[NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        const size_t row = min(m0 + 16 * i + l16, a.M - 1);
+        ap[i] = a.a + row * a.K + 16 * g;
+        sap[i] = a.sa + row * a.nkb;
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        bp[j] = a.b + (size_t)min(n0 + 16 * j + l16, a.N - 1) * a.K + 16 * g;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            sbp[j][r] = a.sb + (BROW ? (size_t)min(n0 + 16 * j + 4 * g + r, a.N - 1) : (size_t)(min(n0 + 16 * j, a.N - 1) >> 7)) * a.nkb;
+    }
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    struct Blk {
+        Frag a[MT], b[NT];
+        float sa[MT], sb[NT][4];
+    };
+    auto load = [&](int kb) __attribute__((always_inline)) {
+        Blk x;
+        const size_t o = (size_t)kb * 128;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            x.b[j].lo = *reinterpret_cast<const i32x4 *>(bp[j] + o);
+            x.b[j].hi = *reinterpret_cast<const i32x4 *>(bp[j] + o + 64);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            x.a[i].lo = *reinterpret_cast<const i32x4 *>(ap[i] + o);
+            x.a[i].hi = *reinterpret_cast<const i32x4 *>(ap[i] + o + 64);
+            x.sa[i] = sap[i][kb];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < (BROW ? 4 : 1); ++r) x.sb[j][r] = sbp[j][r][kb];
+        return x;
+    };
+    auto use = [&](const Blk &x) __attribute__((always_inline)) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const OperandOf<OUT> fb = operand<OUT>(x.b[j]);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const f32x4 p = block_product(fb, operand<OUT>(x.a[i]));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(p[r], x.sa[i] * x.sb[j][BROW ? r : 0], acc[i][j][r]);
+            }
+        }
+    };
+    if (k0 < k1) {
+        Blk x = load(k0);
+        for (int kb = k0; kb < k1; kb += 2) {
+            const Blk y = load(min(kb + 1, k1 - 1));
+            use(x);
+            if (kb + 1 >= k1) break;
+            x = load(min(kb + 2, k1 - 1));
+            use(y);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4 *>(&red[wv][16 * i + l16][16 * j + 4 * g]) = acc[i][j];
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * MT * COLS / 4; e += 64 * KW) {
+        const int m = e / (COLS / 4), n = 4 * (e % (COLS / 4));
+        if (m0 + m >= a.M || n0 + n >= a.N) continue;
+        f32x4 s = *reinterpret_cast<const f32x4 *>(&red[0][m][n]);
+#pragma unroll
+        for (int w = 1; w < KW; ++w) s += *reinterpret_cast<const f32x4 *>(&red[w][m][n]);
+        store_row4(static_cast<OUT *>(a.out) + (size_t)(m0 + m) * a.N, n0 + n, a.N, s);
+    }
+}
+template <int MT, int NT, int KW, typename OUT, bool BROW>
+__global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
+    stream_body<MT, NT, KW, OUT, BROW>(a);
+}
+
+
+// The whole chip on a large product (bf16 output, B scaled in squares).  256
+// workgroups of 8 waves, one per CU, each walk over 256 x 256 tiles; a wave
+// holds 64 tokens x 128 features of the tile as 4 x 8 results (128
+// registers).  Two LDS stages of a block (64 KiB each), filled by direct
+// loads; the sequence of blocks runs on over the tiles' ends, so a tile's
+// first blocks are under way while the last one's results are stored.
+//   - A block is worked off in four phases of two column tiles.  Each phase
+//     starts by reading the next phase's operands into registers, and the
+//     last phase the next block's A; the one barrier of a block stands before
+//     the last phase, when the block's bytes are all in registers and the
+//     next block's have landed, and the loads of the block after that go out
+//     behind it, spread over that phase's products.
+//   - Results are folded two products behind.
+//   - A ninth load per wave and block brings A's scales two blocks ahead (four
+//     waves) or pulls lines three blocks ahead into the XCD's L2 (the others:
+//     a quarter of A's rows and an eighth of B's, which the 32 workgroups of
+//     an XCD share); without it the loads' latency showed (2.18 against
+//     1.70 us per block).
+//   - After a lane swap every lane stores 16 bytes of a row.
+// 16384 x 8192 x 4096: 502 us = 2190 TFLOP/s; of its 1.69 us per block and
+// workgroup the products and folds alone take 1.15, and with the reads of LDS
+// and the barrier but no loads 1.46 (each with the clock that it runs at).
+struct BigTile {
+    int m0, n0, share;  // share: first of the rows whose lines this wave pulls into L2
+};
+
+__device__ __forceinline__ void big_body(const MatArgs &a) {
+    constexpr int BM = 256, BN = 256, NW = 8, TM = 4, TN = 8, LAG = 2, AHEAD = 3;
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    __shared__ __attribute__((aligned(1024))) char As0[BM * 128];
+    __shared__ __attribute__((aligned(1024))) char As1[BM * 128];
+    __shared__ __attribute__((aligned(1024))) char Bs0[BN * 128];
+    __shared__ __attribute__((aligned(1024))) char Bs1[BN * 128];
+    __shared__ float Ss[5][BM];  // a ring of four blocks' scales, and the place where the L2 loads' bytes go
+
+    const int total = a.mt * a.nt, per = (total + 7) / 8, xcd = blockIdx.x % 8, slots = gridDim.x / 8;
+    const int tend = min(per, total - xcd * per);
+    int t = blockIdx.x / 8;
+    if (t >= tend) return;
+
+    const int K = a.K, nkb = a.nkb;
+    const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int l16 = lane & 15, g = lane >> 4, ar = wv / 2 * 64, br = wv % 2 * 128;
+    const bool scales = wv < 4, pulls_a = wv < 6;
+
+    // as tile_of, for tile tt of this XCD's range
+    auto big_tile = [&](int tt) __attribute__((always_inline)) {
+        const int id = xcd * per + tt, grp = id / (8 * a.nt), in = id % (8 * a.nt), gm = min(8, a.mt - grp * 8);
+        const int tm = in % gm, tn = in / gm;
+        return BigTile{(grp * 8 + tm) * BM, tn * BN, scales ? 0 : pulls_a ? 64 * (tn & 3) : 32 * (tm & 7)};
+    };
+    const auto ra = rsrc(a.a, (uint32_t)((size_t)a.M * K)), rb = rsrc(a.b, (uint32_t)((size_t)a.N * K));
+    const auto rx = scales ? rsrc(a.sa, (uint32_t)((size_t)a.M * nkb * 4)) : pulls_a ? ra : rb;
+    const int vo = 8 * wv * K + swizzled_source(lane, wv, K);
+    const int xo = scales ? (64 * wv + lane) * nkb * 4
+                          : (pulls_a ? 32 * (wv & 1) + (lane & 31) : 16 * (wv & 1) + (lane & 15)) * K;
+    const int xstep = scales ? 4 : 128, xahead = scales ? 2 : AHEAD;
+    auto xbase = [&](const BigTile &x) __attribute__((always_inline)) {
+        return scales ? x.m0 * nkb * 4 : ((pulls_a ? x.m0 : x.n0) + x.share) * K;
+    };
+    auto sbase = [&](const BigTile &x) __attribute__((always_inline)) { return (min(x.n0 + br, a.N - 1) >> 7) * nkb; };
+
+    // byte offsets of this tile's and the next one's A, B, extra loads and B scales
+    BigTile cur = big_tile(t), nxt = big_tile(min(t + slots, tend - 1));
+    int a0 = cur.m0 * K, a1 = nxt.m0 * K, b0 = cur.n0 * K, b1 = nxt.n0 * K, x0 = xbase(cur), x1 = xbase(nxt);
+    int s0 = sbase(cur), s1 = sbase(nxt);
+
+    // load i (of 8) of block kb, which may lie past this tile's end: then it is the next tile's
+    auto issue = [&](int kb, char *Ad, char *Bd, int i) __attribute__((always_inline)) {
+        const bool over = kb >= nkb;
+        const int k = (over ? kb - nkb : kb) * 128;
+        if (i < 4)
+            load_lds16(ra, Ad + (wv + NW * i) * 1024, vo, (over ? a1 : a0) + k + i * 64 * K);
+        else
+            load_lds16(rb, Bd + (wv + NW * (i - 4)) * 1024, vo, (over ? b1 : b0) + k + (i - 4) * 64 * K);
+    };
+    // the ninth load, as of block kb, number gs of all blocks
+    auto extra = [&](int kb, int gs) __attribute__((always_inline)) {
+        const int kk = max(kb + xahead, 0);
+        const bool over = kk >= nkb;
+        float *dst = scales ? &Ss[(gs + 2) & 3][64 * wv] : Ss[4];
+        load_lds4(rx, reinterpret_cast<char *>(dst), xo, (over ? x1 : x0) + (over ? kk - nkb : kk) * xstep);
+    };
+    const LaneRow rows(lane);
+
+    f32x4 acc[TM][TN];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    extra(-2, -2);
+    extra(-1, -1);
+    extra(0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(0, As0, Bs0, i);
+    wait_barrier<0>();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) issue(1, As1, Bs1, i);
+    Frag fa[TM], fb[2][2];
+    float sa[TM];
+    const float sb0 = uniform_load(a.sb + s0);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+        fa[i] = rows.load(As0 + (ar + 16 * i) * 128);
+        sa[i] = Ss[0][ar + 16 * i + l16] * sb0;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) fb[0][j] = rows.load(Bs0 + (br + 16 * j) * 128);
+
+    int gs = 0, kb = 0;
+    auto step = [&](char *Ac, char *Bc, char *An, char *Bn) __attribute__((always_inline)) {
+        f32x4 p[4];
+        float sn[TM], sbn;
+        // product u of the block is that of column tile 2 (u / 8) + u % 2 and row tile u / 2 % 4
+        auto fold = [&](int u) __attribute__((always_inline)) {
+            const int j = 2 * (u / (2 * TM)) + (u & 1), i = u / 2 % TM;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(p[u & 3][r], sa[i], acc[i][j][r]);
+        };
+#pragma unroll
+        for (int ph = 0; ph < TN / 2; ++ph) {
+            const bool last = ph == TN / 2 - 1;
+            if (last) {
+                wait_barrier<1>();  // the newest load, the ninth, may still be under way
+#pragma unroll
+                for (int i = 0; i < TM; ++i) sn[i] *= sbn;
+            }
+            __builtin_amdgcn_sched_barrier(0);
+            if (ph == 0) sbn = uniform_load(a.sb + (kb + 1 < nkb ? s0 + kb + 1 : s1));
+            const char *bnext = last ? Bn : Bc;
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                fb[(ph + 1) & 1][j] = rows.load(bnext + (br + 16 * (last ? j : 2 * ph + 2 + j)) * 128);
+            if (ph == 0) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) sn[i] = Ss[(gs + 1) & 3][ar + 16 * i + l16];
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int u = ph * TM * 2 + i * 2 + j;
+                    p[u & 3] = block_product(fb[ph & 1][j], fa[i]);
+                    if (u >= LAG) fold(u - LAG);
+                }
+                if (last) {
+                    fa[i] = rows.load(An + (ar + 16 * i) * 128);
+                    issue(kb + 2, Ac, Bc, 2 * i);
+                    issue(kb + 2, Ac, Bc, 2 * i + 1);
+                }
+                if (ph == 0 && i == 1) extra(kb + 1, gs + 1);
+            }
+        }
+#pragma unroll
+        for (int u = TM * TN - LAG; u < TM * TN; ++u) fold(u);
+#pragma unroll
+        for (int i = 0; i < TM; ++i) sa[i] = sn[i];
+        ++gs;
+        ++kb;
+    };
+    auto tile_end = [&]() __attribute__((always_inline)) {
+        const auto ro = rsrc(static_cast<uint16_t *>(a.out) + (size_t)cur.m0 * a.N, (uint32_t)(min(BM, a.M - cur.m0) * a.N * 2));
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; j += 2) {
+                // lanes of even g take tile j, of odd g tile j + 1: features 8 (g / 2) .. + 7 of it
+                const f32x4 v = acc[i][j], w = acc[i][j + 1];
+                const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0], v[1]), pack_bf16(w[0], w[1]), false, false);
+                const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2], v[3]), pack_bf16(w[2], w[3]), false, false);
+                const int m = ar + 16 * i + l16, n = cur.n0 + br + 16 * (j + (g & 1)) + 8 * (g >> 1);
+                const int off = n < a.N ? (m * a.N + n) * 2 : 0x7fffffff;  // rows and columns past the end are dropped
+                __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, off, 0, 0);
+                acc[i][j] = acc[i][j + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+        t += slots;
+        if (t >= tend) return false;
+        cur = nxt, a0 = a1, b0 = b1, x0 = x1, s0 = s1;
+        nxt = big_tile(min(t + slots, tend - 1));
+        a1 = nxt.m0 * K, b1 = nxt.n0 * K, x1 = xbase(nxt), s1 = sbase(nxt);
+        return true;
+    };
+    do {
+        for (kb = 0; kb < nkb;) {
+            step(As0, Bs0, As1, Bs1);
+            step(As1, Bs1, As0, Bs0);
+        }
+    } while (tile_end());
+    __builtin_amdgcn_s_waitcnt(0);  // loads past the last block still write this workgroup's LDS
+}
+
+__global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_body(a); }
+
+// ---- choice of a kernel -------------------------------------------------------
+// Times of a kernel are close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
+// tile's latency, and the chip's throughput over T tiles, T rounded up to
+// whole rounds of the workgroups that run at once.  The constants (us) are
+// fits to its times over 1 .. 4096 tokens, 512 .. 8192 features and a
+// contraction of 512 .. 8192 (bf16 output; fp32 output in the second row),
+// e.g. tiles of 32 x 32 | 64 x 64 | 128 x 128 | 256 x 256:
+//   300 x 512 x 512        3.3 |   4.0 |   6.7 |  12.5 us
+//   777 x 2048 x 2048     18.7 |  11.7 |  14.6 |  28.6
+//   4096 x 2048 x 2048    76.7 |  38.9 |  24.5 |  31.8
+//   4096 x 8192 x 8192     904 |   566 |   297 |   231
+struct Fit {
+    int rows, round;
+    double f0, f1, t0, t1;
+};
+constexpr Fit kFit[2][4] = {
+    {{32, 1, 2.8, 0.11, 0.0030, 0.000385}, {64, 1, 2.7, 0.23, 0.0025, 0.00104}, {128, 512, 3.5, 0.60, 0.010, 0.0021},
+     {256, 256, 6.0, 1.35, 0.035, 0.0065}},
+    {{32, 1, 2.7, 0.16, 0.0032, 0.000415}, {64, 1, 2.6, 0.42, 0.0037, 0.00108}, {128, 512, 2.6, 1.05, 0.012, 0.00346},
+     {}}};
+
+double fitted_us(const Fit &f, int64_t M, int64_t N, int64_t nkb) {
+    int64_t T = ((M + f.rows - 1) / f.rows) * ((N + f.rows - 1) / f.rows);
+    T = (T + f.round - 1) / f.round * f.round;
+    const double lone = f.f0 + f.f1 * nkb, chip = T * (f.t0 + f.t1 * nkb);
+    return lone > chip ? lone : chip;
+}
+
+template <int BM, int BN, int KG, int WM, int WN, int ST, typename OUT, bool BROW>
+void launch_tile(MatArgs a, hipStream_t st) {
     a.mt = (a.M + BM - 1) / BM;
     a.nt = (a.N + BN - 1) / BN;
-    const unsigned grid = (unsigned)((a.mt * a.nt + 7) / 8 * 8);
-    hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, 2, 2, OUT, BROW>), dim3(grid), dim3(256), 0, st, a);
+    const unsigned grid = (unsigned)(((int64_t)a.mt * a.nt + 7) / 8 * 8);
+    hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, KG, WM, WN, ST, OUT, BROW>), dim3(grid), dim3(64 * KG * WM * WN), 0,
+                       st, a);
+}
+
+template <typename OUT, bool BROW>
+hipError_t matmul(MatArgs a, hipStream_t st) {
+    constexpr bool wide = sizeof(OUT) == 4;
+    if (a.M <= 8 && a.nkb > 0) {
+        // few tokens: one 16-token operand per wave, B straight from memory (1 x 4096 x 4096: 4.6 us, 32 x 32 tiles 7.7;
+        // at 16 tokens the rows of A that every wave reads again tip it: 10.8 against 9.6 us for 512 x 8192)
+        hipLaunchKernelGGL((matmul_stream_kernel<1, 1, 8, OUT, BROW>), dim3((a.N + 15) / 16, 1), dim3(512), 0, st, a);
+        return hipGetLastError();
+    }
+    int best = 0;
+    double us = 1e30;
+    for (int i = 0; i < 4; ++i) {
+        // the large kernel: 32-bit offsets over the whole of A and B, blocks in pairs, 16-byte stores
+        if (i == 3 && (wide || BROW || a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
+                       (int64_t)(a.N + 256) * a.K > INT32_MAX || (int64_t)a.N * 512 > INT32_MAX))
+            break;
+        const double x = fitted_us(kFit[wide][i], a.M, a.N, a.nkb);
+        if (x < us) us = x, best = i;
+    }
+    if (best == 0) launch_tile<32, 32, 2, 2, 1, 4, OUT, BROW>(a, st);
+    else if (best == 1) launch_tile<64, 64, 1, 2, 2, 3, OUT, BROW>(a, st);
+    else if (best == 2) launch_tile<128, 128, 1, 2, 2, 2, OUT, BROW>(a, st);
+    else {
+        a.mt = (a.M + 255) / 256;
+        a.nt = (a.N + 255) / 256;
+        hipLaunchKernelGGL(matmul_big_kernel, dim3(256), dim3(512), 0, st, a);
+    }
     return hipGetLastError();
 }
 
