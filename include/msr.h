@@ -347,7 +347,7 @@ msr_status msr_set_exchange(int32_t mode);
  * by 128 columns, see block_rows) has one fp32 scale and stands for
  * scale * value.  The operators that write them choose
  *   scale = max(largest magnitude / 448, 2^-126),
- *   value = round-to-nearest-even(x * (1 / scale));
+ *   value = round-to-nearest-even(x / scale);
  * a block that holds an infinity or a NaN stands for NaN.
  */
 #define MSR_BLOCK 128

@@ -10,6 +10,8 @@
 // group v of lane l of wave w starts at element 8 (64 (v W + w) + l), so a
 // wave reads contiguous kilobytes and a block of 128 is one row of 16 lanes
 // (its largest magnitude needs four lane-row rotations, no LDS).
+#include <algorithm>
+
 #include "msr_quant.hpp"
 
 namespace {
@@ -29,7 +31,7 @@ struct NormArgs {
 // the sum over the W waves that share a row (team `tm` of the workgroup)
 template <int W>
 __device__ __forceinline__ float team_sum(float x, float *red, int tm, int w) {
-    x = wave_sum(x);
+    x = wave_sum_dpp(x);
     if constexpr (W > 1) {
         if ((threadIdx.x & 63) == 0) red[tm * W + w] = x;
         __syncthreads();
@@ -92,9 +94,9 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = max(m, abs_bits(h[v][i]));
-            const float s = block_scale(row16_max(m)), inv = 1.f / s;
+            const float s = block_scale(row16_max(m));
             if (live && e < a.dpad) {
-                *reinterpret_cast<uint2 *>(a.q + row * a.dpad + e) = pack8(h[v], inv);
+                *reinterpret_cast<uint2 *>(a.q + row * a.dpad + e) = pack8(h[v], s);
                 if ((lane & 15) == 0) a.qs[row * (a.dpad / kBlock) + e / kBlock] = s;
             }
         }
@@ -104,60 +106,82 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
 struct NormBackArgs {
     const void *h, *w, *dy, *dsum;  // w, dsum may be NULL
     void *dx;
-    float *part;                    // [gridDim.x * TEAMS][d], or NULL: no weight gradient
+    float *part;                    // [gridDim.x][d], or NULL: no weight gradient
     int64_t rows;
     int d, w_bf16;
     float eps;
 };
 
-// Each team walks over rows team, team + teams, ... and keeps the weight's
-// gradient over them in registers; the teams' sums go to `part` and are
-// added by column_sum_kernel in a fixed order (no atomics).
+// Each team walks over rows team, team + teams, ... with the next row's loads
+// under way (where the registers allow: V <= 2), and keeps the weight and its gradient over those rows in
+// registers; the workgroup's teams add up in LDS, its sum goes to `part`, and
+// column_sum_kernel adds the parts in a fixed order (no atomics).
 template <typename T, bool VEC, int W, int V>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(NormBackArgs a) {
     constexpr int TEAMS = W < 4 ? 4 / W : 1;
     __shared__ float red[2][2 * TEAMS * W];
+    __shared__ float dws[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? 512 * W * V : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tm = wave / W, w = wave % W;
     const int64_t team = (int64_t)blockIdx.x * TEAMS + tm, teams = (int64_t)gridDim.x * TEAMS;
     const int64_t turns = (a.rows + teams - 1) / teams;  // the same for every team: the barriers match
-    float dw[V][8];
+    const int e0 = 8 * (64 * w + lane);                  // group v starts at e0 + 512 W v
+    Raw8<T, VEC> hr[V], gr[V], dr[V];
+    auto fetch = [&](int64_t t) {  // past the last row: that row again, not used
+        const int64_t r = t * teams + team, row = r < a.rows ? r : a.rows - 1;
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            const int e = e0 + 512 * W * v;
+            hr[v].load(static_cast<const T *>(a.h) + row * a.d + e, a.d - e);
+            gr[v].load(static_cast<const T *>(a.dy) + row * a.d + e, a.d - e);
+            if (a.dsum) dr[v].load(static_cast<const T *>(a.dsum) + row * a.d + e, a.d - e);
+        }
+    };
+    constexpr bool early = V <= 2;
+    float wt[V][8], dw[V][8];
+    fetch(0);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const int e = e0 + 512 * W * v;
+        load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+    }
+    const float inv_d = 1.f / (float)a.d;
     for (int64_t t = 0; t < turns; ++t) {
-        const int64_t row_raw = t * teams + team;
-        const bool live = row_raw < a.rows;
-        const int64_t row = live ? row_raw : a.rows - 1;
-        const T *hp = static_cast<const T *>(a.h) + row * a.d, *dyp = static_cast<const T *>(a.dy) + row * a.d;
-        float h[V][8], g[V][8];
+        const int64_t row = t * teams + team;
+        float h[V][8], g[V][8], ds[V][8];
         float ss = 0.f, gh = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = 8 * (64 * (v * W + w) + lane);
-            load8<VEC>(hp + e, a.d - e, h[v]);
-            load8<VEC>(dyp + e, a.d - e, g[v]);
-        }
+            hr[v].get(h[v]);
+            gr[v].get(g[v]);
+            if (a.dsum) {
+                dr[v].get(ds[v]);
+            } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = 8 * (64 * (v * W + w) + lane);
-            float wt[8];
-            load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt);
+                for (int i = 0; i < 8; ++i) ds[v][i] = 0.f;
+            }
+        }
+        if (early && t + 1 < turns) fetch(t + 1);
+#pragma unroll
+        for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 ss = fmaf(h[v][i], h[v][i], ss);
-                gh = fmaf(h[v][i], g[v][i] * wt[i], gh);
+                gh = fmaf(h[v][i], g[v][i] * wt[v][i], gh);
             }
-        }
-        ss = wave_sum(ss);
-        gh = wave_sum(gh);
+        ss = wave_sum_dpp(ss);
+        gh = wave_sum_dpp(gh);
         if constexpr (W > 1) {
             float *rd = red[t & 1];  // two areas: one barrier per turn separates a turn's reads from its writes
             if (lane == 0) {
                 rd[2 * (tm * W + w)] = ss;
                 rd[2 * (tm * W + w) + 1] = gh;
             }
-            __syncthreads();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_waitcnt(0xc07f);  // lgkmcnt(0): the next row's loads stay under way
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
             ss = gh = 0.f;
 #pragma unroll
             for (int i = 0; i < W; ++i) {
@@ -165,54 +189,75 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
                 gh += rd[2 * (tm * W + i) + 1];
             }
         }
-        const float rstd = 1.f / sqrtf(ss / (float)a.d + a.eps);
-        const float c = rstd * rstd * (gh / (float)a.d);
-        if (!live) continue;
+        const float rstd = 1.f / sqrtf(ss * inv_d + a.eps);
+        const float c = rstd * rstd * (gh * inv_d);
+        if (row >= a.rows) continue;  // the last turn of this team
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = 8 * (64 * (v * W + w) + lane);
-            float wt[8], ds[8];
-            load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt);
-            if (a.dsum) {
-                load8<VEC>(static_cast<const T *>(a.dsum) + row * a.d + e, a.d - e, ds);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) ds[i] = 0.f;
-            }
+            const int e = e0 + 512 * W * v;
             float o[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                o[i] = fmaf(rstd, g[v][i] * wt[i] - h[v][i] * c, ds[i]);
+                o[i] = fmaf(rstd, g[v][i] * wt[v][i] - h[v][i] * c, ds[v][i]);
                 dw[v][i] = fmaf(g[v][i], h[v][i] * rstd, dw[v][i]);
             }
             store8<VEC>(static_cast<T *>(a.dx) + row * a.d + e, a.d - e, o);
         }
+        if (!early && t + 1 < turns) fetch(t + 1);
     }
     if (a.part) {
+        if constexpr (TEAMS > 1) {
+            if (tm > 0) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dws[tm - 1][(v * W + w) * 512 + i * 64 + lane] = dw[v][i];
+            }
+            __syncthreads();
+            if (tm > 0) return;
+#pragma unroll
+            for (int q = 0; q < TEAMS - 1; ++q)
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dw[v][i] += dws[q][(v * W + w) * 512 + i * 64 + lane];
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = 8 * (64 * (v * W + w) + lane);
-            store8<VEC>(a.part + team * a.d + e, a.d - e, dw[v]);
+            const int e = e0 + 512 * W * v;
+            store8<VEC>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, dw[v]);
         }
     }
 }
 
-// out[c] = sum_p part[p][c], p in order within each of 64 slices, the slices in order
-__global__ __launch_bounds__(256) void column_sum_kernel(const float *part, float *out, int parts, int d) {
-    __shared__ float red[64][17];
-    const int c = (int)blockIdx.x * 16 + 4 * (threadIdx.x & 3), sl = threadIdx.x >> 2;
+// out[c] = sum_p part[p][c] for 32 columns: p in order within each of 64
+// slices, the slices in order
+template <bool VEC>
+__global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out, int parts, int d) {
+    __shared__ float red[64][33];
+    const int q = 4 * (threadIdx.x & 7), c = (int)blockIdx.x * 32 + q, sl = threadIdx.x >> 3;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int p = sl; p < parts; p += 64)
+    if constexpr (VEC) {
+        if (c < d)
+#pragma unroll 8
+            for (int p = sl; p < parts; p += 64) {
+                const float4 x = *reinterpret_cast<const float4 *>(part + (size_t)p * d + c);
+                s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+            }
+    } else {
+        for (int p = sl; p < parts; p += 64)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (c + i < d) s[i] += part[(size_t)p * d + c + i];
+            for (int i = 0; i < 4; ++i)
+                if (c + i < d) s[i] += part[(size_t)p * d + c + i];
+    }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[sl][4 * (threadIdx.x & 3) + i] = s[i];
+    for (int i = 0; i < 4; ++i) red[sl][q + i] = s[i];
     __syncthreads();
-    if (threadIdx.x < 16) {
+    if (threadIdx.x < 32) {
         float t = 0.f;
+#pragma unroll
         for (int i = 0; i < 64; ++i) t += red[i][threadIdx.x];
-        const int o = (int)blockIdx.x * 16 + threadIdx.x;
+        const int o = (int)blockIdx.x * 32 + threadIdx.x;
         if (o < d) out[o] = t;
     }
 }
@@ -225,7 +270,7 @@ hipError_t by_width(int d, F f) {
     if (d <= 2048) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
     if (d <= 4096) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
     if (d <= 8192) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
-    if (d <= 16384) return f(std::integral_constant<int, 16>(), std::integral_constant<int, 2>());
+    if (d <= 16384) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 4>());
     return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
 }
 
@@ -235,12 +280,14 @@ hipError_t by_type(int dtype, bool vec, F f) {
     return vec ? f(float(), std::true_type()) : f(float(), std::false_type());
 }
 
-constexpr int kBackGroups = 512;  // workgroups of the backward pass at most
+// Workgroups of the backward pass: each writes one partial weight gradient.
+constexpr int kBackGroups = 512;
 
-int back_teams(int64_t rows, int d) {
-    const int per = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
-    const int64_t g = (rows + per - 1) / per;
-    return (int)(g < kBackGroups ? g : kBackGroups) * per;
+int back_groups(int64_t rows, int d) {
+    const int teams = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
+    const int64_t g = (rows + teams - 1) / teams;
+    const int64_t most = rows / 8 > 256 ? rows / 8 : 256;  // (few rows: the parts' own bytes count)
+    return (int)std::min<int64_t>(g, std::min<int64_t>(most, kBackGroups));
 }
 
 }  // namespace
@@ -258,22 +305,24 @@ hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, con
     });
 }
 
-size_t rmsnorm_backward_workspace(int64_t rows, int d) { return (size_t)back_teams(rows, d) * d * sizeof(float); }
+size_t rmsnorm_backward_workspace(int64_t rows, int d) { return (size_t)back_groups(rows, d) * d * sizeof(float); }
 
 hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h, const void *w, int w_dtype, float eps,
                                    const void *dy, const void *dsum, void *dx, float *dw, float *part, hipStream_t st) {
-    const int parts = back_teams(rows, d);
+    const int parts = back_groups(rows, d);
     const NormBackArgs a{h, w, dy, dsum, dx, dw ? part : nullptr, rows, d, w_dtype == MSR_BF16, eps};
     hipError_t e = parts == 0 ? hipSuccess : by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
         return by_width(d, [&](auto W, auto V) {
-            constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
-            hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), vec.value, W.value, V.value>), dim3(parts / teams),
+            constexpr int nt = W.value < 4 ? 256 : 64 * W.value;
+            hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), vec.value, W.value, V.value>), dim3(parts),
                                dim3(nt), 0, st, a);
             return hipGetLastError();
         });
     });
     if (e == hipSuccess && dw) {
-        hipLaunchKernelGGL(column_sum_kernel, dim3((d + 15) / 16), dim3(256), 0, st, part, dw, parts, d);
+        const dim3 grid((d + 31) / 32), block(512);
+        if (d % 4 == 0) hipLaunchKernelGGL(column_sum_kernel<true>, grid, block, 0, st, part, dw, parts, d);
+        else hipLaunchKernelGGL(column_sum_kernel<false>, grid, block, 0, st, part, dw, parts, d);
         e = hipGetLastError();
     }
     return e;

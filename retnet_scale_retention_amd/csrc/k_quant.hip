@@ -31,7 +31,7 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
         for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
         const float sc = block_scale(row16_max(m));
         if (b_raw < blocks) {
-            *reinterpret_cast<uint2 *>(a.q + row * a.Cp + c) = pack8(v, 1.f / sc);
+            *reinterpret_cast<uint2 *>(a.q + row * a.Cp + c) = pack8(v, sc);
             if ((threadIdx.x & 15) == 0) a.s[b] = sc;
         }
     }
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + 8 * rg + i;
             if (r < a.R) {
-                *reinterpret_cast<uint2 *>(a.q + r * a.Cp + c) = pack8(v[i], 1.f / rs[i]);
+                *reinterpret_cast<uint2 *>(a.q + r * a.Cp + c) = pack8(v[i], rs[i]);
                 if (!SQUARE && cg == 0) a.s[r * (a.Cp / kBlock) + tc] = rs[i];
             }
         }
@@ -119,7 +119,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const float col[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
-            *reinterpret_cast<uint2 *>(tr + (8 * cg + j) * LDT + 8 * rg) = pack8(col, 1.f / cs[j]);
+            *reinterpret_cast<uint2 *>(tr + (8 * cg + j) * LDT + 8 * rg) = pack8(col, cs[j]);
         }
         __syncthreads();
 #pragma unroll

@@ -26,13 +26,21 @@ __device__ __forceinline__ float block_scale(uint32_t amax_bits) {
     return s < kScaleFloor ? kScaleFloor : s;
 }
 
-// eight values times inv as e4m3 bytes, in order (round to nearest even)
-__device__ __forceinline__ uint2 pack8(const float (&v)[8], float inv) {
+// v / s, inv = 1 / s: the product's error is made up for by its remainder (Markstein's step), so that a value is rounded
+// to 8 bits from its correctly rounded quotient; v * inv alone moves values that lie between two e4m3 numbers.
+__device__ __forceinline__ float quotient(float v, float s, float inv) {
+    const float q = v * inv;
+    return fmaf(fmaf(-q, s, v), inv, q);
+}
+
+// eight values over s as e4m3 bytes, in order (round to nearest even)
+__device__ __forceinline__ uint2 pack8(const float (&v)[8], float s) {
+    const float inv = 1.f / s;
     int a = 0, b = 0;
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[0] * inv, v[1] * inv, a, false);
-    a = __builtin_amdgcn_cvt_pk_fp8_f32(v[2] * inv, v[3] * inv, a, true);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[4] * inv, v[5] * inv, b, false);
-    b = __builtin_amdgcn_cvt_pk_fp8_f32(v[6] * inv, v[7] * inv, b, true);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[0], s, inv), quotient(v[1], s, inv), a, false);
+    a = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[2], s, inv), quotient(v[3], s, inv), a, true);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[4], s, inv), quotient(v[5], s, inv), b, false);
+    b = __builtin_amdgcn_cvt_pk_fp8_f32(quotient(v[6], s, inv), quotient(v[7], s, inv), b, true);
     return make_uint2((uint32_t)a, (uint32_t)b);
 }
 
@@ -56,43 +64,72 @@ __device__ __forceinline__ float row16_sum(float x) {
     return x + __uint_as_float(row_ror<1>(__float_as_uint(x)));
 }
 
-// Eight consecutive elements at p (16-byte aligned when VEC): elements from
-// index `left` on lie past the row's end, are not read and count as zero.
-template <bool VEC>
-__device__ __forceinline__ void load8(const uint16_t *p, int left, float (&v)[8]) {
-    if constexpr (VEC) {
-        if (left > 0) {
-            const uint4 u = *reinterpret_cast<const uint4 *>(p);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? bf16_to_f32(p[i]) : 0.f;
-    }
+// the sum over the wave: lane rows by rotation, the four rows by the lane swaps
+__device__ __forceinline__ float wave_sum_dpp(float x) {
+    const uint32_t a = __float_as_uint(row16_sum(x));
+    const auto r = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    const uint32_t b = __float_as_uint(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+    const auto t = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return __uint_as_float(t[0]) + __uint_as_float(t[1]);
 }
 
-template <bool VEC>
-__device__ __forceinline__ void load8(const float *p, int left, float (&v)[8]) {
-    if constexpr (VEC) {
-        if (left > 0) {
-            const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.f;
+// Eight consecutive elements at p (16-byte aligned when VEC) as they lie in
+// memory, and as floats: loads go out early this way and are widened late.
+// Elements from index `left` on lie past the row's end, are not read and
+// count as zero.
+template <typename T, bool VEC>
+struct Raw8;
+
+template <>
+struct Raw8<uint16_t, true> {
+    uint4 u;
+    __device__ __forceinline__ void load(const uint16_t *p, int left) {
+        u = make_uint4(0, 0, 0, 0);
+        if (left > 0) u = *reinterpret_cast<const uint4 *>(p);
     }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+};
+
+template <>
+struct Raw8<float, true> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p, int left) {
+        a = b = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (left > 0) {
+            a = *reinterpret_cast<const float4 *>(p);
+            b = *reinterpret_cast<const float4 *>(p + 4);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+
+template <typename T>
+struct Raw8<T, false> {
+    float x[8];
+    __device__ __forceinline__ void load(const T *p, int left) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = i < left ? msr::load(p, i) : 0.f;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x[i];
+    }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load8(const T *p, int left, float (&v)[8]) {
+    Raw8<T, VEC> r;
+    r.load(p, left);
+    r.get(v);
 }
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));

@@ -362,48 +362,46 @@ def msr_recurrent_step(q, k, v, state, gamma, pos, *, theta=None, scale=0.0, eps
 
 # ------------------------------------------------- the layer around retention
 BLOCK = 128  # MSR_BLOCK
+_codes = {}  # torch dtype -> MSR_* of these entry points' inputs, filled on first use
+
+
+def _code(name, t):
+    """MSR_F32 or MSR_BF16 of a tensor that has to be a contiguous one on the device."""
+    if not _codes:
+        torch = _torch()
+        _codes.update({torch.float32: MSR_F32, torch.bfloat16: MSR_BF16})
+    if not (t.is_cuda and t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous device tensor")
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name}; use float32 or bfloat16")
+    return code
 
 
 def _padded(n: int) -> int:
     return (n + BLOCK - 1) // BLOCK * BLOCK
 
 
-def _expect(name, t, shape, dtype, device):
-    """t, checked to be a contiguous tensor of this shape, type and device."""
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
-    return t
+def _expect(name, t, shape, dtype, index):
+    """t's address, t checked to be a contiguous tensor of this shape and type on device `index`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on device {index}")
+    return t.data_ptr()
 
 
-def _like(name, t, shape, dtype, device):
-    """A new tensor of this shape, type and device, or t after the same checks."""
-    if t is None:
-        return _torch().empty(shape, dtype=dtype, device=device)
-    return _expect(name, t, shape, dtype, device)
+def _new(shape, dtype, device):
+    return _torch().empty(shape, dtype=dtype, device=device)
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
+def _stream_of(index, stream):
+    return _torch()._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _raw_stream(device, stream):
-    return (_torch().cuda.current_stream(device) if stream is None else stream).cuda_stream
-
-
-def _matrix(name, x):
-    """(rows, d) of a contiguous device tensor [..., d]."""
-    if not x.is_cuda or not x.is_contiguous() or x.dim() < 1:
-        raise ValueError(f"{name} must be a contiguous device tensor")
-    *lead, d = x.shape
-    return math.prod(lead), d
-
-
-def _weight(weight, d, device):
+def _weight(weight, d, index):
     if weight is None:
         return None, MSR_F32
-    if weight.shape != (d,) or weight.device != device or not weight.is_contiguous():
-        raise ValueError(f"weight must be a contiguous [{d}] tensor on {device}")
-    return weight.data_ptr(), _dtype_code(weight)
+    code = _code("weight", weight)
+    return _expect("weight", weight, (d,), weight.dtype, index), code
 
 
 def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, want_q=False, out=None, stream=None):
@@ -412,24 +410,39 @@ def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, wan
     not computed: y = n in x's type (want_y); sum = h in x's type (when a residual is given); q, scale (want_q) = n as
     float8_e4m3fn [..., P(d)] (P: the next multiple of 128, zeros there) with a float32 scale per 128 values,
     [..., P(d) / 128].  out: tensors to write, in the same order (sum may be x or residual, y may be x)."""
-    torch = _torch()
-    rows, d = _matrix("x", x)
-    code, dev = _dtype_code(x), x.device
-    if residual is not None and (residual.shape != x.shape or residual.dtype != x.dtype or residual.device != dev
-                                 or not residual.is_contiguous()):
-        raise ValueError("residual must be a contiguous tensor of x's shape, type and device")
-    wp, wcode = _weight(weight, d, dev)
+    code, shape, dtype, dev = _code("x", x), x.shape, x.dtype, x.get_device()
+    d = shape[-1] if shape else 0
     y, total, q, scale = (None, None, None, None) if out is None else out
-    lead, dp = x.shape[:-1], _padded(d)
-    y = _like("y", y, x.shape, x.dtype, dev) if want_y else None
-    total = _like("sum", total, x.shape, x.dtype, dev) if residual is not None else None
+    rp = tp = yp = qp = sp = None
+    if residual is None:
+        total = None
+    else:
+        rp = _expect("residual", residual, shape, dtype, dev)
+        if total is None:
+            total = _new(shape, dtype, x.device)
+        tp = _expect("sum", total, shape, dtype, dev)
+    wp, wcode = _weight(weight, d, dev)
+    if want_y:
+        if y is None:
+            y = _new(shape, dtype, x.device)
+        yp = _expect("y", y, shape, dtype, dev)
+    else:
+        y = None
     if want_q:
-        q = _like("q", q, (*lead, dp), torch.float8_e4m3fn, dev)
-        scale = _like("scale", scale, (*lead, dp // BLOCK), torch.float32, dev)
+        torch = _torch()
+        lead, blocks = shape[:-1], (d + BLOCK - 1) // BLOCK
+        if q is None:
+            q = _new(lead + (blocks * BLOCK,), torch.float8_e4m3fn, x.device)
+        if scale is None:
+            scale = _new(lead + (blocks,), torch.float32, x.device)
+        qp = _expect("q", q, lead + (blocks * BLOCK,), torch.float8_e4m3fn, dev)
+        sp = _expect("scale", scale, lead + (blocks,), torch.float32, dev)
     else:
         q = scale = None
-    _check(load().msr_add_rmsnorm(rows, d, code, x.data_ptr(), _address(residual), wp, wcode, eps, _address(total),
-                                  _address(y), _address(q), _address(scale), _raw_stream(dev, stream)))
+    s = (_lib or load()).msr_add_rmsnorm(math.prod(shape[:-1]), d, code, x.data_ptr(), rp, wp, wcode, eps, tp, yp, qp,
+                                         sp, _stream_of(dev, stream))
+    if s:
+        _check(s)
     return y, total, q, scale
 
 
@@ -439,25 +452,32 @@ def msr_add_rmsnorm_backward(h, weight, grad_y, *, grad_sum=None, eps=1e-6, want
     dL/dsum or None, all [..., d] of one type.  Returns (dx, dweight or None): dx is the gradient of x and of the
     residual, in h's type; dweight is float32 [d].  out: tensors to write, in the same order."""
     torch = _torch()
-    rows, d = _matrix("h", h)
-    code, dev = _dtype_code(h), h.device
-    for name, t in (("grad_y", grad_y), ("grad_sum", grad_sum)):
-        if t is None and name == "grad_sum":
-            continue
-        if t.shape != h.shape or t.dtype != h.dtype or t.device != dev or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous tensor of h's shape, type and device")
+    code, shape, dtype, dev = _code("h", h), h.shape, h.dtype, h.get_device()
+    d = shape[-1] if shape else 0
+    rows = math.prod(shape[:-1])
+    gp = _expect("grad_y", grad_y, shape, dtype, dev)
+    sp = None if grad_sum is None else _expect("grad_sum", grad_sum, shape, dtype, dev)
     wp, wcode = _weight(weight, d, dev)
     dx, dw = (None, None) if out is None else out
-    dx = _like("dx", dx, h.shape, h.dtype, dev)
-    dw = _like("dweight", dw, (d,), torch.float32, dev) if want_weight_grad else None
-    lib, n = load(), 0
+    if dx is None:
+        dx = _new(shape, dtype, h.device)
+    xp, dwp, ws, n = _expect("dx", dx, shape, dtype, dev), None, None, 0
+    lib = _lib or load()
     if want_weight_grad:
+        if dw is None:
+            dw = _new((d,), torch.float32, h.device)
+        dwp = _expect("dweight", dw, (d,), torch.float32, dev)
         n = lib.msr_add_rmsnorm_backward_workspace(rows, d)
-        if n and (workspace is None or workspace.numel() < n):
-            workspace = torch.empty(n, dtype=torch.uint8, device=dev)
-    _check(lib.msr_add_rmsnorm_backward(rows, d, code, h.data_ptr(), wp, wcode, eps, grad_y.data_ptr(),
-                                        _address(grad_sum), dx.data_ptr(), _address(dw),
-                                        _address(workspace) if n else None, n, _raw_stream(dev, stream)))
+        if n:
+            if workspace is None or workspace.numel() < n:
+                workspace = _new(n, torch.uint8, h.device)
+            ws = workspace.data_ptr()
+    else:
+        dw = None
+    s = lib.msr_add_rmsnorm_backward(rows, d, code, h.data_ptr(), wp, wcode, eps, gp, sp, xp, dwp, ws, n,
+                                     _stream_of(dev, stream))
+    if s:
+        _check(s)
     return dx, dw
 
 
@@ -468,25 +488,36 @@ def msr_quantize(x, *, block_rows=1, want_rows=True, want_transposed=False, out=
     128], scale_t [cols, P(rows) / 128]; block_rows 128: a scale per 128 x 128 square, [P(rows) / 128, P(cols) / 128]
     and its transpose.  out: tensors to write, in the same order."""
     torch = _torch()
-    if x.dim() != 2 or not x.is_cuda or not x.is_contiguous():
-        raise ValueError("x must be a contiguous device matrix")
-    R, C = x.shape
-    code, dev, square = _dtype_code(x), x.device, block_rows == BLOCK
-    q, s, qt, st = (None, None, None, None) if out is None else out
-    f8, f32, rp, cp = torch.float8_e4m3fn, torch.float32, _padded(R), _padded(C)
+    code = _code("x", x)
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    (R, C), dev = x.shape, x.get_device()
+    q, sc, qt, st = (None, None, None, None) if out is None else out
+    f8, f32, rb, cb = torch.float8_e4m3fn, torch.float32, (R + BLOCK - 1) // BLOCK, (C + BLOCK - 1) // BLOCK
+    square = block_rows == BLOCK
+    qp = sp = qtp = stp = None
     if want_rows:
-        q = _like("q", q, (R, cp), f8, dev)
-        s = _like("scale", s, (rp // BLOCK if square else R, cp // BLOCK), f32, dev)
+        shape = (rb if square else R, cb)
+        if q is None:
+            q = _new((R, cb * BLOCK), f8, x.device)
+        if sc is None:
+            sc = _new(shape, f32, x.device)
+        qp, sp = _expect("q", q, (R, cb * BLOCK), f8, dev), _expect("scale", sc, shape, f32, dev)
     else:
-        q = s = None
+        q = sc = None
     if want_transposed:
-        qt = _like("qt", qt, (C, rp), f8, dev)
-        st = _like("scale_t", st, (cp // BLOCK if square else C, rp // BLOCK), f32, dev)
+        shape = (cb if square else C, rb)
+        if qt is None:
+            qt = _new((C, rb * BLOCK), f8, x.device)
+        if st is None:
+            st = _new(shape, f32, x.device)
+        qtp, stp = _expect("qt", qt, (C, rb * BLOCK), f8, dev), _expect("scale_t", st, shape, f32, dev)
     else:
         qt = st = None
-    _check(load().msr_quantize(R, C, code, block_rows, x.data_ptr(), _address(q), _address(s), _address(qt),
-                               _address(st), _raw_stream(dev, stream)))
-    return q, s, qt, st
+    s = (_lib or load()).msr_quantize(R, C, code, block_rows, x.data_ptr(), qp, sp, qtp, stp, _stream_of(dev, stream))
+    if s:
+        _check(s)
+    return q, sc, qt, st
 
 
 def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, workspace=None, stream=None):
@@ -494,25 +525,31 @@ def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, works
     128], b [N, K] with b_scale [N, K / 128] or, per 128 x 128 square, [P(N) / 128, K / 128] (float32; K a multiple
     of 128).  Returns [..., N] of out_dtype: bfloat16 (default) or float32."""
     torch = _torch()
-    m, k = _matrix("a", a)
-    if b.dim() != 2 or not b.is_contiguous() or b.device != a.device or b.shape[1] != k:
-        raise ValueError(f"b must be a contiguous [N, {k}] tensor on {a.device}")
-    if a.dtype != torch.float8_e4m3fn or b.dtype != torch.float8_e4m3fn:
+    if not (a.is_cuda and a.is_contiguous()) or not a.dim():
+        raise ValueError("a must be a contiguous device tensor")
+    if a.dtype is not torch.float8_e4m3fn or b.dtype is not torch.float8_e4m3fn:
         raise TypeError("a and b must be float8_e4m3fn")
-    n, dev, kb = b.shape[0], a.device, k // BLOCK
-    _expect("a_scale", a_scale, (*a.shape[:-1], kb), torch.float32, dev)
-    rows = 1 if b_scale.shape[:1] == (n,) else BLOCK
-    _expect("b_scale", b_scale, (n if rows == 1 else _padded(n) // BLOCK, kb), torch.float32, dev)
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if out is None else out.dtype
-    out = _like("out", out, (*a.shape[:-1], n), out_dtype, dev)
-    code, lib = _dtype_code(out), load()
-    ws = lib.msr_scaled_matmul_workspace(m, n, k, code)
-    if ws and (workspace is None or workspace.numel() < ws):
-        workspace = torch.empty(ws, dtype=torch.uint8, device=dev)
-    _check(lib.msr_scaled_matmul(m, n, k, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), rows,
-                                 code, out.data_ptr(), _address(workspace) if ws else None, ws,
-                                 _raw_stream(dev, stream)))
+    lead, dev, f32 = a.shape[:-1], a.get_device(), torch.float32
+    k, n, m = a.shape[-1], b.shape[0] if b.dim() else 0, math.prod(lead)
+    kb = k // BLOCK
+    bp = _expect("b", b, (n, k), torch.float8_e4m3fn, dev)
+    ap = _expect("a_scale", a_scale, lead + (kb,), f32, dev)
+    rows = 1 if b_scale.shape == (n, kb) else BLOCK
+    sp = _expect("b_scale", b_scale, (n if rows == 1 else (n + BLOCK - 1) // BLOCK, kb), f32, dev)
+    if out is None:
+        out = _new(lead + (n,), out_dtype or torch.bfloat16, a.device)
+    code = _code("out", out)
+    op = _expect("out", out, lead + (n,), out_dtype or out.dtype, dev)
+    lib = _lib or load()
+    ws, wp = lib.msr_scaled_matmul_workspace(m, n, k, code), None
+    if ws:
+        if workspace is None or workspace.numel() < ws:
+            workspace = _new(ws, torch.uint8, a.device)
+        wp = workspace.data_ptr()
+    s = lib.msr_scaled_matmul(m, n, k, a.data_ptr(), ap, b.data_ptr(), sp, rows, code, op, wp, ws,
+                              _stream_of(dev, stream))
+    if s:
+        _check(s)
     return out
 
 
