@@ -31,103 +31,124 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
         for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
         const float sc = block_scale(row16_max(m));
         if (b_raw < blocks) {
-            *reinterpret_cast<uint2 *>(a.q + row * a.Cp + c) = pack8(v, sc);
+            stream_out(a.q + row * a.Cp + c, pack8(v, sc));
             if ((threadIdx.x & 15) == 0) a.s[b] = sc;
         }
     }
 }
 
+// the largest over the lanes l, l ^ 16, l ^ 32, l ^ 48
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    const uint32_t y = max((uint32_t)r[0], (uint32_t)r[1]);
+    const auto t = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return max((uint32_t)t[0], (uint32_t)t[1]);
+}
+
 // A workgroup takes a 128 x 128 tile: thread t holds the 8 x 8 values of rows
-// 8 (t / 16) .., columns 8 (t % 16) .. in registers, so both directions'
-// packs are register work; the transposed bytes pass through LDS to leave in
-// whole 128-byte rows.
+// 8 (t / 16) .., columns 8 (t % 16) .. in registers, as they came, so both
+// directions' packs are register work; the transposed bytes pass through LDS
+// to leave in whole 128-byte rows.  Bound by memory: 16384 x 4096 bf16 in
+// both orders 48 us (5.7 TB/s), in squares 42 us (6.4 TB/s).  What it took:
+// the values kept as loaded, not widened (174 -> 117 registers, 74 -> 59 us;
+// the squares' kernel has room for the floats and is faster with them), and
+// stores that do not linger in L2 (59 -> 48 us).
 template <typename T, bool VEC, bool SQUARE>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
     constexpr int LDT = 144;  // bytes between the rows of the transposed tile: 16-byte aligned, off the banks' period
-    __shared__ uint32_t cmax[4][128];
+    __shared__ __attribute__((aligned(16))) uint32_t cmax[4][128];
+    __shared__ float cscale[128];
     __shared__ uint32_t tmax[4];
     __shared__ __attribute__((aligned(16))) uint8_t tr[128 * LDT];
     const int64_t tr_i = blockIdx.x / a.tiles_c, tc = blockIdx.x % a.tiles_c;
     const int64_t r0 = tr_i * 128, c0 = tc * 128;
     const int rg = threadIdx.x >> 4, cg = threadIdx.x & 15, wave = threadIdx.x >> 6;
     const int64_t c = c0 + 8 * cg;
-    float v[8][8];
+    Raw8<T, VEC> x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = r0 + 8 * rg + i;
-        load8<VEC>(static_cast<const T *>(a.x) + r * a.C + c, r < a.R ? (int)(a.C - c) : 0, v[i]);
+        x[i].load(static_cast<const T *>(a.x) + r * a.C + c, r < a.R ? (int)(a.C - c) : 0);
     }
-    uint32_t rm[8], cm[8];
+    uint32_t cm[8], all = 0;  // the columns' largest magnitudes, and the tile's
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rm[i] = cm[i] = 0;
+    for (int j = 0; j < 8; ++j) cm[j] = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 8; ++i) {
+        float v[8];
+        x[i].get(v);
+        uint32_t rm = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const uint32_t m = abs_bits(v[i][j]);
-            rm[i] = max(rm[i], m);
+            const uint32_t m = abs_bits(v[j]);
+            rm = max(rm, m);
             cm[j] = max(cm[j], m);
         }
-    float rs[8], cs[8];
-    if constexpr (SQUARE) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, rm[i]);
-        m = row16_max(m);
-        m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-        m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-        if ((threadIdx.x & 63) == 0) tmax[wave] = m;
-        __syncthreads();
-        const float s = block_scale(max(max(tmax[0], tmax[1]), max(tmax[2], tmax[3])));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rs[i] = cs[i] = s;
-        if (threadIdx.x == 0) {
-            if (a.q) a.s[tr_i * (a.Cp / kBlock) + tc] = s;
-            if (a.qt) a.st[tc * (a.Rp / kBlock) + tr_i] = s;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rs[i] = block_scale(row16_max(rm[i]));
-        if (a.qt) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                uint32_t m = cm[j];
-                m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-                m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-                if ((threadIdx.x & 48) == 0) cmax[wave][8 * cg + j] = m;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int k = 8 * cg + j;
-                cs[j] = block_scale(max(max(cmax[0][k], cmax[1][k]), max(cmax[2][k], cmax[3][k])));
-                if (rg == 0 && c + j < a.C) a.st[(c + j) * (a.Rp / kBlock) + tr_i] = cs[j];
-            }
-        }
-    }
-    if (a.q) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        if constexpr (SQUARE) {
+            all = max(all, rm);
+        } else if (a.q) {
+            const float s = block_scale(row16_max(rm));
             const int64_t r = r0 + 8 * rg + i;
             if (r < a.R) {
-                *reinterpret_cast<uint2 *>(a.q + r * a.Cp + c) = pack8(v[i], rs[i]);
-                if (!SQUARE && cg == 0) a.s[r * (a.Cp / kBlock) + tc] = rs[i];
+                stream_out(a.q + r * a.Cp + c, pack8(v, s));
+                if (cg == 0) a.s[r * (a.Cp / kBlock) + tc] = s;
             }
         }
+        if (!SQUARE) x[i].forget();
+    }
+    float square = 0.f;
+    if constexpr (SQUARE) {
+        all = wave_max(row16_max(all));
+        if ((threadIdx.x & 63) == 0) tmax[wave] = all;
+        __syncthreads();
+        square = block_scale(max(max(tmax[0], tmax[1]), max(tmax[2], tmax[3])));
+        if (threadIdx.x == 0) {
+            if (a.q) a.s[tr_i * (a.Cp / kBlock) + tc] = square;
+            if (a.qt) a.st[tc * (a.Rp / kBlock) + tr_i] = square;
+        }
+        if (a.q) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t r = r0 + 8 * rg + i;
+                float v[8];
+                x[i].get(v);
+                if (r < a.R) stream_out(a.q + r * a.Cp + c, pack8(v, square));
+            }
+        }
+    } else if (a.qt) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) cm[j] = wave_max(cm[j]);
+        if ((threadIdx.x & 48) == 0) {
+            *reinterpret_cast<uint4 *>(&cmax[wave][8 * cg]) = make_uint4(cm[0], cm[1], cm[2], cm[3]);
+            *reinterpret_cast<uint4 *>(&cmax[wave][8 * cg + 4]) = make_uint4(cm[4], cm[5], cm[6], cm[7]);
+        }
+        __syncthreads();
+        if (threadIdx.x < 128) {  // one thread per column
+            const int k = threadIdx.x;
+            const float s = block_scale(max(max(cmax[0][k], cmax[1][k]), max(cmax[2][k], cmax[3][k])));
+            cscale[k] = s;
+            if (c0 + k < a.C) a.st[(c0 + k) * (a.Rp / kBlock) + tr_i] = s;
+        }
+        __syncthreads();
     }
     if (a.qt) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float col[8] = {v[0][j], v[1][j], v[2][j], v[3][j], v[4][j], v[5][j], v[6][j], v[7][j]};
-            *reinterpret_cast<uint2 *>(tr + (8 * cg + j) * LDT + 8 * rg) = pack8(col, cs[j]);
+            float col[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float v[8];
+                x[i].get(v);
+                col[i] = v[j];
+            }
+            *reinterpret_cast<uint2 *>(tr + (8 * cg + j) * LDT + 8 * rg) = pack8(col, SQUARE ? square : cscale[8 * cg + j]);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int k = 32 * i + (int)(threadIdx.x >> 3), b = 16 * (threadIdx.x & 7);
             if (c0 + k < a.C)
-                *reinterpret_cast<uint4 *>(a.qt + (c0 + k) * a.Rp + r0 + b) =
-                    *reinterpret_cast<const uint4 *>(tr + k * LDT + b);
+                stream_out(a.qt + (c0 + k) * a.Rp + r0 + b, *reinterpret_cast<const uint4 *>(tr + k * LDT + b));
         }
     }
 }
