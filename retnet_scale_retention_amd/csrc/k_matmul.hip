@@ -417,18 +417,21 @@ __global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
 //     starts by reading the next phase's operands into registers, and the
 //     last phase the next block's A; the one barrier of a block stands before
 //     the last phase, when the block's bytes are all in registers and the
-//     next block's have landed, and the loads of the block after that go out
-//     behind it, spread over that phase's products.
+//     next block's have landed.  The loads of the block after that go out
+//     behind it, A's between the last phase's products and B's between those
+//     of the phase that follows (all of them in the last phase: 500 us).
 //   - Results are folded two products behind.
 //   - A ninth load per wave and block brings A's scales two blocks ahead (four
 //     waves) or pulls lines three blocks ahead into the XCD's L2 (the others:
 //     a quarter of A's rows and an eighth of B's, which the 32 workgroups of
-//     an XCD share); without it the loads' latency showed (2.18 against
-//     1.70 us per block).
+//     an XCD share); without it the loads' latency showed (2.2 against 1.7 us
+//     per block).
 //   - After a lane swap every lane stores 16 bytes of a row.
-// 16384 x 8192 x 4096: 502 us = 2190 TFLOP/s; of its 1.69 us per block and
-// workgroup the products and folds alone take 1.15, and with the reads of LDS
-// and the barrier but no loads 1.46 (each with the clock that it runs at).
+// 16384 x 8192 x 4096: 485 us = 2270 TFLOP/s.  Of its 1.6 us per block and
+// workgroup the products and folds alone take 1.15, with the reads of LDS and
+// the barrier but no loads 1.45 (each at the clock that it runs at); the
+// tiles' ends cost 70 us, 45 of them the 268 MB of results, which all
+// workgroups write at the same time.
 struct BigTile {
     int m0, n0, share;  // share: first of the rows whose lines this wave pulls into L2
 };
@@ -505,7 +508,7 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     for (int i = 0; i < 8; ++i) issue(0, As0, Bs0, i);
     wait_barrier<0>();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) issue(1, As1, Bs1, i);
+    for (int i = 0; i < 4; ++i) issue(1, As1, Bs1, i);
     Frag fa[TM], fb[2][2];
     float sa[TM];
     const float sb0 = uniform_load(a.sb + s0);
@@ -555,10 +558,10 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
                 }
                 if (last) {
                     fa[i] = rows.load(An + (ar + 16 * i) * 128);
-                    issue(kb + 2, Ac, Bc, 2 * i);
-                    issue(kb + 2, Ac, Bc, 2 * i + 1);
+                    issue(kb + 2, Ac, Bc, i);
                 }
-                if (ph == 0 && i == 1) extra(kb + 1, gs + 1);
+                if (ph == 0) issue(kb + 1, An, Bn, 4 + i);
+                if (ph == 1 && i == 1) extra(kb + 1, gs + 1);
             }
         }
 #pragma unroll

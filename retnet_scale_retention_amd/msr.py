@@ -400,8 +400,10 @@ def _stream_of(index, stream):
 def _weight(weight, d, index):
     if weight is None:
         return None, MSR_F32
-    code = _code("weight", weight)
-    return _expect("weight", weight, (d,), weight.dtype, index), code
+    dtype = weight.dtype
+    if dtype not in _codes:
+        raise TypeError(f"unsupported dtype {dtype} of weight; use float32 or bfloat16")
+    return _expect("weight", weight, (d,), dtype, index), _codes[dtype]
 
 
 def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, want_q=False, out=None, stream=None):
