@@ -418,14 +418,12 @@ msr_status msr_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block
  * The gradients of y = x w^T are products of the same kind:
  *   dx = dy w    A = dy by rows, B = the weight's transposed copy
  *   dw = dy^T x  A, B = the transposed copies of dy and x, b_block_rows 1
- * m or n of 0 launches nothing, k of 0 writes zeros.  Needs a workspace of
- * msr_scaled_matmul_workspace(m, n, k, out_dtype) bytes (0 for most sizes).
- * out must not overlap an input.
+ * m or n of 0 launches nothing, k of 0 writes zeros; k is at most 2^24 - 128.
+ * out must not overlap an input.  Needs no workspace.
  */
 msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, const float *a_scale, const void *b,
-                             const float *b_scale, int32_t b_block_rows, int32_t out_dtype, void *out, void *ws,
-                             size_t ws_bytes, void *hip_stream);
-size_t msr_scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, int32_t out_dtype);
+                             const float *b_scale, int32_t b_block_rows, int32_t out_dtype, void *out,
+                             void *hip_stream);
 
 #ifdef __cplusplus
 }

@@ -673,10 +673,8 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
 
 }  // namespace
 
-size_t scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, int out_dtype) { return 0; }
-
 hipError_t launch_scaled_matmul(int m, int n, int k, const void *A, const float *sa, const void *B, const float *sb,
-                                int b_rows, int out_dtype, void *out, void *ws, hipStream_t st) {
+                                int b_rows, int out_dtype, void *out, hipStream_t st) {
     const MatArgs a{static_cast<const uint8_t *>(A), static_cast<const uint8_t *>(B), sa, sb, out, m, n, k, k / 128, 0, 0};
     if (out_dtype == MSR_BF16) return b_rows == 1 ? matmul<uint16_t, true>(a, st) : matmul<uint16_t, false>(a, st);
     return b_rows == 1 ? matmul<float, true>(a, st) : matmul<float, false>(a, st);

@@ -99,9 +99,8 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h
                                    const void *dy, const void *dsum, void *dx, float *dw, float *part, hipStream_t st);
 hipError_t launch_quantize(int64_t R, int64_t C, int dtype, int block_rows, const void *x, void *q, float *s, void *qt,
                            float *s_t, hipStream_t st);
-size_t scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, int out_dtype);
 hipError_t launch_scaled_matmul(int m, int n, int k, const void *A, const float *sa, const void *B, const float *sb,
-                                int b_rows, int out_dtype, void *out, void *ws, hipStream_t st);
+                                int b_rows, int out_dtype, void *out, hipStream_t st);
 
 // Sets this thread's msr_last_error text and returns s.
 msr_status set_error(msr_status s, const char *fmt, ...);

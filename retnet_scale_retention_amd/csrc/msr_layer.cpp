@@ -129,14 +129,9 @@ msr_status msr_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block
                 "quantize");
 }
 
-size_t msr_scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, int32_t out_dtype) {
-    if (m <= 0 || n <= 0 || k <= 0 || m > INT32_MAX || n > INT32_MAX || k > INT32_MAX || bad_dtype(out_dtype)) return 0;
-    return scaled_matmul_workspace(m, n, k, out_dtype);
-}
-
 msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, const float *a_scale, const void *b,
-                             const float *b_scale, int32_t b_block_rows, int32_t out_dtype, void *out, void *ws,
-                             size_t ws_bytes, void *hip_stream) {
+                             const float *b_scale, int32_t b_block_rows, int32_t out_dtype, void *out,
+                             void *hip_stream) {
     if (bad_dtype(out_dtype))
         return set_error(MSR_ERR_DTYPE, "out_dtype %d is neither MSR_F32 (0) nor MSR_BF16 (1)", out_dtype);
     if (m < 0 || n < 0 || k < 0 || m > INT32_MAX - 1024 || n > INT32_MAX - 1024 || k > INT32_MAX)
@@ -152,15 +147,13 @@ msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, con
     if (m == 0 || n == 0) return MSR_OK;
     if (!out || (k > 0 && (!a || !a_scale || !b || !b_scale)))
         return set_error(MSR_ERR_INVALID_ARG, "a, a_scale, b, b_scale and out must be non-NULL");
-    const size_t kb = (size_t)k / MSR_BLOCK, need = scaled_matmul_workspace(m, n, k, out_dtype);
-    const Tensor t[6] = {{"a", a, (size_t)m * k}, {"a_scale", a_scale, (size_t)m * kb * 4}, {"b", b, (size_t)n * k},
+    const size_t kb = (size_t)k / MSR_BLOCK;
+    const Tensor t[5] = {{"a", a, (size_t)m * k}, {"a_scale", a_scale, (size_t)m * kb * 4}, {"b", b, (size_t)n * k},
                          {"b_scale", b_scale, (size_t)(b_block_rows == 1 ? n : padded(n) / MSR_BLOCK) * kb * 4},
-                         {"out", out, (size_t)m * n * elem(out_dtype)}, {"ws", ws, need}};
+                         {"out", out, (size_t)m * n * elem(out_dtype)}};
     msr_status s;
-    if ((s = check_aligned(t, 6)) != MSR_OK || (s = check_overlap(t, 6, 4, nullptr)) != MSR_OK) return s;
-    if (need > 0 && (!ws || ws_bytes < need))
-        return set_error(MSR_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? ws_bytes : 0);
-    return done(launch_scaled_matmul((int)m, (int)n, (int)k, a, a_scale, b, b_scale, b_block_rows, out_dtype, out, ws,
+    if ((s = check_aligned(t, 5)) != MSR_OK || (s = check_overlap(t, 5, 4, nullptr)) != MSR_OK) return s;
+    return done(launch_scaled_matmul((int)m, (int)n, (int)k, a, a_scale, b, b_scale, b_block_rows, out_dtype, out,
                                      static_cast<hipStream_t>(hip_stream)),
                 "scaled matmul");
 }

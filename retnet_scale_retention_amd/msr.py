@@ -29,7 +29,7 @@ EXPORTS = ("msr_abi_version", "msr_last_error", "msr_workspace_size", "msr_works
            "msr_chunkwise", "msr_chunkwise_noalloc", "msr_chunkwise_backward", "msr_qkv_projection", "msr_qkv_chunkwise",
            "msr_recurrent_step", "msr_set_kernel_events", "msr_set_exchange",
            "msr_add_rmsnorm", "msr_add_rmsnorm_backward", "msr_add_rmsnorm_backward_workspace", "msr_quantize",
-           "msr_scaled_matmul", "msr_scaled_matmul_workspace")
+           "msr_scaled_matmul")
 
 
 class MsrError(RuntimeError):
@@ -96,9 +96,8 @@ def load():
     lib.msr_add_rmsnorm_backward_workspace.argtypes, lib.msr_add_rmsnorm_backward_workspace.restype = [i64, i32], sz
     lib.msr_quantize.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, vp, vp]
     lib.msr_quantize.restype = ctypes.c_int
-    lib.msr_scaled_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp, sz, vp]
+    lib.msr_scaled_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp]
     lib.msr_scaled_matmul.restype = ctypes.c_int
-    lib.msr_scaled_matmul_workspace.argtypes, lib.msr_scaled_matmul_workspace.restype = [i64, i64, i64, i32], sz
     del fp
     _lib = lib
     return lib
@@ -362,24 +361,37 @@ def msr_recurrent_step(q, k, v, state, gamma, pos, *, theta=None, scale=0.0, eps
 
 # ------------------------------------------------- the layer around retention
 BLOCK = 128  # MSR_BLOCK
-_codes = {}  # torch dtype -> MSR_* of these entry points' inputs, filled on first use
+
+
+class _Torch:
+    """What these entry points use of torch, looked up once (they are called for every token, and a call's host time is
+    most of a small one's cost)."""
+
+    def __init__(self):
+        torch = _torch()
+        self.f32, self.f8, self.u8, self.empty = torch.float32, torch.float8_e4m3fn, torch.uint8, torch.empty
+        self.codes = {torch.float32: MSR_F32, torch.bfloat16: MSR_BF16}
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+_tc = None
+
+
+def _setup():
+    global _tc
+    load()
+    _tc = _Torch()
+    return _tc
 
 
 def _code(name, t):
     """MSR_F32 or MSR_BF16 of a tensor that has to be a contiguous one on the device."""
-    if not _codes:
-        torch = _torch()
-        _codes.update({torch.float32: MSR_F32, torch.bfloat16: MSR_BF16})
     if not (t.is_cuda and t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous device tensor")
-    code = _codes.get(t.dtype)
+    code = _tc.codes.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype} of {name}; use float32 or bfloat16")
     return code
-
-
-def _padded(n: int) -> int:
-    return (n + BLOCK - 1) // BLOCK * BLOCK
 
 
 def _expect(name, t, shape, dtype, index):
@@ -389,21 +401,19 @@ def _expect(name, t, shape, dtype, index):
     return t.data_ptr()
 
 
-def _new(shape, dtype, device):
-    return _torch().empty(shape, dtype=dtype, device=device)
-
-
-def _stream_of(index, stream):
-    return _torch()._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-
-
 def _weight(weight, d, index):
     if weight is None:
         return None, MSR_F32
     dtype = weight.dtype
-    if dtype not in _codes:
+    code = _tc.codes.get(dtype)
+    if code is None:
         raise TypeError(f"unsupported dtype {dtype} of weight; use float32 or bfloat16")
-    return _expect("weight", weight, (d,), dtype, index), _codes[dtype]
+    return _expect("weight", weight, (d,), dtype, index), code
+
+
+def _rows(shape):
+    """Rows of an array [..., d]."""
+    return shape[0] if len(shape) == 2 else math.prod(shape[:-1])
 
 
 def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, want_q=False, out=None, stream=None):
@@ -412,37 +422,41 @@ def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, wan
     not computed: y = n in x's type (want_y); sum = h in x's type (when a residual is given); q, scale (want_q) = n as
     float8_e4m3fn [..., P(d)] (P: the next multiple of 128, zeros there) with a float32 scale per 128 values,
     [..., P(d) / 128].  out: tensors to write, in the same order (sum may be x or residual, y may be x)."""
-    code, shape, dtype, dev = _code("x", x), x.shape, x.dtype, x.get_device()
+    tc = _tc or _setup()
+    code = _code("x", x)
+    shape, dtype, dev = x.shape, x.dtype, x.get_device()
     d = shape[-1] if shape else 0
-    y, total, q, scale = (None, None, None, None) if out is None else out
-    rp = tp = yp = qp = sp = None
+    y, total, q, scale = out or (None, None, None, None)
+    rp = tp = wp = yp = qp = sp = None
+    wcode = MSR_F32
     if residual is None:
         total = None
     else:
         rp = _expect("residual", residual, shape, dtype, dev)
         if total is None:
-            total = _new(shape, dtype, x.device)
+            total = tc.empty(shape, dtype=dtype, device=x.device)
         tp = _expect("sum", total, shape, dtype, dev)
-    wp, wcode = _weight(weight, d, dev)
+    if weight is not None:
+        wp, wcode = _weight(weight, d, dev)
     if want_y:
         if y is None:
-            y = _new(shape, dtype, x.device)
+            y = tc.empty(shape, dtype=dtype, device=x.device)
         yp = _expect("y", y, shape, dtype, dev)
     else:
         y = None
     if want_q:
-        torch = _torch()
-        lead, blocks = shape[:-1], (d + BLOCK - 1) // BLOCK
+        blocks = (d + 127) // BLOCK
+        qshape, sshape = (*shape[:-1], blocks * BLOCK), (*shape[:-1], blocks)
         if q is None:
-            q = _new(lead + (blocks * BLOCK,), torch.float8_e4m3fn, x.device)
+            q = tc.empty(qshape, dtype=tc.f8, device=x.device)
         if scale is None:
-            scale = _new(lead + (blocks,), torch.float32, x.device)
-        qp = _expect("q", q, lead + (blocks * BLOCK,), torch.float8_e4m3fn, dev)
-        sp = _expect("scale", scale, lead + (blocks,), torch.float32, dev)
+            scale = tc.empty(sshape, dtype=tc.f32, device=x.device)
+        qp = _expect("q", q, qshape, tc.f8, dev)
+        sp = _expect("scale", scale, sshape, tc.f32, dev)
     else:
         q = scale = None
-    s = (_lib or load()).msr_add_rmsnorm(math.prod(shape[:-1]), d, code, x.data_ptr(), rp, wp, wcode, eps, tp, yp, qp,
-                                         sp, _stream_of(dev, stream))
+    s = _lib.msr_add_rmsnorm(_rows(shape), d, code, x.data_ptr(), rp, wp, wcode, eps, tp, yp, qp, sp,
+                             tc.raw_stream(dev) if stream is None else stream.cuda_stream)
     if s:
         _check(s)
     return y, total, q, scale
@@ -453,31 +467,30 @@ def msr_add_rmsnorm_backward(h, weight, grad_y, *, grad_sum=None, eps=1e-6, want
     """Gradients of msr_add_rmsnorm: h = the forward call's sum (x when it had no residual), grad_y = dL/dn, grad_sum =
     dL/dsum or None, all [..., d] of one type.  Returns (dx, dweight or None): dx is the gradient of x and of the
     residual, in h's type; dweight is float32 [d].  out: tensors to write, in the same order."""
-    torch = _torch()
-    code, shape, dtype, dev = _code("h", h), h.shape, h.dtype, h.get_device()
-    d = shape[-1] if shape else 0
-    rows = math.prod(shape[:-1])
+    tc = _tc or _setup()
+    code = _code("h", h)
+    shape, dtype, dev = h.shape, h.dtype, h.get_device()
+    d, rows = shape[-1] if shape else 0, _rows(shape)
     gp = _expect("grad_y", grad_y, shape, dtype, dev)
     sp = None if grad_sum is None else _expect("grad_sum", grad_sum, shape, dtype, dev)
     wp, wcode = _weight(weight, d, dev)
-    dx, dw = (None, None) if out is None else out
+    dx, dw = out or (None, None)
     if dx is None:
-        dx = _new(shape, dtype, h.device)
+        dx = tc.empty(shape, dtype=dtype, device=h.device)
     xp, dwp, ws, n = _expect("dx", dx, shape, dtype, dev), None, None, 0
-    lib = _lib or load()
     if want_weight_grad:
         if dw is None:
-            dw = _new((d,), torch.float32, h.device)
-        dwp = _expect("dweight", dw, (d,), torch.float32, dev)
-        n = lib.msr_add_rmsnorm_backward_workspace(rows, d)
+            dw = tc.empty((d,), dtype=tc.f32, device=h.device)
+        dwp = _expect("dweight", dw, (d,), tc.f32, dev)
+        n = _lib.msr_add_rmsnorm_backward_workspace(rows, d)
         if n:
             if workspace is None or workspace.numel() < n:
-                workspace = _new(n, torch.uint8, h.device)
+                workspace = tc.empty(n, dtype=tc.u8, device=h.device)
             ws = workspace.data_ptr()
     else:
         dw = None
-    s = lib.msr_add_rmsnorm_backward(rows, d, code, h.data_ptr(), wp, wcode, eps, gp, sp, xp, dwp, ws, n,
-                                     _stream_of(dev, stream))
+    s = _lib.msr_add_rmsnorm_backward(rows, d, code, h.data_ptr(), wp, wcode, eps, gp, sp, xp, dwp, ws, n,
+                                      tc.raw_stream(dev) if stream is None else stream.cuda_stream)
     if s:
         _check(s)
     return dx, dw
@@ -489,67 +502,65 @@ def msr_quantize(x, *, block_rows=1, want_rows=True, want_transposed=False, out=
     counterpart.  block_rows 1: a float32 scale per 128 values of a row of the array written, scale [rows, P(cols) /
     128], scale_t [cols, P(rows) / 128]; block_rows 128: a scale per 128 x 128 square, [P(rows) / 128, P(cols) / 128]
     and its transpose.  out: tensors to write, in the same order."""
-    torch = _torch()
+    tc = _tc or _setup()
     code = _code("x", x)
     if x.dim() != 2:
         raise ValueError("x must be a matrix")
     (R, C), dev = x.shape, x.get_device()
-    q, sc, qt, st = (None, None, None, None) if out is None else out
-    f8, f32, rb, cb = torch.float8_e4m3fn, torch.float32, (R + BLOCK - 1) // BLOCK, (C + BLOCK - 1) // BLOCK
-    square = block_rows == BLOCK
+    q, sc, qt, st = out or (None, None, None, None)
+    rb, cb, square = (R + 127) // BLOCK, (C + 127) // BLOCK, block_rows == BLOCK
     qp = sp = qtp = stp = None
     if want_rows:
         shape = (rb if square else R, cb)
         if q is None:
-            q = _new((R, cb * BLOCK), f8, x.device)
+            q = tc.empty((R, cb * BLOCK), dtype=tc.f8, device=x.device)
         if sc is None:
-            sc = _new(shape, f32, x.device)
-        qp, sp = _expect("q", q, (R, cb * BLOCK), f8, dev), _expect("scale", sc, shape, f32, dev)
+            sc = tc.empty(shape, dtype=tc.f32, device=x.device)
+        qp, sp = _expect("q", q, (R, cb * BLOCK), tc.f8, dev), _expect("scale", sc, shape, tc.f32, dev)
     else:
         q = sc = None
     if want_transposed:
         shape = (cb if square else C, rb)
         if qt is None:
-            qt = _new((C, rb * BLOCK), f8, x.device)
+            qt = tc.empty((C, rb * BLOCK), dtype=tc.f8, device=x.device)
         if st is None:
-            st = _new(shape, f32, x.device)
-        qtp, stp = _expect("qt", qt, (C, rb * BLOCK), f8, dev), _expect("scale_t", st, shape, f32, dev)
+            st = tc.empty(shape, dtype=tc.f32, device=x.device)
+        qtp, stp = _expect("qt", qt, (C, rb * BLOCK), tc.f8, dev), _expect("scale_t", st, shape, tc.f32, dev)
     else:
         qt = st = None
-    s = (_lib or load()).msr_quantize(R, C, code, block_rows, x.data_ptr(), qp, sp, qtp, stp, _stream_of(dev, stream))
+    s = _lib.msr_quantize(R, C, code, block_rows, x.data_ptr(), qp, sp, qtp, stp,
+                          tc.raw_stream(dev) if stream is None else stream.cuda_stream)
     if s:
         _check(s)
     return q, sc, qt, st
 
 
-def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, workspace=None, stream=None):
+def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, stream=None):
     """a b^T of 8-bit operands with a scale for each block of 128: a [..., K] float8_e4m3fn with a_scale [..., K /
     128], b [N, K] with b_scale [N, K / 128] or, per 128 x 128 square, [P(N) / 128, K / 128] (float32; K a multiple
     of 128).  Returns [..., N] of out_dtype: bfloat16 (default) or float32."""
-    torch = _torch()
+    tc = _tc or _setup()
     if not (a.is_cuda and a.is_contiguous()) or not a.dim():
         raise ValueError("a must be a contiguous device tensor")
-    if a.dtype is not torch.float8_e4m3fn or b.dtype is not torch.float8_e4m3fn:
+    if a.dtype is not tc.f8 or b.dtype is not tc.f8:
         raise TypeError("a and b must be float8_e4m3fn")
-    lead, dev, f32 = a.shape[:-1], a.get_device(), torch.float32
-    k, n, m = a.shape[-1], b.shape[0] if b.dim() else 0, math.prod(lead)
+    shape, dev = a.shape, a.get_device()
+    lead, k, n, m = shape[:-1], shape[-1], b.shape[0] if b.dim() else 0, _rows(shape)
     kb = k // BLOCK
-    bp = _expect("b", b, (n, k), torch.float8_e4m3fn, dev)
-    ap = _expect("a_scale", a_scale, lead + (kb,), f32, dev)
+    bp = _expect("b", b, (n, k), tc.f8, dev)
+    ap = _expect("a_scale", a_scale, (*lead, kb), tc.f32, dev)
     rows = 1 if b_scale.shape == (n, kb) else BLOCK
-    sp = _expect("b_scale", b_scale, (n if rows == 1 else (n + BLOCK - 1) // BLOCK, kb), f32, dev)
+    sp = _expect("b_scale", b_scale, (n if rows == 1 else (n + 127) // BLOCK, kb), tc.f32, dev)
     if out is None:
-        out = _new(lead + (n,), out_dtype or torch.bfloat16, a.device)
-    code = _code("out", out)
-    op = _expect("out", out, lead + (n,), out_dtype or out.dtype, dev)
-    lib = _lib or load()
-    ws, wp = lib.msr_scaled_matmul_workspace(m, n, k, code), None
-    if ws:
-        if workspace is None or workspace.numel() < ws:
-            workspace = _new(ws, torch.uint8, a.device)
-        wp = workspace.data_ptr()
-    s = lib.msr_scaled_matmul(m, n, k, a.data_ptr(), ap, b.data_ptr(), sp, rows, code, op, wp, ws,
-                              _stream_of(dev, stream))
+        out = tc.empty((*lead, n), dtype=out_dtype or _torch().bfloat16, device=a.device)
+    elif out_dtype is None:
+        out_dtype = out.dtype
+    code = tc.codes.get(out.dtype)
+    if code is None:
+        raise TypeError(f"unsupported output dtype {out.dtype}; use float32 or bfloat16")
+    op = _expect("out", out, (*lead, n), out_dtype or out.dtype, dev)
+    s = _lib.msr_scaled_matmul(m, n, k, a.data_ptr(), ap, b.data_ptr(), sp, rows, code, op,
+                               tc.raw_stream(dev) if stream is None else stream.cuda_stream)
     if s:
         _check(s)
     return out

@@ -369,12 +369,10 @@ def test_graph_replays_match_the_eager_calls():
     x = torch.zeros(8, 2048, dtype=torch.bfloat16, device=dev)
     y = torch.empty(8, 1024, dtype=torch.bfloat16, device=dev)
     q, s = torch.empty(8, 2048, dtype=torch.float8_e4m3fn, device=dev), torch.empty(8, 16, device=dev)
-    n = msr.load().msr_scaled_matmul_workspace(8, 1024, 2048, msr.MSR_BF16)
-    ws = torch.empty(max(n, 1), dtype=torch.uint8, device=dev)
 
     def step():
         msr.msr_add_rmsnorm(x, want_y=False, want_q=True, out=(None, None, q, s))
-        msr.msr_scaled_matmul(q, s, qb, sb, out=y, workspace=ws)
+        msr.msr_scaled_matmul(q, s, qb, sb, out=y)
 
     step()
     torch.cuda.synchronize()
