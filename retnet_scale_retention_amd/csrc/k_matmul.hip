@@ -608,34 +608,39 @@ __global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_bod
 // Times of a kernel are close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
 // tile's latency, and the chip's throughput over T tiles, T rounded up to
 // whole rounds of the workgroups that run at once.  The constants (us) are
-// fits to its times over 1 .. 4096 tokens, 512 .. 8192 features and a
-// contraction of 512 .. 8192 (bf16 output; fp32 output in the second row),
-// e.g. tiles of 32 x 32 | 64 x 64 | 128 x 128 | 256 x 256:
-//   300 x 512 x 512        3.3 |   4.0 |   6.7 |  12.5 us
-//   777 x 2048 x 2048     18.7 |  11.7 |  14.6 |  28.6
-//   4096 x 2048 x 2048    76.7 |  38.9 |  24.5 |  31.8
-//   4096 x 8192 x 8192     904 |   566 |   297 |   231
+// fits to measured times over 1 .. 16384 tokens, 512 .. 8192 features and a
+// contraction of 256 .. 8192, for bf16 and for fp32 output.  Tiles of
+// 32 x 32 | 64 x 64 | 128 x 64 | 128 x 128 | 256 x 256, bf16 output, us:
+//   300 x 512 x 512        3.3 |   4.0 |   4.4 |   6.7 |  12.5
+//   300 x 4096 x 2048     12.8 |  10.7 |  10.0 |  13.7 |
+//   2000 x 1544 x 2048    27.0 |  19.7 |  13.5 |  14.6 |
+//   4096 x 2048 x 2048    61.1 |  37.7 |  29.8 |  23.6 |  31.8
+//   4096 x 8192 x 8192         |   566 |   432 |   297 |   231
 struct Fit {
-    int rows, round;
+    int rows, cols, round;
     double f0, f1, t0, t1;
 };
-constexpr Fit kFit[2][4] = {
-    {{32, 1, 2.8, 0.11, 0.0030, 0.000385}, {64, 1, 2.7, 0.23, 0.0025, 0.00104}, {128, 512, 3.5, 0.60, 0.010, 0.0021},
-     {256, 256, 6.0, 1.35, 0.035, 0.0065}},
-    {{32, 1, 2.7, 0.16, 0.0032, 0.000415}, {64, 1, 2.6, 0.42, 0.0037, 0.00108}, {128, 512, 2.6, 1.05, 0.012, 0.00346},
-     {}}};
+constexpr int kConfigs = 5;
+constexpr Fit kFit[2][kConfigs] = {{{32, 32, 1, 2.8, 0.15, 0.0016, 0.000365},
+                                    {64, 64, 1, 2.7, 0.23, 0.0033, 0.00097},
+                                    {128, 64, 1, 2.9, 0.36, 0.0075, 0.00140},
+                                    {128, 128, 512, 3.5, 0.60, 0.0115, 0.00205},
+                                    {256, 256, 256, 6.0, 1.35, 0.035, 0.0063}},
+                                   {{32, 32, 1, 2.7, 0.20, 0.0019, 0.00042},
+                                    {64, 64, 1, 2.6, 0.42, 0.0042, 0.00105},
+                                    {128, 64, 1, 2.8, 0.62, 0.0075, 0.00200},
+                                    {128, 128, 512, 2.6, 1.05, 0.012, 0.00346},
+                                    {}}};
 
 double fitted_us(const Fit &f, int64_t M, int64_t N, int64_t nkb) {
-    int64_t T = ((M + f.rows - 1) / f.rows) * ((N + f.rows - 1) / f.rows);
+    int64_t T = ((M + f.rows - 1) / f.rows) * ((N + f.cols - 1) / f.cols);
     T = (T + f.round - 1) / f.round * f.round;
     const double lone = f.f0 + f.f1 * nkb, chip = T * (f.t0 + f.t1 * nkb);
     return lone > chip ? lone : chip;
 }
 
 template <int BM, int BN, int KG, int WM, int WN, int ST, typename OUT, bool BROW>
-void launch_tile(MatArgs a, hipStream_t st) {
-    a.mt = (a.M + BM - 1) / BM;
-    a.nt = (a.N + BN - 1) / BN;
+void launch_tile(const MatArgs &a, hipStream_t st) {
     const unsigned grid = (unsigned)(((int64_t)a.mt * a.nt + 7) / 8 * 8);
     hipLaunchKernelGGL((matmul_tile_kernel<BM, BN, KG, WM, WN, ST, OUT, BROW>), dim3(grid), dim3(64 * KG * WM * WN), 0,
                        st, a);
@@ -644,28 +649,43 @@ void launch_tile(MatArgs a, hipStream_t st) {
 template <typename OUT, bool BROW>
 hipError_t matmul(MatArgs a, hipStream_t st) {
     constexpr bool wide = sizeof(OUT) == 4;
-    if (a.M <= 8 && a.nkb > 0) {
-        // few tokens: one 16-token operand per wave, B straight from memory (1 x 4096 x 4096: 4.6 us, 32 x 32 tiles 7.7;
-        // at 16 tokens the rows of A that every wave reads again tip it: 10.8 against 9.6 us for 512 x 8192)
+    if (a.M <= 8 && a.N <= 4096 && a.nkb > 0) {
+        // few tokens and no more workgroups than CUs: one 16-token operand per wave, B straight from memory
+        // (1 x 4096 x 4096: 4.6 us, 32 x 32 tiles 6.0; but 8 x 8192 x 8192 16.7 against 12.2, 16 x 4096 x 4096 6.8
+        // against 6.1: every wave reads A's rows again)
         hipLaunchKernelGGL((matmul_stream_kernel<1, 1, 8, OUT, BROW>), dim3((a.N + 15) / 16, 1), dim3(512), 0, st, a);
         return hipGetLastError();
     }
     int best = 0;
     double us = 1e30;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kConfigs; ++i) {
         // the large kernel: 32-bit offsets over the whole of A and B, blocks in pairs, 16-byte stores
-        if (i == 3 && (wide || BROW || a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
+        if (i == 4 && (wide || BROW || a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
                        (int64_t)(a.N + 256) * a.K > INT32_MAX || (int64_t)a.N * 512 > INT32_MAX))
             break;
         const double x = fitted_us(kFit[wide][i], a.M, a.N, a.nkb);
         if (x < us) us = x, best = i;
     }
-    if (best == 0) launch_tile<32, 32, 2, 2, 1, 4, OUT, BROW>(a, st);
-    else if (best == 1) launch_tile<64, 64, 1, 2, 2, 3, OUT, BROW>(a, st);
-    else if (best == 2) launch_tile<128, 128, 1, 2, 2, 2, OUT, BROW>(a, st);
-    else {
-        a.mt = (a.M + 255) / 256;
-        a.nt = (a.N + 255) / 256;
+    const Fit &f = kFit[wide][best];
+    a.mt = (a.M + f.rows - 1) / f.rows;
+    a.nt = (a.N + f.cols - 1) / f.cols;
+    // up to a tile per CU, a tile's own latency counts: two groups of waves share its blocks, or a third stage is loaded
+    // ahead (1 x 4096 x 4096: 6.0 against 8.1 us, 700 x 700 x 2048: 6.5 against 7.5); beyond, more workgroups per CU
+    // do (4096 x 2048 x 512: 32 x 32 23.9 against 35.6 us, 64 x 64 13.9 against 15.2)
+    const int64_t tiles = (int64_t)a.mt * a.nt;
+    const bool few = tiles <= 256;
+    if (best == 0) {
+        // (over a long contraction the second group pays for longer: 1336 x 320 x 5632, 420 tiles: 15.4 against 22.5 us)
+        if (few || (tiles <= 512 && a.nkb >= 24)) launch_tile<32, 32, 2, 2, 1, 4, OUT, BROW>(a, st);
+        else launch_tile<32, 32, 1, 2, 1, 4, OUT, BROW>(a, st);
+    } else if (best == 1) {
+        if (few) launch_tile<64, 64, 1, 2, 2, 3, OUT, BROW>(a, st);
+        else launch_tile<64, 64, 1, 2, 2, 2, OUT, BROW>(a, st);
+    } else if (best == 2) {
+        launch_tile<128, 64, 1, 2, 2, 2, OUT, BROW>(a, st);
+    } else if (best == 3) {
+        launch_tile<128, 128, 1, 2, 2, 2, OUT, BROW>(a, st);
+    } else {
         hipLaunchKernelGGL(matmul_big_kernel, dim3(256), dim3(512), 0, st, a);
     }
     return hipGetLastError();
