@@ -427,9 +427,9 @@ __global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
 //     an XCD share); without it the loads' latency showed (2.2 against 1.7 us
 //     per block).
 //   - After a lane swap every lane stores 16 bytes of a row.
-// 16384 x 8192 x 4096: 485 us = 2270 TFLOP/s.  Of its 1.6 us per block and
-// workgroup the products and folds alone take 1.15, with the reads of LDS and
-// the barrier but no loads 1.45 (each at the clock that it runs at); the
+// 16384 x 8192 x 4096: 485 us = 2270 TFLOP/s.  It is bound by the chip's power:
+// the same kernel over zeros takes 388 us, and its blocks without loads 1.05
+// us each, the products' own rate (1.6 with random bytes and all).  The
 // tiles' ends cost 70 us, 45 of them the 268 MB of results, which all
 // workgroups write at the same time.
 struct BigTile {

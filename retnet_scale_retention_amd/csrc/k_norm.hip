@@ -27,7 +27,7 @@ struct NormArgs {
     void *sum, *y;          // may be NULL
     uint8_t *q;             // may be NULL; [rows][dpad]
     float *qs;              // [rows][dpad / 128]
-    int64_t rows;
+    int64_t row0, rows;     // first row of this launch
     int d, dpad, w_bf16;
     float eps;
 };
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
     constexpr int TEAMS = W < 4 ? 4 / W : 1;
     __shared__ float red[TEAMS * W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tm = wave / W, w = wave % W;
-    const int64_t row_raw = (int64_t)blockIdx.x * TEAMS + tm;
+    const int64_t row_raw = a.row0 + (int64_t)blockIdx.x * TEAMS + tm;
     const bool live = row_raw < a.rows;
     const int64_t row = live ? row_raw : a.rows - 1;  // a team past the end repeats the last row and stores nothing
     const T *x = static_cast<const T *>(a.x) + row * a.d;
@@ -250,10 +250,15 @@ __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, floa
     float s[4] = {0.f, 0.f, 0.f, 0.f};
     if constexpr (VEC) {
         if (c < d)
-#pragma unroll 8
-            for (int p = sl; p < parts; p += 64) {
-                const float4 x = *reinterpret_cast<const float4 *>(part + (size_t)p * d + c);
-                s[0] += x.x, s[1] += x.y, s[2] += x.z, s[3] += x.w;
+            for (int p0 = sl; p0 < parts; p0 += 512) {  // eight loads at once, zeros past the last part
+                float4 x[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (p0 + 64 * u < parts) x[u] = *reinterpret_cast<const float4 *>(part + (size_t)(p0 + 64 * u) * d + c);
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) s[0] += x[u].x, s[1] += x[u].y, s[2] += x[u].z, s[3] += x[u].w;
             }
     } else {
         for (int p = sl; p < parts; p += 64)
@@ -292,26 +297,36 @@ hipError_t by_type(int dtype, bool vec, F f) {
 }
 
 // Workgroups of the backward pass: each writes one partial weight gradient.
+// At most 512, and about one per eight rows but no fewer than the CUs (few
+// rows: the parts' own bytes count), evened out so that all walk over equally
+// many rows.
 constexpr int kBackGroups = 512;
 
 int back_groups(int64_t rows, int d) {
-    const int teams = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;
-    const int64_t g = (rows + teams - 1) / teams;
-    const int64_t most = rows / 8 > 256 ? rows / 8 : 256;  // (few rows: the parts' own bytes count)
-    return (int)std::min<int64_t>(g, std::min<int64_t>(most, kBackGroups));
+    if (rows == 0) return 0;
+    const int64_t teams = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;  // as by_width's kernels have
+    const int64_t g = std::min<int64_t>((rows + teams - 1) / teams, std::min<int64_t>(std::max<int64_t>(rows / 8, 256), kBackGroups));
+    const int64_t turns = std::max<int64_t>((rows + g * teams / 2) / (g * teams), 1);
+    return (int)std::min<int64_t>((rows + turns * teams - 1) / (turns * teams), kBackGroups);
 }
 
 }  // namespace
 
 hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, const void *r, const void *w, int w_dtype,
                               float eps, void *sum, void *y, void *q, float *qs, hipStream_t st) {
-    const NormArgs a{x, r, w, sum, y, static_cast<uint8_t *>(q), qs, rows, d, (int)round128(d), w_dtype == MSR_BF16, eps};
+    NormArgs a{x, r, w, sum, y, static_cast<uint8_t *>(q), qs, 0, rows, d, (int)round128(d), w_dtype == MSR_BF16, eps};
     return by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
         return by_width(d, [&](auto W, auto V) {
             constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
-            hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(t), vec.value, W.value, V.value>),
-                               dim3((unsigned)((rows + teams - 1) / teams)), dim3(nt), 0, st, a);
-            return hipGetLastError();
+            constexpr int64_t most = (int64_t)1 << 21;  // workgroups of a launch: its threads stay below 2^32
+            hipError_t e = hipSuccess;
+            for (a.row0 = 0; a.row0 < rows && e == hipSuccess; a.row0 += most * teams) {
+                const int64_t g = std::min<int64_t>((rows - a.row0 + teams - 1) / teams, most);
+                hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(t), vec.value, W.value, V.value>), dim3((unsigned)g),
+                                   dim3(nt), 0, st, a);
+                e = hipGetLastError();
+            }
+            return e;
         });
     });
 }

@@ -17,22 +17,36 @@ struct QuantArgs {
     int tiles_c;
 };
 
-// Own order, blocks within a row: 16 lanes take a block, 8 values each.
+// Own order, blocks within a row: 16 lanes take a block, 8 values each, and
+// four blocks one after the other, loaded together.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
-    const int64_t blocks = a.R * (a.Cp / kBlock), per = (int64_t)gridDim.x * 16;
-    for (int64_t b0 = (int64_t)blockIdx.x * 16; b0 < blocks; b0 += per) {
-        const int64_t b_raw = b0 + (threadIdx.x >> 4), b = b_raw < blocks ? b_raw : blocks - 1;
-        const int64_t row = b / (a.Cp / kBlock), c = (b % (a.Cp / kBlock)) * kBlock + 8 * (threadIdx.x & 15);
+    constexpr int U = 4;
+    const uint32_t per_row = (uint32_t)(a.Cp / kBlock);
+    const int64_t first = (int64_t)blockIdx.x * (16 * U), row0 = first / per_row;  // the same for the workgroup
+    const uint32_t col0 = (uint32_t)(first - row0 * per_row);
+    Raw8<T, VEC> x[U];
+    int64_t row[U];
+    uint32_t blk[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const uint32_t at = col0 + 16 * u + (threadIdx.x >> 4);
+        row[u] = row0 + at / per_row;
+        blk[u] = at % per_row;
+        const int64_t c = (int64_t)blk[u] * kBlock + 8 * (threadIdx.x & 15);
+        x[u].load(static_cast<const T *>(a.x) + row[u] * a.C + c, row[u] < a.R ? (int)(a.C - c) : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
         float v[8];
-        load8<VEC>(static_cast<const T *>(a.x) + row * a.C + c, (int)(a.C - c), v);
+        x[u].get(v);
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
         const float sc = block_scale(row16_max(m));
-        if (b_raw < blocks) {
-            stream_out(a.q + row * a.Cp + c, pack8(v, sc));
-            if ((threadIdx.x & 15) == 0) a.s[b] = sc;
+        if (row[u] < a.R) {
+            stream_out(a.q + row[u] * a.Cp + (int64_t)blk[u] * kBlock + 8 * (threadIdx.x & 15), pack8(v, sc));
+            if ((threadIdx.x & 15) == 0) a.s[row[u] * per_row + blk[u]] = sc;
         }
     }
 }
@@ -55,11 +69,10 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 // stores that do not linger in L2 (59 -> 48 us).
 template <typename T, bool VEC, bool SQUARE>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
-    constexpr int LDT = 144;  // bytes between the rows of the transposed tile: 16-byte aligned, off the banks' period
     __shared__ __attribute__((aligned(16))) uint32_t cmax[4][128];
     __shared__ float cscale[128];
     __shared__ uint32_t tmax[4];
-    __shared__ __attribute__((aligned(16))) uint8_t tr[128 * LDT];
+    __shared__ __attribute__((aligned(16))) uint8_t tr[128 * 128];
     const int64_t tr_i = blockIdx.x / a.tiles_c, tc = blockIdx.x % a.tiles_c;
     const int64_t r0 = tr_i * 128, c0 = tc * 128;
     const int rg = threadIdx.x >> 4, cg = threadIdx.x & 15, wave = threadIdx.x >> 6;
@@ -141,14 +154,17 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
                 x[i].get(v);
                 col[i] = v[j];
             }
-            *reinterpret_cast<uint2 *>(tr + (8 * cg + j) * LDT + 8 * rg) = pack8(col, SQUARE ? square : cscale[8 * cg + j]);
+            // 8-byte pieces of a row XOR-swizzled by row / 8: the wave's 16 rows per store fall on different banks
+            *reinterpret_cast<uint2 *>(tr + (8 * cg + j) * 128 + 8 * (rg ^ cg)) =
+                pack8(col, SQUARE ? square : cscale[8 * cg + j]);
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int k = 32 * i + (int)(threadIdx.x >> 3), b = 16 * (threadIdx.x & 7);
-            if (c0 + k < a.C)
-                stream_out(a.qt + (c0 + k) * a.Rp + r0 + b, *reinterpret_cast<const uint4 *>(tr + k * LDT + b));
+            const int k = 32 * i + (int)(threadIdx.x >> 3), p = threadIdx.x & 7, x = k >> 3;
+            uint4 u = *reinterpret_cast<const uint4 *>(tr + k * 128 + 16 * (p ^ (x >> 1)));
+            if (x & 1) u = make_uint4(u.z, u.w, u.x, u.y);
+            if (c0 + k < a.C) stream_out(a.qt + (c0 + k) * a.Rp + r0 + 16 * p, u);
         }
     }
 }
@@ -156,8 +172,8 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
 template <typename T, bool VEC>
 hipError_t quantize(const QuantArgs &a, int block_rows, hipStream_t st) {
     if (block_rows == 1 && !a.qt) {
-        const int64_t g = (a.R * (a.Cp / kBlock) + 15) / 16;
-        hipLaunchKernelGGL((quantize_rows_kernel<T, VEC>), dim3((unsigned)(g < 16384 ? g : 16384)), dim3(256), 0, st, a);
+        const int64_t g = (a.R * (a.Cp / kBlock) + 63) / 64;
+        hipLaunchKernelGGL((quantize_rows_kernel<T, VEC>), dim3((unsigned)g), dim3(256), 0, st, a);
     } else {
         const unsigned tiles = (unsigned)(a.Rp / 128 * a.tiles_c);
         if (block_rows == 1)

@@ -250,6 +250,19 @@ def test_quantize_beyond_two_to_the_32():
     check_blocks(q2[-7:], s2[-7:], ol.add_rmsnorm(tf, None, None, EPS)[0], 1, 64 * U["f32"], "norm tail")
 
 
+def test_add_rmsnorm_more_rows_than_one_launch_takes():
+    torch, dev = torch_dev()
+    msr = _msr()
+    rows = (1 << 23) + 11  # launches of 2^21 workgroups of four rows
+    x = torch.zeros(rows, 8, dtype=torch.bfloat16, device=dev)
+    tail, tf = values(torch, dev, (29, 8), "bf16", 34)
+    x[-29:] = tail
+    y, _, q, s = msr.msr_add_rmsnorm(x, eps=EPS, want_q=True)
+    n = ol.add_rmsnorm(tf, None, None, EPS)[0]
+    assert np.all(np.abs(down(y[-29:]) - n) <= (64 * U["f32"] + U["bf16"]) * np.abs(n)) and not y[:-29].any()
+    check_blocks(q[-29:], s[-29:], n, 1, 64 * U["f32"], "tail")
+
+
 # m, n, k (padded): single tokens, ragged edges of every tile, one block and many
 MSIZES = [(1, 1, 128), (1, 64, 256), (2, 200, 1024), (5, 4096, 512), (16, 48, 384), (17, 130, 128), (33, 1000, 2048),
           (64, 256, 4096), (65, 257, 640), (100, 96, 16384), (127, 129, 256), (128, 512, 1152), (200, 72, 8192),
