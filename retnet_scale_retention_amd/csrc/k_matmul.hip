@@ -607,8 +607,7 @@ __global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_bod
 // ---- choice of a kernel -------------------------------------------------------
 // Times of a kernel are close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
 // tile's latency, and the chip's throughput over T tiles, T rounded up to
-// whole rounds of the workgroups that run at once.  The constants (us) are
-// fits to measured times over 1 .. 16384 tokens, 512 .. 8192 features and a
+// what fills the CUs evenly.  The constants (us) are fits to measured times over 1 .. 16384 tokens, 512 .. 8192 features and a
 // contraction of 256 .. 8192, for bf16 and for fp32 output.  Tiles of
 // 32 x 32 | 64 x 64 | 128 x 64 | 128 x 128 | 256 x 256, bf16 output, us:
 //   300 x 512 x 512        3.3 |   4.0 |   4.4 |   6.7 |  12.5
@@ -622,13 +621,13 @@ struct Fit {
 };
 constexpr int kConfigs = 5;
 constexpr Fit kFit[2][kConfigs] = {{{32, 32, 1, 2.8, 0.15, 0.0016, 0.000365},
-                                    {64, 64, 1, 2.7, 0.23, 0.0033, 0.00097},
-                                    {128, 64, 1, 2.9, 0.36, 0.0075, 0.00140},
+                                    {64, 64, 256, 2.7, 0.23, 0.0033, 0.00097},
+                                    {128, 64, 256, 2.9, 0.36, 0.0075, 0.00140},
                                     {128, 128, 512, 3.5, 0.60, 0.0115, 0.00205},
                                     {256, 256, 256, 6.0, 1.35, 0.035, 0.0063}},
                                    {{32, 32, 1, 2.7, 0.20, 0.0019, 0.00042},
-                                    {64, 64, 1, 2.6, 0.42, 0.0042, 0.00105},
-                                    {128, 64, 1, 2.8, 0.62, 0.0075, 0.00200},
+                                    {64, 64, 256, 2.6, 0.42, 0.0042, 0.00105},
+                                    {128, 64, 256, 2.8, 0.62, 0.0075, 0.00200},
                                     {128, 128, 512, 2.6, 1.05, 0.012, 0.00346},
                                     {}}};
 
@@ -676,13 +675,14 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
     const bool few = tiles <= 256;
     if (best == 0) {
         // (over a long contraction the second group pays for longer: 1336 x 320 x 5632, 420 tiles: 15.4 against 22.5 us)
-        if (few || (tiles <= 512 && a.nkb >= 24)) launch_tile<32, 32, 2, 2, 1, 4, OUT, BROW>(a, st);
+        if (few || (tiles <= 512 && a.nkb >= (wide ? 8 : 24))) launch_tile<32, 32, 2, 2, 1, 4, OUT, BROW>(a, st);
         else launch_tile<32, 32, 1, 2, 1, 4, OUT, BROW>(a, st);
     } else if (best == 1) {
         if (few) launch_tile<64, 64, 1, 2, 2, 3, OUT, BROW>(a, st);
         else launch_tile<64, 64, 1, 2, 2, 2, OUT, BROW>(a, st);
     } else if (best == 2) {
-        launch_tile<128, 64, 1, 2, 2, 2, OUT, BROW>(a, st);
+        if (few) launch_tile<128, 64, 1, 2, 2, 4, OUT, BROW>(a, st);
+        else launch_tile<128, 64, 1, 2, 2, 2, OUT, BROW>(a, st);
     } else if (best == 3) {
         launch_tile<128, 128, 1, 2, 2, 2, OUT, BROW>(a, st);
     } else {
