@@ -141,8 +141,8 @@ msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, con
     if (k % MSR_BLOCK) return set_error(MSR_ERR_SHAPE, "k=%lld must be a multiple of %d", (long long)k, MSR_BLOCK);
     if (b_block_rows != 1 && b_block_rows != MSR_BLOCK)
         return set_error(MSR_ERR_INVALID_ARG, "b_block_rows=%d is neither 1 nor %d", b_block_rows, MSR_BLOCK);
-    // the smallest tile is 32 x 32: its count has to fit the grid
-    if (((m + 31) / 32) * ((n + 31) / 32) > INT32_MAX / 64)
+    // the smallest tiles are 32 x 32, of 128 threads: a launch holds fewer than 2^32 threads
+    if (((m + 31) / 32) * ((n + 31) / 32) > (1 << 25) - 8)
         return set_error(MSR_ERR_SHAPE, "m=%lld x n=%lld is too large", (long long)m, (long long)n);
     if (m == 0 || n == 0) return MSR_OK;
     if (!out || (k > 0 && (!a || !a_scale || !b || !b_scale)))

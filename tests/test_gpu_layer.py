@@ -327,6 +327,70 @@ def test_scaled_matmul_positions(out):
             assert torch.equal(c.cpu(), want), (m, n, k, block)
 
 
+# the larger tiles: 64 x 64, 128 x 64 (four stages, two stages), 128 x 128, 256 x 256, each with ends inside a tile
+LSIZES = [(300, 6001, 512), (1025, 1990, 256), (250, 8184, 4096), (2040, 1545, 640), (4101, 4100, 512),
+          (2561, 2050, 1024), (3001, 4100, 256), (4010, 8200, 512), (8300, 8200, 1024)]
+
+
+def product64(qa, sa, qb, sb, block):
+    # the product and the sum of its terms' sizes in 64 bits on the card (these sizes are slow on the host)
+    import torch
+    a = qa.to(torch.float32).double() * sa.double().repeat_interleave(128, 1)
+    rows = sb if block == 1 else sb.repeat_interleave(128, 0)[:qb.shape[0]]
+    b = (qb.to(torch.float32).double() * rows.double().repeat_interleave(128, 1)).t().contiguous()
+    return a @ b, a.abs() @ b.abs()
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [128, 1])
+@pytest.mark.parametrize("m,n,k", LSIZES)
+def test_scaled_matmul_large_tiles(m, n, k, block, out):
+    torch, dev = torch_dev()
+    msr = _msr()
+    note(f"matmul {m}x{n}x{k} block {block} {out}")
+    ops = operands(torch, dev, msr, m, n, k, block, 53)
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    c = msr.msr_scaled_matmul(*ops, out_dtype=dt)
+    assert torch.equal(msr.msr_scaled_matmul(*ops, out_dtype=dt), c)
+    r, mag = product64(*ops, block)
+    d = (c.double() - r).abs()
+    if out == "f32":
+        assert bool((d <= (16 * k // 128 + 64) * U["f32"] * mag).all())
+    else:
+        assert bool((d <= U["bf16"] * r.abs() + 2.0 ** -10 * mag).all())
+        assert float(d.norm()) <= (U["bf16"] / np.sqrt(3) + 2.0 ** -12) * float(r.norm())
+
+
+@pytest.mark.parametrize("m,n,k", LSIZES)
+def test_scaled_matmul_large_tiles_positions(m, n, k):
+    # as above: sums of whole quarters that fp32 holds exactly, rounded once
+    torch, dev = torch_dev()
+    msr = _msr()
+    note(f"matmul positions {m}x{n}x{k}")
+    g = torch.Generator(device=dev).manual_seed(m)
+    pick = lambda *s: torch.randint(-1, 2, s, generator=g, device=dev).float()
+    qa, qb = pick(m, k).to(torch.float8_e4m3fn), pick(n, k).to(torch.float8_e4m3fn)
+    for block in (1, 128):
+        sa, sb = torch.exp2(pick(m, k // 128)), torch.exp2(pick(n if block == 1 else -(-n // 128), k // 128))
+        r, _ = product64(qa, sa, qb, sb, block)
+        for dt in (torch.float32, torch.bfloat16):
+            assert torch.equal(msr.msr_scaled_matmul(qa, sa, qb, sb, out_dtype=dt), r.float().to(dt)), (block, dt)
+
+
+@pytest.mark.parametrize("m,n,k", [(2040, 1545, 640), (2561, 2050, 1024), (4010, 8200, 512)])
+def test_scaled_matmul_large_tiles_non_finite(m, n, k):
+    torch, dev = torch_dev()
+    msr = _msr()
+    note(f"matmul non-finite {m}x{n}x{k}")
+    qa, sa, qb, sb = operands(torch, dev, msr, m, n, k, 128, 55)
+    clean = msr.msr_scaled_matmul(qa, sa, qb, sb)
+    sa[m - 1, 1], sa[m - 2, 0] = float("nan"), float("inf")
+    qb.view(torch.uint8)[n - 1, 5] = 0x7F
+    c = msr.msr_scaled_matmul(qa, sa, qb, sb)
+    assert torch.isnan(c[m - 1]).all() and torch.isnan(c[:, n - 1]).all() and not torch.isfinite(c[m - 2]).any()
+    assert torch.equal(c[:m - 2, :n - 1], clean[:m - 2, :n - 1])
+
+
 @pytest.mark.parametrize("m,n,k", [(3, 100, 384), (150, 300, 384)])
 def test_scaled_matmul_non_finite_blocks_stay_in_their_row_and_column(m, n, k):
     torch, dev = torch_dev()
