@@ -170,6 +170,15 @@ __device__ __forceinline__ bool tile_of(int block, int mt, int nt, int &tm, int 
 // arrays: the compiler then knows that reads of one do not wait for the loads
 // into the others (in one array it drained every load before each block's
 // first read: 787 us against 645 for 16384 x 8192 x 4096).
+// With fp32 output the vector instructions bind it: a bf16 matrix instruction
+// takes 8 cycles of a SIMD's issue and 16 of its matrix core, a vector
+// instruction 4.3, and at 128 x 128 (64 x 64 per wave) each matrix instruction
+// comes with two conversions and, B scaled by rows, a scale product and a
+// fold: 26 cycles at best, 30 measured (4096 x 4096 x 16384: 511 us = 1075
+// TFLOP/s, the clock at 1.94 GHz by the chip's power; without the
+// conversions 486 us, over zeros 433).  Reading the operands half a block
+// ahead, or spreading all vector work evenly between the matrix
+// instructions, changed nothing (539, 543 us).
 template <int BM, int BN, int KG, int WM, int WN, int ST, typename OUT, bool BROW>
 __device__ __forceinline__ void tile_body(const MatArgs &a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -311,8 +320,13 @@ __global__ __launch_bounds__(64 * KG * WM * WN) void matmul_tile_kernel(MatArgs 
     tile_body<BM, BN, KG, WM, WN, ST, OUT, BROW>(a);
 }
 
-// A few tokens against all of B (a decode step): B is read once, straight into registers.  A workgroup of KW waves takes
-// 16 NT features and up to 16 MT tokens; the waves split the contraction's blocks and their sums meet in LDS.
+// A few tokens against all of B (a decode step): B is read once, straight
+// into registers, two blocks at a time.  A workgroup of KW waves takes 16 NT
+// features and up to 16 MT tokens; the waves split the contraction's blocks
+// and their sums meet in LDS, so that 4096 features already give 256
+// workgroups with 2048 waves' loads under way.  1 x 4096 x 4096: 4.6 us, of
+// which 17 MB at the caches' 7.2 TB/s are 2.3 and a launch's start and end
+// most of the rest (32 x 32 tiles: 6.0).
 template <int MT, int NT, int KW, typename OUT, bool BROW>
 __device__ __forceinline__ void stream_body(const MatArgs &a) {
     constexpr int COLS = 16 * NT, LD = COLS + 4;
@@ -405,7 +419,6 @@ template <int MT, int NT, int KW, typename OUT, bool BROW>
 __global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
     stream_body<MT, NT, KW, OUT, BROW>(a);
 }
-
 
 // The whole chip on a large product (bf16 output, B scaled in squares).  256
 // workgroups of 8 waves, one per CU, each walk over 256 x 256 tiles; a wave
@@ -605,30 +618,47 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
 __global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_body(a); }
 
 // ---- choice of a kernel -------------------------------------------------------
-// Times of a kernel are close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
+// A kernel's time is close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
 // tile's latency, and the chip's throughput over T tiles, T rounded up to
-// what fills the CUs evenly.  The constants (us) are fits to measured times over 1 .. 16384 tokens, 512 .. 8192 features and a
-// contraction of 256 .. 8192, for bf16 and for fp32 output.  Tiles of
-// 32 x 32 | 64 x 64 | 128 x 64 | 128 x 128 | 256 x 256, bf16 output, us:
-//   300 x 512 x 512        3.3 |   4.0 |   4.4 |   6.7 |  12.5
-//   300 x 4096 x 2048     12.8 |  10.7 |  10.0 |  13.7 |
-//   2000 x 1544 x 2048    27.0 |  19.7 |  13.5 |  14.6 |
-//   4096 x 2048 x 2048    61.1 |  37.7 |  29.8 |  23.6 |  31.8
-//   4096 x 8192 x 8192         |   566 |   432 |   297 |   231
+// what fills the CUs evenly.  The constants (us) are least-squares fits to
+// times over 330 random sizes (9 .. 8192 tokens, 128 .. 16384 features, a
+// contraction of 256 .. 16384), for bf16 and for fp32 output; taking the
+// smallest costs 1.5% (1.0%) over the best kernel of each size, and 2.3% over
+// 160 other sizes.  Groups of waves that share a tile's blocks, and stages
+// further ahead, pay where there are few tiles; small LDS, so more workgroups
+// per CU, where there are many.  Times in us, bf16 output (32 x 32 by four groups | by one | 32 x 64
+// | 64 x 64 by two | by one | 128 x 64 | 128 x 128 | 128 x 64 with four
+// stages | 256 x 256):
+//   64 x 4096 x 4096        6.0 |  8.5 |  7.8 | 10.3 |      |      |      | 15.0 |
+//   64 x 8192 x 4096       12.5 | 11.0 |  8.9 | 11.8 |      |      |      | 16.5 |
+//   100 x 8192 x 4096      20.5 | 16.1 | 12.5 | 11.8 |      |      |      | 16.9 |
+//   256 x 8192 x 4096      44.9 | 33.4 | 24.6 | 22.9 | 22.5 | 25.9 | 27.9 | 19.4 |  47
+//   4096 x 2048 x 2048      112 |   62 |   51 |   51 |   38 |   30 |   24 |   38 |  31
+//   4096 x 4096 x 4096      338 |  220 |  167 |  162 |  134 |  105 |   84 |  136 |  67
+//   16384 x 8192 x 4096    2620 | 1740 | 1320 | 1290 | 1040 |  868 |  648 | 1070 | 481
 struct Fit {
     int rows, cols, round;
     double f0, f1, t0, t1;
 };
-constexpr int kConfigs = 5;
-constexpr Fit kFit[2][kConfigs] = {{{32, 32, 1, 2.8, 0.15, 0.0016, 0.000365},
-                                    {64, 64, 256, 2.7, 0.23, 0.0033, 0.00097},
-                                    {128, 64, 256, 2.9, 0.36, 0.0075, 0.00140},
-                                    {128, 128, 512, 3.5, 0.60, 0.0115, 0.00205},
-                                    {256, 256, 256, 6.0, 1.35, 0.035, 0.0063}},
-                                   {{32, 32, 1, 2.7, 0.20, 0.0019, 0.00042},
-                                    {64, 64, 256, 2.6, 0.42, 0.0042, 0.00105},
-                                    {128, 64, 256, 2.8, 0.62, 0.0075, 0.00200},
-                                    {128, 128, 512, 2.6, 1.05, 0.012, 0.00346},
+// the last two are for bf16 output alone
+constexpr int kConfigs = 9;
+constexpr Fit kFit[2][kConfigs] = {{{32, 32, 256, 3.08, 0.0944, 0.00831, 0.000428},
+                                    {32, 32, 512, 2.61, 0.197, 0.00227, 0.000393},
+                                    {32, 64, 256, 2.94, 0.164, 0.0056, 0.000595},
+                                    {64, 64, 256, 3.36, 0.222, 0.00967, 0.00102},
+                                    {64, 64, 256, 2.69, 0.282, 0.00414, 0.001},
+                                    {128, 64, 256, 2.46, 0.546, 0.00666, 0.00152},
+                                    {128, 128, 256, 3.99, 0.709, 0.0138, 0.00211},
+                                    {128, 64, 256, 3.38, 0.446, 0.0118, 0.00174},
+                                    {256, 256, 256, 5.5, 1.25, 0.027, 0.0068}},
+                                   {{32, 32, 256, 3.04, 0.131, 0.00832, 0.000587},
+                                    {32, 32, 512, 2.24, 0.412, 0.00238, 0.000517},
+                                    {32, 64, 256, 2.98, 0.264, 0.00576, 0.000851},
+                                    {64, 64, 256, 3.41, 0.390, 0.0116, 0.00152},
+                                    {64, 64, 256, 2.89, 0.457, 0.00287, 0.00139},
+                                    {128, 64, 256, 3.07, 0.737, 0.00724, 0.00223},
+                                    {128, 128, 256, 5.43, 1.06, 0.0122, 0.00384},
+                                    {},
                                     {}}};
 
 double fitted_us(const Fit &f, int64_t M, int64_t N, int64_t nkb) {
@@ -657,9 +687,9 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
     }
     int best = 0;
     double us = 1e30;
-    for (int i = 0; i < kConfigs; ++i) {
+    for (int i = 0; i < (wide ? kConfigs - 2 : kConfigs); ++i) {
         // the large kernel: 32-bit offsets over the whole of A and B, blocks in pairs, 16-byte stores
-        if (i == 4 && (wide || BROW || a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
+        if (i == 8 && (BROW || a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
                        (int64_t)(a.N + 256) * a.K > INT32_MAX || (int64_t)a.N * 512 > INT32_MAX))
             break;
         const double x = fitted_us(kFit[wide][i], a.M, a.N, a.nkb);
@@ -668,25 +698,22 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
     const Fit &f = kFit[wide][best];
     a.mt = (a.M + f.rows - 1) / f.rows;
     a.nt = (a.N + f.cols - 1) / f.cols;
-    // up to a tile per CU, a tile's own latency counts: two groups of waves share its blocks, or a third stage is loaded
-    // ahead (1 x 4096 x 4096: 6.0 against 8.1 us, 700 x 700 x 2048: 6.5 against 7.5); beyond, more workgroups per CU
-    // do (4096 x 2048 x 512: 32 x 32 23.9 against 35.6 us, 64 x 64 13.9 against 15.2)
-    const int64_t tiles = (int64_t)a.mt * a.nt;
-    const bool few = tiles <= 256;
-    if (best == 0) {
-        // (over a long contraction the second group pays for longer: 1336 x 320 x 5632, 420 tiles: 15.4 against 22.5 us)
-        if (few || (tiles <= 512 && a.nkb >= (wide ? 8 : 24))) launch_tile<32, 32, 2, 2, 1, 4, OUT, BROW>(a, st);
-        else launch_tile<32, 32, 1, 2, 1, 4, OUT, BROW>(a, st);
-    } else if (best == 1) {
-        if (few) launch_tile<64, 64, 1, 2, 2, 3, OUT, BROW>(a, st);
-        else launch_tile<64, 64, 1, 2, 2, 2, OUT, BROW>(a, st);
-    } else if (best == 2) {
-        if (few) launch_tile<128, 64, 1, 2, 2, 4, OUT, BROW>(a, st);
-        else launch_tile<128, 64, 1, 2, 2, 2, OUT, BROW>(a, st);
-    } else if (best == 3) {
-        launch_tile<128, 128, 1, 2, 2, 2, OUT, BROW>(a, st);
-    } else {
-        hipLaunchKernelGGL(matmul_big_kernel, dim3(256), dim3(512), 0, st, a);
+    switch (best) {
+        case 0: launch_tile<32, 32, 4, 2, 1, 3, OUT, BROW>(a, st); break;
+        case 1: launch_tile<32, 32, 1, 2, 1, 4, OUT, BROW>(a, st); break;
+        case 2: launch_tile<32, 64, 2, 1, 2, 3, OUT, BROW>(a, st); break;
+        case 3: launch_tile<64, 64, 2, 2, 2, 3, OUT, BROW>(a, st); break;
+        case 4: launch_tile<64, 64, 1, 2, 2, 2, OUT, BROW>(a, st); break;
+        case 5: launch_tile<128, 64, 1, 2, 2, 2, OUT, BROW>(a, st); break;
+        case 6: launch_tile<128, 128, 1, 2, 2, 2, OUT, BROW>(a, st); break;
+        default:
+            if constexpr (!wide) {
+                if (best == 7) {
+                    launch_tile<128, 64, 1, 2, 2, 4, OUT, BROW>(a, st);
+                    break;
+                }
+            }
+            if constexpr (!wide && !BROW) hipLaunchKernelGGL(matmul_big_kernel, dim3(256), dim3(512), 0, st, a);
     }
     return hipGetLastError();
 }

@@ -117,9 +117,10 @@ struct NormBackArgs {
 };
 
 // Each team walks over rows team, team + teams, ... with the next row's loads
-// under way (where the registers allow), and keeps the weight and its gradient over those rows in
-// registers (as loaded: held as floats across the barrier, 512 workgroups
-// took 118 us instead of 101 for 16384 x 4096; without the loads ahead 216);
+// under way (where the registers allow), and keeps the weight and its
+// gradient over those rows in registers (the row's values as loaded: held as
+// floats across the barrier, 512 workgroups took 118 us instead of 101 for
+// 16384 x 4096; without the loads ahead 216);
 // the workgroup's teams add up in LDS, its sum goes to `part`, and
 // column_sum_kernel adds the parts in a fixed order (no atomics).
 template <typename T, bool VEC, int W, int V>
