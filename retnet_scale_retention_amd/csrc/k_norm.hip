@@ -132,6 +132,10 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
     const int64_t team = (int64_t)blockIdx.x * TEAMS + tm, teams = (int64_t)gridDim.x * TEAMS;
     const int64_t turns = (a.rows + teams - 1) / teams;  // the same for every team: the barriers match
     const int e0 = 8 * (64 * w + lane);                  // group v starts at e0 + 512 W v
+    // the longest rows are read a second time instead of kept, and their weight gradient stays in LDS (all in registers,
+    // 276 of them spilled: 1024 x 32768 bf16 231 us)
+    constexpr bool keep = W * V <= 32;
+    __shared__ __attribute__((aligned(16))) float4 dwl[keep ? 1 : 128 * W * V];
     Raw8<T, VEC> hr[V], gr[V], dr[V];
     auto fetch = [&](int64_t t) {  // past the last row: that row again, not used
         const int64_t r = t * teams + team, row = r < a.rows ? r : a.rows - 1;
@@ -143,27 +147,41 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
             if (a.dsum) dr[v].load(static_cast<const T *>(a.dsum) + row * a.d + e, a.d - e);
         }
     };
-    constexpr bool early = V * (VEC ? sizeof(T) : 4) <= 8;
+    constexpr bool early = keep && V * (VEC ? sizeof(T) : 4) <= 8;
     float wt[V][8], dw[V][8];
-    fetch(0);
+    if (keep) fetch(0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = e0 + 512 * W * v;
-        load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
+        if constexpr (keep) {
+            load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+            for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
+        } else {
+            dwl[64 * (2 * (v * W + w)) + lane] = dwl[64 * (2 * (v * W + w) + 1) + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
     }
     const float inv_d = 1.f / (float)a.d;
     for (int64_t t = 0; t < turns; ++t) {
         const int64_t row = t * teams + team;
+        const int64_t at = (row < a.rows ? row : a.rows - 1) * a.d;
         Raw8<T, VEC> hc[V], gc[V], dc[V];
+        if constexpr (keep) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) hc[v] = hr[v], gc[v] = gr[v], dc[v] = dr[v];
+            for (int v = 0; v < V; ++v) hc[v] = hr[v], gc[v] = gr[v], dc[v] = dr[v];
+        }
         if (early && t + 1 < turns) fetch(t + 1);
         float ss = 0.f, gh = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             float h[8], g[8];
+            if constexpr (!keep) {
+                const int e = e0 + 512 * W * v;
+                __builtin_amdgcn_sched_barrier(0);  // a group's loads at a time
+                hc[v].load(static_cast<const T *>(a.h) + at + e, a.d - e);
+                gc[v].load(static_cast<const T *>(a.dy) + at + e, a.d - e);
+                load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
+            }
             hc[v].get(h);
             gc[v].get(g);
 #pragma unroll
@@ -198,8 +216,16 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
         for (int v = 0; v < V; ++v) {
             const int e = e0 + 512 * W * v;
             float h[8], g[8], ds[8], o[8];
-            hc[v].forget();
-            gc[v].forget();
+            if constexpr (keep) {
+                hc[v].forget();
+                gc[v].forget();
+            } else {
+                __builtin_amdgcn_sched_barrier(0);
+                hc[v].load(static_cast<const T *>(a.h) + at + e, a.d - e);
+                gc[v].load(static_cast<const T *>(a.dy) + at + e, a.d - e);
+                if (a.dsum) dc[v].load(static_cast<const T *>(a.dsum) + at + e, a.d - e);
+                load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
+            }
             hc[v].get(h);
             gc[v].get(g);
             if (a.dsum) {
@@ -211,11 +237,23 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 o[i] = fmaf(rstd, g[i] * wt[v][i] - h[i] * c, ds[i]);
-                dw[v][i] = fmaf(g[i], h[i] * rstd, dw[v][i]);
+                if constexpr (keep) dw[v][i] = fmaf(g[i], h[i] * rstd, dw[v][i]);
+            }
+            if constexpr (!keep) {
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {  // this lane's own numbers: no barrier
+                    float4 &x = dwl[64 * (2 * (v * W + w) + b) + lane];
+                    float4 y = x;
+                    y.x = fmaf(g[4 * b], h[4 * b] * rstd, y.x);
+                    y.y = fmaf(g[4 * b + 1], h[4 * b + 1] * rstd, y.y);
+                    y.z = fmaf(g[4 * b + 2], h[4 * b + 2] * rstd, y.z);
+                    y.w = fmaf(g[4 * b + 3], h[4 * b + 3] * rstd, y.w);
+                    x = y;
+                }
             }
             store8<VEC>(static_cast<T *>(a.dx) + row * a.d + e, a.d - e, o);
         }
-        if (!early && t + 1 < turns) fetch(t + 1);
+        if (keep && !early && t + 1 < turns) fetch(t + 1);
     }
     if (a.part) {
         if constexpr (TEAMS > 1) {
@@ -237,7 +275,13 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = e0 + 512 * W * v;
-            store8<VEC>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, dw[v]);
+            if constexpr (!keep) {
+                const float4 x = dwl[64 * (2 * (v * W + w)) + lane], y = dwl[64 * (2 * (v * W + w) + 1) + lane];
+                const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+                store8<VEC>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, z);
+            } else {
+                store8<VEC>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, dw[v]);
+            }
         }
     }
 }
@@ -279,14 +323,20 @@ __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, floa
     }
 }
 
-template <typename F>
+// (waves, groups per lane) that hold a row of d <= 512 W V values.  Twice the
+// waves with one group each (ONE) suit the gradients (16384 x 4096: 93 us
+// against 98, f32 16384 x 2048 94 against 101) and f32 forwards (77 against
+// 79), whose lanes have 32 bytes of each array under way all the same; bf16
+// forwards want two (70 against 76).
+template <bool ONE, typename F>
 hipError_t by_width(int d, F f) {
-    // (waves, groups per lane) that hold a row of d <= 512 W V values
+    constexpr int m = ONE ? 2 : 1;
+    using V = std::integral_constant<int, 2 / m>;
     if (d <= 512) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    if (d <= 1024) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 2>());
-    if (d <= 2048) return f(std::integral_constant<int, 2>(), std::integral_constant<int, 2>());
-    if (d <= 4096) return f(std::integral_constant<int, 4>(), std::integral_constant<int, 2>());
-    if (d <= 8192) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 2>());
+    if (d <= 1024) return f(std::integral_constant<int, m>(), V());
+    if (d <= 2048) return f(std::integral_constant<int, 2 * m>(), V());
+    if (d <= 4096) return f(std::integral_constant<int, 4 * m>(), V());
+    if (d <= 8192) return f(std::integral_constant<int, 8 * m>(), V());
     if (d <= 16384) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 4>());
     return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
 }
@@ -298,15 +348,18 @@ hipError_t by_type(int dtype, bool vec, F f) {
 }
 
 // Workgroups of the backward pass: each writes one partial weight gradient.
-// At most 512, and about one per eight rows but no fewer than the CUs (few
-// rows: the parts' own bytes count), evened out so that all walk over equally
-// many rows.
+// At most 512 of them where a workgroup's rows are up to 4 KiB, 256 where
+// they are longer: about 6 MB under way in both cases (512 x bf16: 43 us
+// against 52 for 65536 rows, but 4096 x bf16 100 against 93 for 16384); about
+// one per eight rows but no fewer than the CUs (few rows: the parts' own bytes
+// count), evened out so that all walk over equally many rows.
 constexpr int kBackGroups = 512;
 
-int back_groups(int64_t rows, int d) {
+int back_groups(int64_t rows, int d, int dtype) {
     if (rows == 0) return 0;
-    const int64_t teams = d <= 1024 ? 4 : d <= 2048 ? 2 : 1;  // as by_width's kernels have
-    const int64_t g = std::min<int64_t>((rows + teams - 1) / teams, std::min<int64_t>(std::max<int64_t>(rows / 8, 256), kBackGroups));
+    const int64_t teams = d <= 512 ? 4 : d <= 1024 ? 2 : 1;  // as by_width's kernels have
+    const int64_t most = teams * d * (dtype == MSR_BF16 ? 2 : 4) <= 4096 ? kBackGroups : kBackGroups / 2;
+    const int64_t g = std::min<int64_t>((rows + teams - 1) / teams, std::min<int64_t>(std::max<int64_t>(rows / 8, 256), most));
     const int64_t turns = std::max<int64_t>((rows + g * teams / 2) / (g * teams), 1);
     return (int)std::min<int64_t>((rows + turns * teams - 1) / (turns * teams), kBackGroups);
 }
@@ -317,7 +370,7 @@ hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, con
                               float eps, void *sum, void *y, void *q, float *qs, hipStream_t st) {
     NormArgs a{x, r, w, sum, y, static_cast<uint8_t *>(q), qs, 0, rows, d, (int)round128(d), w_dtype == MSR_BF16, eps};
     return by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
-        return by_width(d, [&](auto W, auto V) {
+        return by_width<sizeof(t) == 4>(d, [&](auto W, auto V) {
             constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
             constexpr int64_t most = (int64_t)1 << 21;  // workgroups of a launch: its threads stay below 2^32
             hipError_t e = hipSuccess;
@@ -332,14 +385,17 @@ hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, con
     });
 }
 
-size_t rmsnorm_backward_workspace(int64_t rows, int d) { return (size_t)back_groups(rows, d) * d * sizeof(float); }
+// enough for either type
+size_t rmsnorm_backward_workspace(int64_t rows, int d) {
+    return (size_t)std::max(back_groups(rows, d, MSR_BF16), back_groups(rows, d, MSR_F32)) * d * sizeof(float);
+}
 
 hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h, const void *w, int w_dtype, float eps,
                                    const void *dy, const void *dsum, void *dx, float *dw, float *part, hipStream_t st) {
-    const int parts = back_groups(rows, d);
+    const int parts = back_groups(rows, d, dtype);
     const NormBackArgs a{h, w, dy, dsum, dx, dw ? part : nullptr, rows, d, w_dtype == MSR_BF16, eps};
     hipError_t e = parts == 0 ? hipSuccess : by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
-        return by_width(d, [&](auto W, auto V) {
+        return by_width<true>(d, [&](auto W, auto V) {
             constexpr int nt = W.value < 4 ? 256 : 64 * W.value;
             hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), vec.value, W.value, V.value>), dim3(parts),
                                dim3(nt), 0, st, a);
