@@ -420,12 +420,12 @@ __global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
     stream_body<MT, NT, KW, OUT, BROW>(a);
 }
 
-// The whole chip on a large product (bf16 output, B scaled in squares).  256
-// workgroups of 8 waves, one per CU, each walk over 256 x 256 tiles; a wave
-// holds 64 tokens x 128 features of the tile as 4 x 8 results (128
-// registers).  Two LDS stages of a block (64 KiB each), filled by direct
-// loads; the sequence of blocks runs on over the tiles' ends, so a tile's
-// first blocks are under way while the last one's results are stored.
+// The whole chip on a large product (bf16 output).  256 workgroups of 8
+// waves, one per CU, each walk over 256 x 256 tiles; a wave holds 64 tokens x
+// 128 features of the tile as 4 x 8 results (128 registers).  Two LDS stages
+// of a block (64 KiB each), filled by direct loads; the sequence of blocks
+// runs on over the tiles' ends, so a tile's first blocks are under way while
+// the last one's results are stored.
 //   - A block is worked off in four phases of two column tiles.  Each phase
 //     starts by reading the next phase's operands into registers, and the
 //     last phase the next block's A; the one barrier of a block stands before
@@ -438,17 +438,21 @@ __global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
 //     waves) or pulls lines three blocks ahead into the XCD's L2 (the others:
 //     a quarter of A's rows and an eighth of B's, which the 32 workgroups of
 //     an XCD share); without it the loads' latency showed (2.2 against 1.7 us
-//     per block).
+//     per block).  With B scaled by rows every wave does both, scales (A's or
+//     B's) and lines.
 //   - After a lane swap every lane stores 16 bytes of a row.
 // 16384 x 8192 x 4096: 485 us = 2270 TFLOP/s.  It is bound by the chip's power:
 // the same kernel over zeros takes 388 us, and its blocks without loads 1.05
 // us each, the products' own rate (1.6 with random bytes and all).  The
 // tiles' ends cost 70 us, 45 of them the 268 MB of results, which all
-// workgroups write at the same time.
+// workgroups write at the same time.  With B scaled by rows 625 us (128 x 128
+// tiles 732): the scales' products double the vector instructions, which then
+// take longer than the matrix instructions beside them.
 struct BigTile {
     int m0, n0, share;  // share: first of the rows whose lines this wave pulls into L2
 };
 
+template <bool BROW>
 __device__ __forceinline__ void big_body(const MatArgs &a) {
     constexpr int BM = 256, BN = 256, NW = 8, TM = 4, TN = 8, LAG = 2, AHEAD = 3;
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -456,7 +460,12 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     __shared__ __attribute__((aligned(1024))) char As1[BM * 128];
     __shared__ __attribute__((aligned(1024))) char Bs0[BN * 128];
     __shared__ __attribute__((aligned(1024))) char Bs1[BN * 128];
-    __shared__ float Ss[5][BM];  // a ring of four blocks' scales, and the place where the L2 loads' bytes go
+    constexpr int SR = BROW ? BM + BN : BM, X = BROW ? 2 : 1;  // scales of a block; extra loads of a wave
+    // a ring of blocks' scales (A's, and B's by rows, which slower waves still read in a block's last phase when others
+    // load three blocks ahead), and the place where the L2 loads' bytes go
+    constexpr int RING = BROW ? 8 : 4;
+    __shared__ __attribute__((aligned(16))) float Ss[RING][SR];
+    __shared__ float sink[64];
 
     const int total = a.mt * a.nt, per = (total + 7) / 8, xcd = blockIdx.x % 8, slots = gridDim.x / 8;
     const int tend = min(per, total - xcd * per);
@@ -466,7 +475,7 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     const int K = a.K, nkb = a.nkb;
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int l16 = lane & 15, g = lane >> 4, ar = wv / 2 * 64, br = wv % 2 * 128;
-    const bool scales = wv < 4, pulls_a = wv < 6;
+    const bool scales = !BROW && wv < 4, pulls_a = BROW ? (wv & 2) == 0 : wv < 6;
 
     // as tile_of, for tile tt of this XCD's range
     auto big_tile = [&](int tt) __attribute__((always_inline)) {
@@ -477,13 +486,21 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     const auto ra = rsrc(a.a, (uint32_t)((size_t)a.M * K)), rb = rsrc(a.b, (uint32_t)((size_t)a.N * K));
     const auto rx = scales ? rsrc(a.sa, (uint32_t)((size_t)a.M * nkb * 4)) : pulls_a ? ra : rb;
     const int vo = 8 * wv * K + swizzled_source(lane, wv, K);
-    const int xo = scales ? (64 * wv + lane) * nkb * 4
-                          : (pulls_a ? 32 * (wv & 1) + (lane & 31) : 16 * (wv & 1) + (lane & 15)) * K;
+    int xo = scales ? (64 * wv + lane) * nkb * 4
+                    : (pulls_a ? 32 * (wv & 1) + (lane & 31) : 16 * (wv & 1) + (lane & 15)) * K;
+    if (BROW) {
+        const int part = (wv & 1) + (wv >> 2) * 2;  // of four waves
+        xo = (pulls_a ? 16 * part + (lane & 15) : 8 * part + (lane & 7)) * K;
+    }
+    const auto ry = wv < 4 ? rsrc(a.sa, (uint32_t)((size_t)a.M * nkb * 4)) : rsrc(a.sb, (uint32_t)((size_t)a.N * nkb * 4));
+    const int yo = (64 * (wv & 3) + lane) * nkb * 4;
     const int xstep = scales ? 4 : 128, xahead = scales ? 2 : AHEAD;
     auto xbase = [&](const BigTile &x) __attribute__((always_inline)) {
         return scales ? x.m0 * nkb * 4 : ((pulls_a ? x.m0 : x.n0) + x.share) * K;
     };
-    auto sbase = [&](const BigTile &x) __attribute__((always_inline)) { return (min(x.n0 + br, a.N - 1) >> 7) * nkb; };
+    auto sbase = [&](const BigTile &x) __attribute__((always_inline)) {
+        return BROW ? (wv < 4 ? x.m0 : x.n0) * nkb * 4 : (min(x.n0 + br, a.N - 1) >> 7) * nkb;
+    };
 
     // byte offsets of this tile's and the next one's A, B, extra loads and B scales
     BigTile cur = big_tile(t), nxt = big_tile(min(t + slots, tend - 1));
@@ -503,7 +520,12 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     auto extra = [&](int kb, int gs) __attribute__((always_inline)) {
         const int kk = max(kb + xahead, 0);
         const bool over = kk >= nkb;
-        float *dst = scales ? &Ss[(gs + 2) & 3][64 * wv] : Ss[4];
+        float *dst = scales ? &Ss[(gs + 2) & (RING - 1)][64 * wv] : sink;
+        if constexpr (BROW) {
+            const int ks = max(kb + 2, 0);
+            const bool past = ks >= nkb;
+            load_lds4(ry, reinterpret_cast<char *>(&Ss[(gs + 2) & (RING - 1)][64 * wv]), yo, (past ? s1 : s0) + (past ? ks - nkb : ks) * 4);
+        }
         load_lds4(rx, reinterpret_cast<char *>(dst), xo, (over ? x1 : x0) + (over ? kk - nkb : kk) * xstep);
     };
     const LaneRow rows(lane);
@@ -524,7 +546,7 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     for (int i = 0; i < 4; ++i) issue(1, As1, Bs1, i);
     Frag fa[TM], fb[2][2];
     float sa[TM];
-    const float sb0 = uniform_load(a.sb + s0);
+    const float sb0 = BROW ? 1.f : uniform_load(a.sb + s0);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         fa[i] = rows.load(As0 + (ar + 16 * i) * 128);
@@ -535,31 +557,38 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
 
     int gs = 0, kb = 0;
     auto step = [&](char *Ac, char *Bc, char *An, char *Bn) __attribute__((always_inline)) {
-        f32x4 p[4];
-        float sn[TM], sbn;
+        f32x4 p[4], sb[2][2];
+        float sn[TM], sbn = 1.f;
         // product u of the block is that of column tile 2 (u / 8) + u % 2 and row tile u / 2 % 4
         auto fold = [&](int u) __attribute__((always_inline)) {
             const int j = 2 * (u / (2 * TM)) + (u & 1), i = u / 2 % TM;
 #pragma unroll
-            for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(p[u & 3][r], sa[i], acc[i][j][r]);
+            for (int r = 0; r < 4; ++r)
+                acc[i][j][r] = fmaf(p[u & 3][r], BROW ? sa[i] * sb[u / (2 * TM) & 1][u & 1][r] : sa[i], acc[i][j][r]);
         };
 #pragma unroll
         for (int ph = 0; ph < TN / 2; ++ph) {
             const bool last = ph == TN / 2 - 1;
             if (last) {
-                wait_barrier<1>();  // the newest load, the ninth, may still be under way
+                wait_barrier<X>();  // the newest load, the ninth, may still be under way
 #pragma unroll
-                for (int i = 0; i < TM; ++i) sn[i] *= sbn;
+                for (int i = 0; i < TM; ++i)
+                    if (!BROW) sn[i] *= sbn;
             }
             __builtin_amdgcn_sched_barrier(0);
-            if (ph == 0) sbn = uniform_load(a.sb + (kb + 1 < nkb ? s0 + kb + 1 : s1));
+            if (!BROW && ph == 0) sbn = uniform_load(a.sb + (kb + 1 < nkb ? s0 + kb + 1 : s1));
             const char *bnext = last ? Bn : Bc;
+            if constexpr (BROW) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    sb[ph & 1][j] = *reinterpret_cast<const f32x4 *>(&Ss[gs & (RING - 1)][BM + br + 16 * (2 * ph + j) + 4 * g]);
+            }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
                 fb[(ph + 1) & 1][j] = rows.load(bnext + (br + 16 * (last ? j : 2 * ph + 2 + j)) * 128);
             if (ph == 0) {
 #pragma unroll
-                for (int i = 0; i < TM; ++i) sn[i] = Ss[(gs + 1) & 3][ar + 16 * i + l16];
+                for (int i = 0; i < TM; ++i) sn[i] = Ss[(gs + 1) & (RING - 1)][ar + 16 * i + l16];
             }
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
@@ -615,7 +644,8 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     __builtin_amdgcn_s_waitcnt(0);  // loads past the last block still write this workgroup's LDS
 }
 
-__global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_body(a); }
+template <bool BROW>
+__global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_body<BROW>(a); }
 
 // ---- choice of a kernel -------------------------------------------------------
 // A kernel's time is close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
@@ -660,6 +690,8 @@ constexpr Fit kFit[2][kConfigs] = {{{32, 32, 256, 3.08, 0.0944, 0.00831, 0.00042
                                     {128, 128, 256, 5.43, 1.06, 0.0122, 0.00384},
                                     {},
                                     {}}};
+// the large kernel with B scaled by rows, on the tiles' scale above (by rows they take 1.1 times as long)
+constexpr Fit kBigRows = {256, 256, 256, 5.5, 1.6, 0.027, 0.0082};
 
 double fitted_us(const Fit &f, int64_t M, int64_t N, int64_t nkb) {
     int64_t T = ((M + f.rows - 1) / f.rows) * ((N + f.cols - 1) / f.cols);
@@ -689,10 +721,10 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
     double us = 1e30;
     for (int i = 0; i < (wide ? kConfigs - 2 : kConfigs); ++i) {
         // the large kernel: 32-bit offsets over the whole of A and B, blocks in pairs, 16-byte stores
-        if (i == 8 && (BROW || a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
+        if (i == 8 && (a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
                        (int64_t)(a.N + 256) * a.K > INT32_MAX || (int64_t)a.N * 512 > INT32_MAX))
             break;
-        const double x = fitted_us(kFit[wide][i], a.M, a.N, a.nkb);
+        const double x = fitted_us(BROW && i == 8 ? kBigRows : kFit[wide][i], a.M, a.N, a.nkb);
         if (x < us) us = x, best = i;
     }
     const Fit &f = kFit[wide][best];
@@ -713,7 +745,7 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
                     break;
                 }
             }
-            if constexpr (!wide && !BROW) hipLaunchKernelGGL(matmul_big_kernel, dim3(256), dim3(512), 0, st, a);
+            if constexpr (!wide) hipLaunchKernelGGL(matmul_big_kernel<BROW>, dim3(256), dim3(512), 0, st, a);
     }
     return hipGetLastError();
 }
