@@ -132,17 +132,17 @@ __device__ __forceinline__ int swizzled_source(int lane, int q, int K) {
     return (lane >> 3) * K + 16 * ((lane & 7) ^ ((4 * (q & 1) + (lane >> 4)) & 7));
 }
 
-// Four consecutive output features of one token (n < N for the first).
+// Four consecutive output features of one token (n < N for the first), at an element's own alignment.
 template <typename OUT>
 __device__ __forceinline__ void store_row4(OUT *row, int n, int N, f32x4 v) {
-    if ((N & 3) == 0) {
+    if (n + 4 <= N) {
         if constexpr (sizeof(OUT) == 2)
-            *reinterpret_cast<uint2 *>(row + n) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+            store_any(row + n, (uint64_t)pack_bf16(v[2], v[3]) << 32 | pack_bf16(v[0], v[1]));
         else
-            *reinterpret_cast<float4 *>(row + n) = make_float4(v[0], v[1], v[2], v[3]);
+            store_any(row + n, v);
     } else {
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
+        for (int r = 0; r < 3; ++r)
             if (n + r < N) store(row, n + r, v[r]);
     }
 }
@@ -615,32 +615,47 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
     };
     auto tile_end = [&]() __attribute__((always_inline)) {
         const auto ro = rsrc(static_cast<uint16_t *>(a.out) + (size_t)cur.m0 * a.N, (uint32_t)(min(BM, a.M - cur.m0) * a.N * 2));
+        if (a.N % 8 == 0) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; j += 2) {
+                    // lanes of even g take tile j, of odd g tile j + 1: features 8 (g / 2) .. + 7 of it
+                    const f32x4 v = acc[i][j], w = acc[i][j + 1];
+                    const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0], v[1]), pack_bf16(w[0], w[1]), false, false);
+                    const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2], v[3]), pack_bf16(w[2], w[3]), false, false);
+                    const int m = ar + 16 * i + l16, n = cur.n0 + br + 16 * (j + (g & 1)) + 8 * (g >> 1);
+                    const int off = n < a.N ? (m * a.N + n) * 2 : 0x7fffffff;  // rows and columns past the end are dropped
+                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, off, 0, 0);
+                }
+        } else {  // rows that start anywhere
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int m = cur.m0 + ar + 16 * i + l16, n = cur.n0 + br + 4 * g;
+                uint16_t *row = static_cast<uint16_t *>(a.out) + (size_t)m * a.N;
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    if (m < a.M && n + 16 * j < a.N) store_row4(row, n + 16 * j, a.N, acc[i][j]);
+            }
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int j = 0; j < TN; j += 2) {
-                // lanes of even g take tile j, of odd g tile j + 1: features 8 (g / 2) .. + 7 of it
-                const f32x4 v = acc[i][j], w = acc[i][j + 1];
-                const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0], v[1]), pack_bf16(w[0], w[1]), false, false);
-                const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2], v[3]), pack_bf16(w[2], w[3]), false, false);
-                const int m = ar + 16 * i + l16, n = cur.n0 + br + 16 * (j + (g & 1)) + 8 * (g >> 1);
-                const int off = n < a.N ? (m * a.N + n) * 2 : 0x7fffffff;  // rows and columns past the end are dropped
-                __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, off, 0, 0);
-                acc[i][j] = acc[i][j + 1] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int j = 0; j < TN; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
         t += slots;
         if (t >= tend) return false;
+        kb = 0;
         cur = nxt, a0 = a1, b0 = b1, x0 = x1, s0 = s1;
         nxt = big_tile(min(t + slots, tend - 1));
         a1 = nxt.m0 * K, b1 = nxt.n0 * K, x1 = xbase(nxt), s1 = sbase(nxt);
         return true;
     };
-    do {
-        for (kb = 0; kb < nkb;) {
-            step(As0, Bs0, As1, Bs1);
-            step(As1, Bs1, As0, Bs0);
-        }
-    } while (tile_end());
+    for (;;) {
+        step(As0, Bs0, As1, Bs1);
+        if (kb == nkb && !tile_end()) break;
+        step(As1, Bs1, As0, Bs0);
+        if (kb == nkb && !tile_end()) break;
+    }
     __builtin_amdgcn_s_waitcnt(0);  // loads past the last block still write this workgroup's LDS
 }
 
@@ -651,14 +666,14 @@ __global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_bod
 // A kernel's time is close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
 // tile's latency, and the chip's throughput over T tiles, T rounded up to
 // what fills the CUs evenly.  The constants (us) are least-squares fits to
-// times over 330 random sizes (9 .. 8192 tokens, 128 .. 16384 features, a
-// contraction of 256 .. 16384), for bf16 and for fp32 output; taking the
-// smallest costs 1.5% (1.0%) over the best kernel of each size, and 2.3% over
-// 160 other sizes.  Groups of waves that share a tile's blocks, and stages
-// further ahead, pay where there are few tiles; small LDS, so more workgroups
-// per CU, where there are many.  Times in us, bf16 output (32 x 32 by four groups | by one | 32 x 64
-// | 64 x 64 by two | by one | 128 x 64 | 128 x 128 | 128 x 64 with four
-// stages | 256 x 256):
+// times over 480 random sizes (9 .. 16384 tokens, 64 .. 16384 features, a
+// contraction of 256 .. 16384; B by rows and by squares alike), for bf16 and
+// for fp32 output; taking the smallest costs 1.2% over the best kernel of each
+// size.  Groups of waves that share a tile's blocks, and stages further ahead,
+// pay where there are few tiles; small LDS, so more workgroups per CU, where
+// there are many.  Times in us, bf16 output (32 x 32 by four groups | by one
+// | 32 x 64 | 64 x 64 by two | by one | 128 x 64 | 128 x 128 | 128 x 64 with
+// four stages | 256 x 256):
 //   64 x 4096 x 4096        6.0 |  8.5 |  7.8 | 10.3 |      |      |      | 15.0 |
 //   64 x 8192 x 4096       12.5 | 11.0 |  8.9 | 11.8 |      |      |      | 16.5 |
 //   100 x 8192 x 4096      20.5 | 16.1 | 12.5 | 11.8 |      |      |      | 16.9 |
@@ -672,26 +687,24 @@ struct Fit {
 };
 // the last two are for bf16 output alone
 constexpr int kConfigs = 9;
-constexpr Fit kFit[2][kConfigs] = {{{32, 32, 256, 3.08, 0.0944, 0.00831, 0.000428},
-                                    {32, 32, 512, 2.61, 0.197, 0.00227, 0.000393},
-                                    {32, 64, 256, 2.94, 0.164, 0.0056, 0.000595},
-                                    {64, 64, 256, 3.36, 0.222, 0.00967, 0.00102},
-                                    {64, 64, 256, 2.69, 0.282, 0.00414, 0.001},
-                                    {128, 64, 256, 2.46, 0.546, 0.00666, 0.00152},
-                                    {128, 128, 256, 3.99, 0.709, 0.0138, 0.00211},
-                                    {128, 64, 256, 3.38, 0.446, 0.0118, 0.00174},
-                                    {256, 256, 256, 5.5, 1.25, 0.027, 0.0068}},
-                                   {{32, 32, 256, 3.04, 0.131, 0.00832, 0.000587},
-                                    {32, 32, 512, 2.24, 0.412, 0.00238, 0.000517},
-                                    {32, 64, 256, 2.98, 0.264, 0.00576, 0.000851},
-                                    {64, 64, 256, 3.41, 0.390, 0.0116, 0.00152},
-                                    {64, 64, 256, 2.89, 0.457, 0.00287, 0.00139},
-                                    {128, 64, 256, 3.07, 0.737, 0.00724, 0.00223},
-                                    {128, 128, 256, 5.43, 1.06, 0.0122, 0.00384},
+constexpr Fit kFit[2][kConfigs] = {{{32, 32, 256, 3.04, 0.0956, 0.00824, 0.000466},
+                                    {32, 32, 256, 2.62, 0.186, 0.00194, 0.000498},
+                                    {32, 64, 256, 2.89, 0.166, 0.00486, 0.00069},
+                                    {64, 64, 256, 3.33, 0.22, 0.00872, 0.00109},
+                                    {64, 64, 256, 2.58, 0.294, 0.0029, 0.00109},
+                                    {128, 64, 256, 2.43, 0.545, 0.00623, 0.00153},
+                                    {128, 128, 256, 4.34, 0.747, 0.0116, 0.00227},
+                                    {128, 64, 256, 3.28, 0.447, 0.0114, 0.00186},
+                                    {256, 256, 256, 9.42, 1.51, 0.0322, 0.00594}},
+                                   {{32, 32, 256, 3.05, 0.127, 0.00853, 0.000532},
+                                    {32, 32, 512, 2.47, 0.319, 0.00266, 0.00048},
+                                    {32, 64, 256, 2.99, 0.236, 0.00615, 0.000751},
+                                    {64, 64, 256, 3.35, 0.35, 0.0109, 0.0014},
+                                    {64, 64, 256, 2.67, 0.446, 0.00577, 0.00119},
+                                    {128, 64, 256, 3.29, 0.731, 0.00863, 0.00206},
+                                    {128, 128, 256, 4.99, 1.08, 0.0121, 0.00347},
                                     {},
                                     {}}};
-// the large kernel with B scaled by rows, on the tiles' scale above (by rows they take 1.1 times as long)
-constexpr Fit kBigRows = {256, 256, 256, 5.5, 1.6, 0.027, 0.0082};
 
 double fitted_us(const Fit &f, int64_t M, int64_t N, int64_t nkb) {
     int64_t T = ((M + f.rows - 1) / f.rows) * ((N + f.cols - 1) / f.cols);
@@ -720,11 +733,11 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
     int best = 0;
     double us = 1e30;
     for (int i = 0; i < (wide ? kConfigs - 2 : kConfigs); ++i) {
-        // the large kernel: 32-bit offsets over the whole of A and B, blocks in pairs, 16-byte stores
-        if (i == 8 && (a.nkb < 4 || a.nkb % 2 || a.N % 8 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
+        // the large kernel: 32-bit offsets over the whole of A and B, loads up to four blocks ahead
+        if (i == 8 && (a.nkb < 4 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
                        (int64_t)(a.N + 256) * a.K > INT32_MAX || (int64_t)a.N * 512 > INT32_MAX))
             break;
-        const double x = fitted_us(BROW && i == 8 ? kBigRows : kFit[wide][i], a.M, a.N, a.nkb);
+        const double x = fitted_us(kFit[wide][i], a.M, a.N, a.nkb);
         if (x < us) us = x, best = i;
     }
     const Fit &f = kFit[wide][best];

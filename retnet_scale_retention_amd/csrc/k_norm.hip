@@ -147,7 +147,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
             if (a.dsum) dr[v].load(static_cast<const T *>(a.dsum) + row * a.d + e, a.d - e);
         }
     };
-    constexpr bool early = keep && V * (VEC ? sizeof(T) : 4) <= 8;
+    constexpr bool early = keep && V * sizeof(T) <= 8;
     float wt[V][8], dw[V][8];
     if (keep) fetch(0);
 #pragma unroll
@@ -287,24 +287,23 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 }
 
 // out[c] = sum_p part[p][c] for 32 columns: p in order within each of 64
-// slices, the slices in order
-template <bool VEC>
+// slices (eight loads of four columns under way), the slices in order
 __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out, int parts, int d) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
     __shared__ float red[64][33];
     const int q = 4 * (threadIdx.x & 7), c = (int)blockIdx.x * 32 + q, sl = threadIdx.x >> 3;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (VEC) {
-        if (c < d)
-            for (int p0 = sl; p0 < parts; p0 += 512) {  // eight loads at once, zeros past the last part
-                float4 x[8];
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (c + 4 <= d) {
+        for (int p0 = sl; p0 < parts; p0 += 512) {
+            f32x4 x[8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (p0 + 64 * u < parts) x[u] = *reinterpret_cast<const float4 *>(part + (size_t)(p0 + 64 * u) * d + c);
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u) s[0] += x[u].x, s[1] += x[u].y, s[2] += x[u].z, s[3] += x[u].w;
+            for (int u = 0; u < 8; ++u) {  // zeros past the last part
+                x[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (p0 + 64 * u < parts) x[u] = load_any<f32x4>(part + (size_t)(p0 + 64 * u) * d + c);
             }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s += x[u];
+        }
     } else {
         for (int p = sl; p < parts; p += 64)
 #pragma unroll
@@ -403,9 +402,7 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h
         });
     });
     if (e == hipSuccess && dw) {
-        const dim3 grid((d + 31) / 32), block(512);
-        if (d % 4 == 0) hipLaunchKernelGGL(column_sum_kernel<true>, grid, block, 0, st, part, dw, parts, d);
-        else hipLaunchKernelGGL(column_sum_kernel<false>, grid, block, 0, st, part, dw, parts, d);
+        hipLaunchKernelGGL(column_sum_kernel, dim3((d + 31) / 32), dim3(512), 0, st, part, dw, parts, d);
         e = hipGetLastError();
     }
     return e;

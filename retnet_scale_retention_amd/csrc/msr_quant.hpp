@@ -74,58 +74,98 @@ __device__ __forceinline__ float wave_sum_dpp(float x) {
     return __uint_as_float(t[0]) + __uint_as_float(t[1]);
 }
 
+// Accesses of 4 to 16 bytes at an element's own alignment: rows of a width that is not a multiple of 8 start anywhere,
+// and the memory pipeline takes any address (element by element, the norm's gradients of 2941 x 1789 bf16 took 50 us).
+template <typename V>
+struct __attribute__((packed, aligned(2))) AnyAlign {
+    V v;
+};
+template <typename V>
+__device__ __forceinline__ V load_any(const void *p) {
+    return static_cast<const AnyAlign<V> *>(p)->v;
+}
+template <typename V>
+__device__ __forceinline__ void store_any(void *p, V v) {
+    static_cast<AnyAlign<V> *>(p)->v = v;
+}
+
 // Eight consecutive elements at p (16-byte aligned when VEC) as they lie in
 // memory, and as floats: loads go out early this way and are widened late.
 // Elements from index `left` on lie past the row's end, are not read and
-// count as zero.
+// count as zero (VEC: none or all eight do).
 template <typename T, bool VEC>
 struct Raw8;
 
-template <>
-struct Raw8<uint16_t, true> {
-    uint4 u;
+template <bool VEC>
+struct Raw8<uint16_t, VEC> {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    u32x4 u;
     __device__ __forceinline__ void load(const uint16_t *p, int left) {
-        u = make_uint4(0, 0, 0, 0);
-        if (left > 0) u = *reinterpret_cast<const uint4 *>(p);
+        u = u32x4{0, 0, 0, 0};
+        if constexpr (VEC) {
+            if (left > 0) u = *reinterpret_cast<const u32x4 *>(p);
+        } else if (left >= 8) {
+            u = load_any<u32x4>(p);
+        } else if (left > 0) {  // 4 + 2 + 1 elements
+            if (left & 4) {
+                const uint64_t x = load_any<uint64_t>(p);
+                u[0] = (uint32_t)x, u[1] = (uint32_t)(x >> 32);
+            }
+            if (left & 2) {
+                const uint32_t x = load_any<uint32_t>(p + (left & 4));
+                if (left & 4) u[2] = x;
+                else u[0] = x;
+            }
+            if (left & 1) {
+                const uint32_t x = p[left & 6], w = left >> 1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] = w == i ? x : u[i];
+            }
+        }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
         }
     }
     // keeps the compiler from holding the floats (twice the registers) from one get() to the next
-    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(u.x), "+v"(u.y), "+v"(u.z), "+v"(u.w)); }
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(u)); }
 };
 
-template <>
-struct Raw8<float, true> {
-    float4 a, b;
+template <bool VEC>
+struct Raw8<float, VEC> {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    f32x4 a, b;
     __device__ __forceinline__ void load(const float *p, int left) {
-        a = b = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (left > 0) {
-            a = *reinterpret_cast<const float4 *>(p);
-            b = *reinterpret_cast<const float4 *>(p + 4);
+        a = b = f32x4{0.f, 0.f, 0.f, 0.f};
+        if constexpr (VEC) {
+            if (left > 0) {
+                a = *reinterpret_cast<const f32x4 *>(p);
+                b = *reinterpret_cast<const f32x4 *>(p + 4);
+            }
+        } else if (left >= 8) {
+            a = load_any<f32x4>(p);
+            b = load_any<f32x4>(p + 4);
+        } else if (left > 0) {
+            if (left & 4) a = load_any<f32x4>(p);
+            if (left & 2) {
+                const f32x2 x = load_any<f32x2>(p + (left & 4));
+                if (left & 4) b[0] = x[0], b[1] = x[1];
+                else a[0] = x[0], a[1] = x[1];
+            }
+            if (left & 1) {
+                const float x = p[left & 6];
+                const int w = left & 6;  // 0, 2, 4 or 6
+                a[0] = w == 0 ? x : a[0], a[2] = w == 2 ? x : a[2], b[0] = w == 4 ? x : b[0], b[2] = w == 6 ? x : b[2];
+            }
         }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    }
-    __device__ __forceinline__ void forget() {}
-};
-
-template <typename T>
-struct Raw8<T, false> {
-    float x[8];
-    __device__ __forceinline__ void load(const T *p, int left) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = i < left ? msr::load(p, i) : 0.f;
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = x[i];
+        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
     }
     __device__ __forceinline__ void forget() {}
 };
@@ -155,30 +195,39 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return __builtin_bit_cast(uint32_t, p);
 }
 
+// Stores of eight elements, those from `left` on left out.  Ordinary ones where lanes do not fill whole lines.
 template <bool VEC>
 __device__ __forceinline__ void store8(uint16_t *p, int left, const float (&v)[8]) {
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 u = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
     if constexpr (VEC) {
-        if (left > 0)
-            stream_out(p, make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
-                                     pack_bf16(v[6], v[7])));
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = f32_to_bf16(v[i]);
+        if (left > 0) stream_out(p, make_uint4(u[0], u[1], u[2], u[3]));
+    } else if (left >= 8) {
+        store_any(p, u);
+    } else if (left > 0) {
+        if (left & 4) store_any(p, (uint64_t)u[1] << 32 | u[0]);
+        if (left & 2) store_any(p + (left & 4), (left & 4) ? u[2] : u[0]);
+        if (left & 1) p[left & 6] = (uint16_t)((left & 4) ? ((left & 2) ? u[3] : u[2]) : ((left & 2) ? u[1] : u[0]));
     }
 }
 
 template <bool VEC>
 __device__ __forceinline__ void store8(float *p, int left, const float (&v)[8]) {
+    typedef float f32x4 __attribute__((ext_vector_type(4)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
     if constexpr (VEC) {
         if (left > 0) {
-            *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            *reinterpret_cast<f32x4 *>(p) = a;
+            *reinterpret_cast<f32x4 *>(p + 4) = b;
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = v[i];
+    } else if (left >= 8) {
+        store_any(p, a);
+        store_any(p + 4, b);
+    } else if (left > 0) {
+        if (left & 4) store_any(p, a);
+        if (left & 2) store_any(p + (left & 4), (left & 4) ? f32x2{b[0], b[1]} : f32x2{a[0], a[1]});
+        if (left & 1) p[left & 6] = (left & 4) ? ((left & 2) ? b[2] : b[0]) : ((left & 2) ? a[2] : a[0]);
     }
 }
 

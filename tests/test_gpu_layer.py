@@ -61,7 +61,8 @@ def check_blocks(q, s, x, block_rows, err, name):
 
 
 SIZES = [(1, 1), (1, 64), (3, 128), (5, 136), (64, 200), (7, 511), (130, 512), (9, 1000), (33, 1024), (6, 2047),
-         (17, 2048), (5, 4096), (3, 4100), (4, 8192), (2, 16384), (2, 20001), (1, 32768)]
+         (17, 2048), (5, 4096), (3, 4100), (4, 8192), (2, 16384), (2, 20001), (1, 32768),
+         (9, 2), (10, 6), (11, 517), (300, 1002), (5, 2067), (4, 6006), (3, 16381)]  # rows that end 2, 3, 5 or 6 past a group
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -191,7 +192,8 @@ def test_add_rmsnorm_backward_without_rows_gives_a_zero_weight_gradient():
     assert y.shape == (0, 96) and q.shape == (0, 128) and s.shape == (0, 1)
 
 
-QSIZES = [(1, 1), (1, 128), (128, 1), (5, 77), (127, 129), (128, 128), (130, 264), (300, 1000), (257, 512), (64, 4096)]
+QSIZES = [(1, 1), (1, 128), (128, 1), (5, 77), (127, 129), (128, 128), (130, 264), (300, 1000), (257, 512), (64, 4096),
+          (129, 258), (40, 1003), (131, 518), (7, 2047)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -329,7 +331,7 @@ def test_scaled_matmul_positions(out):
 
 # the larger tiles: 32 x 64, 64 x 64, 128 x 64 (four stages, two stages), 128 x 128, 256 x 256, with ends inside a tile
 LSIZES = [(700, 701, 2048), (90, 8190, 1152), (70, 8190, 2048), (1000, 1100, 4096), (300, 6001, 512), (1025, 1990, 256), (250, 8184, 4096), (2040, 1545, 640), (4101, 4100, 512),
-          (2561, 2050, 1024), (3001, 4100, 256), (4010, 8200, 512), (8300, 8200, 1024)]
+          (2561, 2050, 1024), (3001, 4100, 256), (4010, 8200, 512), (8300, 8200, 1024), (3000, 5003, 640), (4099, 8194, 1152)]
 
 
 def product64(qa, sa, qb, sb, block):
