@@ -425,7 +425,7 @@ __global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
 // 128 features of the tile as 4 x 8 results (128 registers).  Two LDS stages
 // of a block (64 KiB each), filled by direct loads; the sequence of blocks
 // runs on over the tiles' ends, so a tile's first blocks are under way while
-// the last one's results are stored.
+// the last one's results are stored, for any count of blocks from four on.
 //   - A block is worked off in four phases of two column tiles.  Each phase
 //     starts by reading the next phase's operands into registers, and the
 //     last phase the next block's A; the one barrier of a block stands before
@@ -440,7 +440,8 @@ __global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
 //     an XCD share); without it the loads' latency showed (2.2 against 1.7 us
 //     per block).  With B scaled by rows every wave does both, scales (A's or
 //     B's) and lines.
-//   - After a lane swap every lane stores 16 bytes of a row.
+//   - After a lane swap every lane stores 16 bytes of a row (8 where rows
+//     start anywhere; 16 at a time were no faster there).
 // 16384 x 8192 x 4096: 485 us = 2270 TFLOP/s.  It is bound by the chip's power:
 // the same kernel over zeros takes 388 us, and its blocks without loads 1.05
 // us each, the products' own rate (1.6 with random bytes and all).  The
@@ -733,8 +734,10 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
     int best = 0;
     double us = 1e30;
     for (int i = 0; i < (wide ? kConfigs - 2 : kConfigs); ++i) {
-        // the large kernel: 32-bit offsets over the whole of A and B, loads up to four blocks ahead
-        if (i == 8 && (a.nkb < 4 || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
+        // the large kernel: 32-bit offsets over the whole of A and B, and four blocks (its loads run that far ahead) or,
+        // with rows of results that start anywhere, eight (3465 x 2663 x 512: 20.9 us against 16.5 with 128 x 64 tiles,
+        // but 8192 x 8191 x 1024 117 against 130)
+        if (i == 8 && (a.nkb < (a.N % 8 ? 8 : 4) || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
                        (int64_t)(a.N + 256) * a.K > INT32_MAX || (int64_t)a.N * 512 > INT32_MAX))
             break;
         const double x = fitted_us(kFit[wide][i], a.M, a.N, a.nkb);
