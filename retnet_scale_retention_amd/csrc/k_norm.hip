@@ -46,7 +46,7 @@ __device__ __forceinline__ float team_sum(float x, float *red, int tm, int w) {
     return x;
 }
 
-template <typename T, bool VEC, int W, int V>
+template <typename T, int ROWS, int W, int V>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormArgs a) {
     constexpr int TEAMS = W < 4 ? 4 / W : 1;
     __shared__ float red[TEAMS * W];
@@ -61,14 +61,14 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         const int e = 8 * (64 * (v * W + w) + lane);
-        load8<VEC>(x + e, a.d - e, h[v]);
+        load8<ROWS>(x + e, a.d - e, h[v]);
     }
     if (r) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = 8 * (64 * (v * W + w) + lane);
             float t[8];
-            load8<VEC>(r + e, a.d - e, t);
+            load8<ROWS>(r + e, a.d - e, t);
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[v][i] += t[i];
         }
@@ -82,7 +82,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = 8 * (64 * (v * W + w) + lane);
-            store8<VEC>(s + e, a.d - e, h[v]);
+            store8<ROWS>(s + e, a.d - e, h[v]);
         }
     }
     const float rstd = 1.f / sqrtf(team_sum<W>(ss, red, tm, w) / (float)a.d + a.eps);
@@ -90,10 +90,10 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
     for (int v = 0; v < V; ++v) {
         const int e = 8 * (64 * (v * W + w) + lane);
         float g[8];
-        load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, g);
+        load_weight8<ROWS>(a.w, a.w_bf16, e, a.d - e, g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[v][i] = h[v][i] * rstd * g[i];
-        if (a.y && live) store8<VEC>(static_cast<T *>(a.y) + row * a.d + e, a.d - e, h[v]);
+        if (a.y && live) store8<ROWS>(static_cast<T *>(a.y) + row * a.d + e, a.d - e, h[v]);
         if (a.q) {
             uint32_t m = 0;
 #pragma unroll
@@ -123,7 +123,7 @@ struct NormBackArgs {
 // 16384 x 4096; without the loads ahead 216);
 // the workgroup's teams add up in LDS, its sum goes to `part`, and
 // column_sum_kernel adds the parts in a fixed order (no atomics).
-template <typename T, bool VEC, int W, int V>
+template <typename T, int ROWS, int W, int V>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(NormBackArgs a) {
     constexpr int TEAMS = W < 4 ? 4 / W : 1;
     __shared__ float red[2][2 * TEAMS * W];
@@ -134,9 +134,9 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
     const int e0 = 8 * (64 * w + lane);                  // group v starts at e0 + 512 W v
     // the longest rows are read a second time instead of kept, and their weight gradient stays in LDS (all in registers,
     // 276 of them spilled: 1024 x 32768 bf16 231 us)
-    constexpr bool keep = W * V <= 32;
+    constexpr bool keep = W * V <= (ROWS == kAligned ? 32 : 16);
     __shared__ __attribute__((aligned(16))) float4 dwl[keep ? 1 : 128 * W * V];
-    Raw8<T, VEC> hr[V], gr[V], dr[V];
+    Raw8<T, ROWS> hr[V], gr[V], dr[V];
     auto fetch = [&](int64_t t) {  // past the last row: that row again, not used
         const int64_t r = t * teams + team, row = r < a.rows ? r : a.rows - 1;
 #pragma unroll
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
     for (int v = 0; v < V; ++v) {
         const int e = e0 + 512 * W * v;
         if constexpr (keep) {
-            load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
+            load_weight8<ROWS>(a.w, a.w_bf16, e, a.d - e, wt[v]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) dw[v][i] = 0.f;
         } else {
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
     for (int64_t t = 0; t < turns; ++t) {
         const int64_t row = t * teams + team;
         const int64_t at = (row < a.rows ? row : a.rows - 1) * a.d;
-        Raw8<T, VEC> hc[V], gc[V], dc[V];
+        Raw8<T, ROWS> hc[V], gc[V], dc[V];
         if constexpr (keep) {
 #pragma unroll
             for (int v = 0; v < V; ++v) hc[v] = hr[v], gc[v] = gr[v], dc[v] = dr[v];
@@ -180,7 +180,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
                 __builtin_amdgcn_sched_barrier(0);  // a group's loads at a time
                 hc[v].load(static_cast<const T *>(a.h) + at + e, a.d - e);
                 gc[v].load(static_cast<const T *>(a.dy) + at + e, a.d - e);
-                load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
+                load_weight8<ROWS>(a.w, a.w_bf16, e, a.d - e, wt[v]);
             }
             hc[v].get(h);
             gc[v].get(g);
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
                 hc[v].load(static_cast<const T *>(a.h) + at + e, a.d - e);
                 gc[v].load(static_cast<const T *>(a.dy) + at + e, a.d - e);
                 if (a.dsum) dc[v].load(static_cast<const T *>(a.dsum) + at + e, a.d - e);
-                load_weight8<VEC>(a.w, a.w_bf16, e, a.d - e, wt[v]);
+                load_weight8<ROWS>(a.w, a.w_bf16, e, a.d - e, wt[v]);
             }
             hc[v].get(h);
             gc[v].get(g);
@@ -251,7 +251,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
                     x = y;
                 }
             }
-            store8<VEC>(static_cast<T *>(a.dx) + row * a.d + e, a.d - e, o);
+            store8<ROWS>(static_cast<T *>(a.dx) + row * a.d + e, a.d - e, o);
         }
         if (keep && !early && t + 1 < turns) fetch(t + 1);
     }
@@ -278,9 +278,9 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
             if constexpr (!keep) {
                 const float4 x = dwl[64 * (2 * (v * W + w)) + lane], y = dwl[64 * (2 * (v * W + w) + 1) + lane];
                 const float z[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-                store8<VEC>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, z);
+                store8<ROWS>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, z);
             } else {
-                store8<VEC>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, dw[v]);
+                store8<ROWS>(a.part + (int64_t)blockIdx.x * a.d + e, a.d - e, dw[v]);
             }
         }
     }
@@ -340,10 +340,13 @@ hipError_t by_width(int d, F f) {
     return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
 }
 
-template <typename F>
-hipError_t by_type(int dtype, bool vec, F f) {
-    if (dtype == MSR_BF16) return vec ? f(uint16_t(), std::true_type()) : f(uint16_t(), std::false_type());
-    return vec ? f(float(), std::true_type()) : f(float(), std::false_type());
+template <bool ONE, typename T, typename F>
+hipError_t by_rows(int d, F f) {
+    if (d % 8 == 0)
+        return by_width<ONE>(d, [&](auto W, auto V) { return f(T(), std::integral_constant<int, kAligned>(), W, V); });
+    if (d > 8)
+        return by_width<ONE>(d, [&](auto W, auto V) { return f(T(), std::integral_constant<int, kAny>(), W, V); });
+    return f(T(), std::integral_constant<int, kTiny>(), std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
 }
 
 // Workgroups of the backward pass: each writes one partial weight gradient.
@@ -368,20 +371,19 @@ int back_groups(int64_t rows, int d, int dtype) {
 hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, const void *r, const void *w, int w_dtype,
                               float eps, void *sum, void *y, void *q, float *qs, hipStream_t st) {
     NormArgs a{x, r, w, sum, y, static_cast<uint8_t *>(q), qs, 0, rows, d, (int)round128(d), w_dtype == MSR_BF16, eps};
-    return by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
-        return by_width<sizeof(t) == 4>(d, [&](auto W, auto V) {
-            constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
-            constexpr int64_t most = (int64_t)1 << 21;  // workgroups of a launch: its threads stay below 2^32
-            hipError_t e = hipSuccess;
-            for (a.row0 = 0; a.row0 < rows && e == hipSuccess; a.row0 += most * teams) {
-                const int64_t g = std::min<int64_t>((rows - a.row0 + teams - 1) / teams, most);
-                hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(t), vec.value, W.value, V.value>), dim3((unsigned)g),
-                                   dim3(nt), 0, st, a);
-                e = hipGetLastError();
-            }
-            return e;
-        });
-    });
+    auto launch = [&](auto t, auto rw, auto W, auto V) {
+        constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
+        constexpr int64_t most = (int64_t)1 << 21;  // workgroups of a launch: its threads stay below 2^32
+        hipError_t e = hipSuccess;
+        for (a.row0 = 0; a.row0 < rows && e == hipSuccess; a.row0 += most * teams) {
+            const int64_t g = std::min<int64_t>((rows - a.row0 + teams - 1) / teams, most);
+            hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(t), rw.value, W.value, V.value>), dim3((unsigned)g), dim3(nt),
+                               0, st, a);
+            e = hipGetLastError();
+        }
+        return e;
+    };
+    return dtype == MSR_BF16 ? by_rows<false, uint16_t>(d, launch) : by_rows<true, float>(d, launch);
 }
 
 // enough for either type
@@ -393,14 +395,14 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h
                                    const void *dy, const void *dsum, void *dx, float *dw, float *part, hipStream_t st) {
     const int parts = back_groups(rows, d, dtype);
     const NormBackArgs a{h, w, dy, dsum, dx, dw ? part : nullptr, rows, d, w_dtype == MSR_BF16, eps};
-    hipError_t e = parts == 0 ? hipSuccess : by_type(dtype, d % 8 == 0, [&](auto t, auto vec) {
-        return by_width<true>(d, [&](auto W, auto V) {
-            constexpr int nt = W.value < 4 ? 256 : 64 * W.value;
-            hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), vec.value, W.value, V.value>), dim3(parts),
-                               dim3(nt), 0, st, a);
-            return hipGetLastError();
-        });
-    });
+    auto launch = [&](auto t, auto rw, auto W, auto V) {
+        constexpr int nt = W.value < 4 ? 256 : 64 * W.value;
+        hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), rw.value, W.value, V.value>), dim3(parts), dim3(nt), 0, st,
+                           a);
+        return hipGetLastError();
+    };
+    hipError_t e = hipSuccess;
+    if (parts > 0) e = dtype == MSR_BF16 ? by_rows<true, uint16_t>(d, launch) : by_rows<true, float>(d, launch);
     if (e == hipSuccess && dw) {
         hipLaunchKernelGGL(column_sum_kernel, dim3((d + 31) / 32), dim3(512), 0, st, part, dw, parts, d);
         e = hipGetLastError();

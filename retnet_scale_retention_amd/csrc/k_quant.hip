@@ -19,13 +19,13 @@ struct QuantArgs {
 
 // Own order, blocks within a row: 16 lanes take a block, 8 values each, and
 // four blocks one after the other, loaded together.
-template <typename T, bool VEC>
+template <typename T, int ROWS>
 __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
     constexpr int U = 4;
     const uint32_t per_row = (uint32_t)(a.Cp / kBlock);
     const int64_t first = (int64_t)blockIdx.x * (16 * U), row0 = first / per_row;  // the same for the workgroup
     const uint32_t col0 = (uint32_t)(first - row0 * per_row);
-    Raw8<T, VEC> x[U];
+    Raw8<T, ROWS> x[U];
     int64_t row[U];
     uint32_t blk[U];
 #pragma unroll
@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
 // the values kept as loaded, not widened (174 -> 117 registers, 74 -> 59 us;
 // the squares' kernel has room for the floats and is faster with them), and
 // stores that do not linger in L2 (59 -> 48 us).
-template <typename T, bool VEC, bool SQUARE>
+template <typename T, int ROWS, bool SQUARE>
 __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
     __shared__ __attribute__((aligned(16))) uint32_t cmax[4][128];
     __shared__ float cscale[128];
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
     const int64_t r0 = tr_i * 128, c0 = tc * 128;
     const int rg = threadIdx.x >> 4, cg = threadIdx.x & 15, wave = threadIdx.x >> 6;
     const int64_t c = c0 + 8 * cg;
-    Raw8<T, VEC> x[8];
+    Raw8<T, ROWS> x[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int64_t r = r0 + 8 * rg + i;
@@ -169,17 +169,17 @@ __global__ __launch_bounds__(256) void quantize_tile_kernel(QuantArgs a) {
     }
 }
 
-template <typename T, bool VEC>
+template <typename T, int ROWS>
 hipError_t quantize(const QuantArgs &a, int block_rows, hipStream_t st) {
     if (block_rows == 1 && !a.qt) {
         const int64_t g = (a.R * (a.Cp / kBlock) + 63) / 64;
-        hipLaunchKernelGGL((quantize_rows_kernel<T, VEC>), dim3((unsigned)g), dim3(256), 0, st, a);
+        hipLaunchKernelGGL((quantize_rows_kernel<T, ROWS>), dim3((unsigned)g), dim3(256), 0, st, a);
     } else {
         const unsigned tiles = (unsigned)(a.Rp / 128 * a.tiles_c);
         if (block_rows == 1)
-            hipLaunchKernelGGL((quantize_tile_kernel<T, VEC, false>), dim3(tiles), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((quantize_tile_kernel<T, ROWS, false>), dim3(tiles), dim3(256), 0, st, a);
         else
-            hipLaunchKernelGGL((quantize_tile_kernel<T, VEC, true>), dim3(tiles), dim3(256), 0, st, a);
+            hipLaunchKernelGGL((quantize_tile_kernel<T, ROWS, true>), dim3(tiles), dim3(256), 0, st, a);
     }
     return hipGetLastError();
 }
@@ -191,6 +191,10 @@ hipError_t launch_quantize(int64_t R, int64_t C, int dtype, int block_rows, cons
     const QuantArgs a{x, static_cast<uint8_t *>(q), static_cast<uint8_t *>(qt), s, s_t, R, C, round128(C), round128(R),
                       (int)(round128(C) / 128)};
     if (dtype == MSR_BF16)
-        return C % 8 == 0 ? quantize<uint16_t, true>(a, block_rows, st) : quantize<uint16_t, false>(a, block_rows, st);
-    return C % 8 == 0 ? quantize<float, true>(a, block_rows, st) : quantize<float, false>(a, block_rows, st);
+        return C % 8 == 0 ? quantize<uint16_t, kAligned>(a, block_rows, st)
+               : C > 8    ? quantize<uint16_t, kAny>(a, block_rows, st)
+                          : quantize<uint16_t, kTiny>(a, block_rows, st);
+    return C % 8 == 0 ? quantize<float, kAligned>(a, block_rows, st)
+           : C > 8    ? quantize<float, kAny>(a, block_rows, st)
+                      : quantize<float, kTiny>(a, block_rows, st);
 }

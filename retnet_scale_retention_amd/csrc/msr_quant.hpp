@@ -89,90 +89,92 @@ __device__ __forceinline__ void store_any(void *p, V v) {
     static_cast<AnyAlign<V> *>(p)->v = v;
 }
 
-// Eight consecutive elements at p (16-byte aligned when VEC) as they lie in
-// memory, and as floats: loads go out early this way and are widened late.
-// Elements from index `left` on lie past the row's end, are not read and
-// count as zero (VEC: none or all eight do).
-template <typename T, bool VEC>
+// How rows lie: of widths that are multiples of 8 (every group of eight aligned to 16 bytes, none cut), of any width
+// from 8 on, or of fewer than 8 elements.
+enum { kTiny, kAny, kAligned };
+
+// Eight consecutive elements at p as they lie in memory, and as floats: loads go out early this way and are widened
+// late.  Elements from index `left` on lie past the row's end, are not read and count as zero.  Where a row of any
+// width ends inside the eight, its last eight are read instead and moved down in get(): no lane then waits for its loads
+// before the others' (pieces of 4, 2 and 1 in a branch of their own: the norm's gradients of 2941 x 1789 took 24 us).
+template <typename T, int ROWS>
 struct Raw8;
 
-template <bool VEC>
-struct Raw8<uint16_t, VEC> {
+template <int ROWS>
+struct Raw8<uint16_t, ROWS> {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     u32x4 u;
+    int down;  // kAny: elements to move down by
     __device__ __forceinline__ void load(const uint16_t *p, int left) {
         u = u32x4{0, 0, 0, 0};
-        if constexpr (VEC) {
+        if constexpr (ROWS == kAligned) {
             if (left > 0) u = *reinterpret_cast<const u32x4 *>(p);
-        } else if (left >= 8) {
-            u = load_any<u32x4>(p);
-        } else if (left > 0) {  // 4 + 2 + 1 elements
-            if (left & 4) {
-                const uint64_t x = load_any<uint64_t>(p);
-                u[0] = (uint32_t)x, u[1] = (uint32_t)(x >> 32);
-            }
-            if (left & 2) {
-                const uint32_t x = load_any<uint32_t>(p + (left & 4));
-                if (left & 4) u[2] = x;
-                else u[0] = x;
-            }
-            if (left & 1) {
-                const uint32_t x = p[left & 6], w = left >> 1;
+        } else if constexpr (ROWS == kTiny) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) u[i] = w == i ? x : u[i];
-            }
+            for (int i = 0; i < 7; ++i)
+                if (i < left) u[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+        } else {
+            down = left < 8 && left > 0 ? 8 - left : 0;
+            if (left > 0) u = load_any<u32x4>(p - down);
         }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
+        u32x4 x = u;
+        if constexpr (ROWS == kAny) {
+            if (down & 4) x = u32x4{x[2], x[3], 0, 0};
+            if (down & 2) x = u32x4{x[1], x[2], x[3], 0};
+            if (down & 1) x = u32x4{x[0] >> 16 | x[1] << 16, x[1] >> 16 | x[2] << 16, x[2] >> 16 | x[3] << 16, x[3] >> 16};
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            v[2 * i] = __uint_as_float(x[i] << 16);
+            v[2 * i + 1] = __uint_as_float(x[i] & 0xffff0000u);
         }
     }
     // keeps the compiler from holding the floats (twice the registers) from one get() to the next
     __device__ __forceinline__ void forget() { asm volatile("" : "+v"(u)); }
 };
 
-template <bool VEC>
-struct Raw8<float, VEC> {
+template <int ROWS>
+struct Raw8<float, ROWS> {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
-    typedef float f32x2 __attribute__((ext_vector_type(2)));
     f32x4 a, b;
+    int down;
     __device__ __forceinline__ void load(const float *p, int left) {
         a = b = f32x4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (VEC) {
+        if constexpr (ROWS == kAligned) {
             if (left > 0) {
                 a = *reinterpret_cast<const f32x4 *>(p);
                 b = *reinterpret_cast<const f32x4 *>(p + 4);
             }
-        } else if (left >= 8) {
-            a = load_any<f32x4>(p);
-            b = load_any<f32x4>(p + 4);
-        } else if (left > 0) {
-            if (left & 4) a = load_any<f32x4>(p);
-            if (left & 2) {
-                const f32x2 x = load_any<f32x2>(p + (left & 4));
-                if (left & 4) b[0] = x[0], b[1] = x[1];
-                else a[0] = x[0], a[1] = x[1];
-            }
-            if (left & 1) {
-                const float x = p[left & 6];
-                const int w = left & 6;  // 0, 2, 4 or 6
-                a[0] = w == 0 ? x : a[0], a[2] = w == 2 ? x : a[2], b[0] = w == 4 ? x : b[0], b[2] = w == 6 ? x : b[2];
+        } else if constexpr (ROWS == kTiny) {
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < left) (i < 4 ? a : b)[i & 3] = p[i];
+        } else {
+            down = left < 8 && left > 0 ? 8 - left : 0;
+            if (left > 0) {
+                a = load_any<f32x4>(p - down);
+                b = load_any<f32x4>(p - down + 4);
             }
         }
     }
     __device__ __forceinline__ void get(float (&v)[8]) const {
+        f32x4 x = a, y = b;
+        if constexpr (ROWS == kAny) {
+            if (down & 4) x = y, y = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (down & 2) x = f32x4{x[2], x[3], y[0], y[1]}, y = f32x4{y[2], y[3], 0.f, 0.f};
+            if (down & 1) x = f32x4{x[1], x[2], x[3], y[0]}, y = f32x4{y[1], y[2], y[3], 0.f};
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+        for (int i = 0; i < 4; ++i) v[i] = x[i], v[4 + i] = y[i];
     }
     __device__ __forceinline__ void forget() {}
 };
 
-template <bool VEC, typename T>
+template <int ROWS, typename T>
 __device__ __forceinline__ void load8(const T *p, int left, float (&v)[8]) {
-    Raw8<T, VEC> r;
+    Raw8<T, ROWS> r;
     r.load(p, left);
     r.get(v);
 }
@@ -196,11 +198,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // Stores of eight elements, those from `left` on left out.  Ordinary ones where lanes do not fill whole lines.
-template <bool VEC>
+template <int ROWS>
 __device__ __forceinline__ void store8(uint16_t *p, int left, const float (&v)[8]) {
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     const u32x4 u = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-    if constexpr (VEC) {
+    if constexpr (ROWS == kAligned) {
         if (left > 0) stream_out(p, make_uint4(u[0], u[1], u[2], u[3]));
     } else if (left >= 8) {
         store_any(p, u);
@@ -211,12 +213,12 @@ __device__ __forceinline__ void store8(uint16_t *p, int left, const float (&v)[8
     }
 }
 
-template <bool VEC>
+template <int ROWS>
 __device__ __forceinline__ void store8(float *p, int left, const float (&v)[8]) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
     const f32x4 a = {v[0], v[1], v[2], v[3]}, b = {v[4], v[5], v[6], v[7]};
-    if constexpr (VEC) {
+    if constexpr (ROWS == kAligned) {
         if (left > 0) {
             *reinterpret_cast<f32x4 *>(p) = a;
             *reinterpret_cast<f32x4 *>(p + 4) = b;
@@ -232,15 +234,15 @@ __device__ __forceinline__ void store8(float *p, int left, const float (&v)[8]) 
 }
 
 // the same for a weight row whose type is known at run time only (NULL: ones)
-template <bool VEC>
+template <int ROWS>
 __device__ __forceinline__ void load_weight8(const void *w, int bf16, size_t i, int left, float (&v)[8]) {
     if (!w) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[e] = 1.f;
     } else if (bf16) {
-        load8<VEC>(static_cast<const uint16_t *>(w) + i, left, v);
+        load8<ROWS>(static_cast<const uint16_t *>(w) + i, left, v);
     } else {
-        load8<VEC>(static_cast<const float *>(w) + i, left, v);
+        load8<ROWS>(static_cast<const float *>(w) + i, left, v);
     }
 }
 
