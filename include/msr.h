@@ -380,7 +380,7 @@ msr_status msr_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, const void *x
  * dx (dtype) is the gradient of x and of the residual alike; it may be dy or
  * dsum.  Nothing else from the forward call is needed.  The sums over rows
  * run in a fixed order.  With a dweight it needs a workspace of
- * msr_add_rmsnorm_backward_workspace(rows, d) bytes.
+ * msr_add_rmsnorm_backward_workspace(rows, d) bytes (0 for few rows).
  */
 msr_status msr_add_rmsnorm_backward(int64_t rows, int32_t d, int32_t dtype, const void *h, const void *weight,
                                     int32_t weight_dtype, float eps, const void *dy, const void *dsum, void *dx,

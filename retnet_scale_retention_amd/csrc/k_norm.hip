@@ -9,7 +9,9 @@
 // A row is held in registers by W waves, V groups of 8 elements per lane:
 // group v of lane l of wave w starts at element 8 (64 (v W + w) + l), so a
 // wave reads contiguous kilobytes and a block of 128 is one row of 16 lanes
-// (its largest magnitude needs four lane-row rotations, no LDS).
+// (its largest magnitude needs four lane-row rotations, no LDS).  Rows of up
+// to 128 (256) elements, a head's for one, take L = 16 (32) lanes, four (two)
+// of them to a wave.
 //
 // Bound by memory: 16384 x 4096 bf16 with the residual's addition and 8-bit
 // output 70 us (6.7 TB/s of the 472 MB, part of them from the last-level
@@ -32,10 +34,23 @@ struct NormArgs {
     float eps;
 };
 
-// the sum over the W waves that share a row (team `tm` of the workgroup)
-template <int W>
+// the sum over the L lanes of a wave that share a row
+template <int L>
+__device__ __forceinline__ float lanes_sum(float x) {
+    if constexpr (L == 64) return wave_sum_dpp(x);
+    x = row16_sum(x);
+    if constexpr (L == 32) {
+        const uint32_t u = __float_as_uint(x);
+        const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+        x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+    }
+    return x;
+}
+
+// the sum over the W waves (of L lanes) that share a row (team `tm` of the workgroup)
+template <int W, int L>
 __device__ __forceinline__ float team_sum(float x, float *red, int tm, int w) {
-    x = wave_sum_dpp(x);
+    x = lanes_sum<L>(x);
     if constexpr (W > 1) {
         if ((threadIdx.x & 63) == 0) red[tm * W + w] = x;
         __syncthreads();
@@ -46,12 +61,14 @@ __device__ __forceinline__ float team_sum(float x, float *red, int tm, int w) {
     return x;
 }
 
-template <typename T, int ROWS, int W, int V>
+template <typename T, int ROWS, int W, int V, int L>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormArgs a) {
     constexpr int TEAMS = W < 4 ? 4 / W : 1;
+    static_assert(L == 64 || W * V == 1, "");
     __shared__ float red[TEAMS * W];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tm = wave / W, w = wave % W;
-    const int64_t row_raw = a.row0 + (int64_t)blockIdx.x * TEAMS + tm;
+    const int64_t row_raw = a.row0 + ((int64_t)blockIdx.x * TEAMS + tm) * (64 / L) + lane / L;
+    const int e0 = 8 * (64 * w + lane % L);  // group v starts at e0 + 512 W v
     const bool live = row_raw < a.rows;
     const int64_t row = live ? row_raw : a.rows - 1;  // a team past the end repeats the last row and stores nothing
     const T *x = static_cast<const T *>(a.x) + row * a.d;
@@ -60,13 +77,13 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
     float ss = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = 8 * (64 * (v * W + w) + lane);
+        const int e = e0 + 512 * W * v;
         load8<ROWS>(x + e, a.d - e, h[v]);
     }
     if (r) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = 8 * (64 * (v * W + w) + lane);
+            const int e = e0 + 512 * W * v;
             float t[8];
             load8<ROWS>(r + e, a.d - e, t);
 #pragma unroll
@@ -81,14 +98,14 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void add_rmsnorm_kernel(NormA
         T *s = static_cast<T *>(a.sum) + row * a.d;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            const int e = 8 * (64 * (v * W + w) + lane);
+            const int e = e0 + 512 * W * v;
             store8<ROWS>(s + e, a.d - e, h[v]);
         }
     }
-    const float rstd = 1.f / sqrtf(team_sum<W>(ss, red, tm, w) / (float)a.d + a.eps);
+    const float rstd = 1.f / sqrtf(team_sum<W, L>(ss, red, tm, w) / (float)a.d + a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        const int e = 8 * (64 * (v * W + w) + lane);
+        const int e = e0 + 512 * W * v;
         float g[8];
         load_weight8<ROWS>(a.w, a.w_bf16, e, a.d - e, g);
 #pragma unroll
@@ -123,15 +140,16 @@ struct NormBackArgs {
 // 16384 x 4096; without the loads ahead 216);
 // the workgroup's teams add up in LDS, its sum goes to `part`, and
 // column_sum_kernel adds the parts in a fixed order (no atomics).
-template <typename T, int ROWS, int W, int V>
+template <typename T, int ROWS, int W, int V, int L>
 __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(NormBackArgs a) {
-    constexpr int TEAMS = W < 4 ? 4 / W : 1;
+    constexpr int TEAMS = W < 4 ? 4 / W : 1, PER = 64 / L;  // teams of a workgroup, rows of a team at a time
+    static_assert(L == 64 || W * V == 1, "");
     __shared__ float red[2][2 * TEAMS * W];
     __shared__ float dws[TEAMS > 1 ? TEAMS - 1 : 1][TEAMS > 1 ? 512 * W * V : 1];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, tm = wave / W, w = wave % W;
-    const int64_t team = (int64_t)blockIdx.x * TEAMS + tm, teams = (int64_t)gridDim.x * TEAMS;
+    const int64_t team = ((int64_t)blockIdx.x * TEAMS + tm) * PER + lane / L, teams = (int64_t)gridDim.x * TEAMS * PER;
     const int64_t turns = (a.rows + teams - 1) / teams;  // the same for every team: the barriers match
-    const int e0 = 8 * (64 * w + lane);                  // group v starts at e0 + 512 W v
+    const int e0 = 8 * (64 * w + lane % L);              // group v starts at e0 + 512 W v
     // the longest rows are read a second time instead of kept, and their weight gradient stays in LDS (all in registers,
     // 276 of them spilled: 1024 x 32768 bf16 231 us)
     constexpr bool keep = W * V <= (ROWS == kAligned ? 32 : 16);
@@ -190,8 +208,8 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
                 gh = fmaf(h[i], g[i] * wt[v][i], gh);
             }
         }
-        ss = wave_sum_dpp(ss);
-        gh = wave_sum_dpp(gh);
+        ss = lanes_sum<L>(ss);
+        gh = lanes_sum<L>(gh);
         if constexpr (W > 1) {
             float *rd = red[t & 1];  // two areas: one barrier per turn separates a turn's reads from its writes
             if (lane == 0) {
@@ -256,6 +274,18 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
         if (keep && !early && t + 1 < turns) fetch(t + 1);
     }
     if (a.part) {
+        if constexpr (PER > 1) {  // the rows of a team
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                uint32_t u = __float_as_uint(dw[0][i]);
+                if constexpr (PER == 4) {
+                    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+                    u = __float_as_uint(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+                }
+                const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+                dw[0][i] = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+            }
+        }
         if constexpr (TEAMS > 1) {
             if (tm > 0) {
 #pragma unroll
@@ -272,6 +302,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 #pragma unroll
                     for (int i = 0; i < 8; ++i) dw[v][i] += dws[q][(v * W + w) * 512 + i * 64 + lane];
         }
+        if (lane >= L) return;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = e0 + 512 * W * v;
@@ -322,7 +353,10 @@ __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, floa
     }
 }
 
-// (waves, groups per lane) that hold a row of d <= 512 W V values.  Twice the
+template <int N>
+using C = std::integral_constant<int, N>;
+
+// (waves, groups per lane, lanes of a wave) that hold a row of d <= 8 L W V values.  Twice the
 // waves with one group each (ONE) suit the gradients (16384 x 4096: 93 us
 // against 98, f32 16384 x 2048 94 against 101) and f32 forwards (77 against
 // 79), whose lanes have 32 bytes of each array under way all the same; bf16
@@ -330,23 +364,22 @@ __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, floa
 template <bool ONE, typename F>
 hipError_t by_width(int d, F f) {
     constexpr int m = ONE ? 2 : 1;
-    using V = std::integral_constant<int, 2 / m>;
-    if (d <= 512) return f(std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
-    if (d <= 1024) return f(std::integral_constant<int, m>(), V());
-    if (d <= 2048) return f(std::integral_constant<int, 2 * m>(), V());
-    if (d <= 4096) return f(std::integral_constant<int, 4 * m>(), V());
-    if (d <= 8192) return f(std::integral_constant<int, 8 * m>(), V());
-    if (d <= 16384) return f(std::integral_constant<int, 8>(), std::integral_constant<int, 4>());
-    return f(std::integral_constant<int, 16>(), std::integral_constant<int, 4>());
+    if (d <= 128) return f(C<1>(), C<1>(), C<16>());
+    if (d <= 256) return f(C<1>(), C<1>(), C<32>());
+    if (d <= 512) return f(C<1>(), C<1>(), C<64>());
+    if (d <= 1024) return f(C<m>(), C<2 / m>(), C<64>());
+    if (d <= 2048) return f(C<2 * m>(), C<2 / m>(), C<64>());
+    if (d <= 4096) return f(C<4 * m>(), C<2 / m>(), C<64>());
+    if (d <= 8192) return f(C<8 * m>(), C<2 / m>(), C<64>());
+    if (d <= 16384) return f(C<8>(), C<4>(), C<64>());
+    return f(C<16>(), C<4>(), C<64>());
 }
 
 template <bool ONE, typename T, typename F>
 hipError_t by_rows(int d, F f) {
-    if (d % 8 == 0)
-        return by_width<ONE>(d, [&](auto W, auto V) { return f(T(), std::integral_constant<int, kAligned>(), W, V); });
-    if (d > 8)
-        return by_width<ONE>(d, [&](auto W, auto V) { return f(T(), std::integral_constant<int, kAny>(), W, V); });
-    return f(T(), std::integral_constant<int, kTiny>(), std::integral_constant<int, 1>(), std::integral_constant<int, 1>());
+    if (d % 8 == 0) return by_width<ONE>(d, [&](auto... c) { return f(T(), C<kAligned>(), c...); });
+    if (d > 8) return by_width<ONE>(d, [&](auto... c) { return f(T(), C<kAny>(), c...); });
+    return f(T(), C<kTiny>(), C<1>(), C<1>(), C<16>());
 }
 
 // Workgroups of the backward pass: each writes one partial weight gradient.
@@ -354,12 +387,16 @@ hipError_t by_rows(int d, F f) {
 // they are longer: about 6 MB under way in both cases (512 x bf16: 43 us
 // against 52 for 65536 rows, but 4096 x bf16 100 against 93 for 16384); about
 // one per eight rows but no fewer than the CUs (few rows: the parts' own bytes
-// count), evened out so that all walk over equally many rows.
+// count), evened out so that all walk over equally many rows.  A few turns of
+// one workgroup go straight into the weight gradient instead of a second
+// launch (bf16, 32 x 512 7.1 us against 11.5, 8 x 4096 9.6 against 11.7, but
+// 12 x 4096 13.3 and 8 x 16384 21).
 constexpr int kBackGroups = 512;
 
 int back_groups(int64_t rows, int d, int dtype) {
     if (rows == 0) return 0;
-    const int64_t teams = d <= 512 ? 4 : d <= 1024 ? 2 : 1;  // as by_width's kernels have
+    const int64_t teams = d <= 128 ? 16 : d <= 256 ? 8 : d <= 512 ? 4 : d <= 1024 ? 2 : 1;  // rows at a time, by_width
+    if (rows <= std::min(8, std::max(MSR_MAX_NORM_DIM / d, 1)) * teams) return 1;
     const int64_t most = teams * d * (dtype == MSR_BF16 ? 2 : 4) <= 4096 ? kBackGroups : kBackGroups / 2;
     const int64_t g = std::min<int64_t>((rows + teams - 1) / teams, std::min<int64_t>(std::max<int64_t>(rows / 8, 256), most));
     const int64_t turns = std::max<int64_t>((rows + g * teams / 2) / (g * teams), 1);
@@ -371,13 +408,13 @@ int back_groups(int64_t rows, int d, int dtype) {
 hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, const void *r, const void *w, int w_dtype,
                               float eps, void *sum, void *y, void *q, float *qs, hipStream_t st) {
     NormArgs a{x, r, w, sum, y, static_cast<uint8_t *>(q), qs, 0, rows, d, (int)round128(d), w_dtype == MSR_BF16, eps};
-    auto launch = [&](auto t, auto rw, auto W, auto V) {
-        constexpr int teams = W.value < 4 ? 4 / W.value : 1, nt = W.value < 4 ? 256 : 64 * W.value;
+    auto launch = [&](auto t, auto rw, auto W, auto V, auto L) {
+        constexpr int teams = (W.value < 4 ? 4 / W.value : 1) * (64 / L.value), nt = W.value < 4 ? 256 : 64 * W.value;
         constexpr int64_t most = (int64_t)1 << 21;  // workgroups of a launch: its threads stay below 2^32
         hipError_t e = hipSuccess;
         for (a.row0 = 0; a.row0 < rows && e == hipSuccess; a.row0 += most * teams) {
             const int64_t g = std::min<int64_t>((rows - a.row0 + teams - 1) / teams, most);
-            hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(t), rw.value, W.value, V.value>), dim3((unsigned)g), dim3(nt),
+            hipLaunchKernelGGL((add_rmsnorm_kernel<decltype(t), rw.value, W.value, V.value, L.value>), dim3((unsigned)g), dim3(nt),
                                0, st, a);
             e = hipGetLastError();
         }
@@ -386,24 +423,25 @@ hipError_t launch_add_rmsnorm(int64_t rows, int d, int dtype, const void *x, con
     return dtype == MSR_BF16 ? by_rows<false, uint16_t>(d, launch) : by_rows<true, float>(d, launch);
 }
 
-// enough for either type
+// enough for either type; none for a single part, which is the weight gradient itself
 size_t rmsnorm_backward_workspace(int64_t rows, int d) {
-    return (size_t)std::max(back_groups(rows, d, MSR_BF16), back_groups(rows, d, MSR_F32)) * d * sizeof(float);
+    const int parts = std::max(back_groups(rows, d, MSR_BF16), back_groups(rows, d, MSR_F32));
+    return parts > 1 ? (size_t)parts * d * sizeof(float) : 0;
 }
 
 hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h, const void *w, int w_dtype, float eps,
                                    const void *dy, const void *dsum, void *dx, float *dw, float *part, hipStream_t st) {
     const int parts = back_groups(rows, d, dtype);
-    const NormBackArgs a{h, w, dy, dsum, dx, dw ? part : nullptr, rows, d, w_dtype == MSR_BF16, eps};
-    auto launch = [&](auto t, auto rw, auto W, auto V) {
+    const NormBackArgs a{h, w, dy, dsum, dx, dw ? (parts > 1 ? part : dw) : nullptr, rows, d, w_dtype == MSR_BF16, eps};
+    auto launch = [&](auto t, auto rw, auto W, auto V, auto L) {
         constexpr int nt = W.value < 4 ? 256 : 64 * W.value;
-        hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), rw.value, W.value, V.value>), dim3(parts), dim3(nt), 0, st,
-                           a);
+        hipLaunchKernelGGL((rmsnorm_backward_kernel<decltype(t), rw.value, W.value, V.value, L.value>), dim3(parts),
+                           dim3(nt), 0, st, a);
         return hipGetLastError();
     };
     hipError_t e = hipSuccess;
     if (parts > 0) e = dtype == MSR_BF16 ? by_rows<true, uint16_t>(d, launch) : by_rows<true, float>(d, launch);
-    if (e == hipSuccess && dw) {
+    if (e == hipSuccess && dw && parts != 1) {
         hipLaunchKernelGGL(column_sum_kernel, dim3((d + 31) / 32), dim3(512), 0, st, part, dw, parts, d);
         e = hipGetLastError();
     }

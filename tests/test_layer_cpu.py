@@ -101,9 +101,10 @@ def test_norm_refusals():
 def test_norm_backward_refusals():
     lib = msr.load()
     f = lib.msr_add_rmsnorm_backward
-    need = lib.msr_add_rmsnorm_backward_workspace(4, 512)
-    assert need > 0 and lib.msr_add_rmsnorm_backward_workspace(4, 0) == 0
-    ok = [4, 512, 1, A, NULL, 0, 1e-6, B, NULL, C, D, E, need, NULL]
+    need = lib.msr_add_rmsnorm_backward_workspace(33, 512)
+    assert need > 0 and lib.msr_add_rmsnorm_backward_workspace(33, 0) == 0
+    assert lib.msr_add_rmsnorm_backward_workspace(32, 512) == 0  # one workgroup: no partial gradients
+    ok = [33, 512, 1, A, NULL, 0, 1e-6, B, NULL, C, D, E, need, NULL]
 
     def call(**kw):
         v = list(ok)
