@@ -302,6 +302,28 @@ __device__ __forceinline__ void tile_body(const MatArgs &a) {
 #pragma unroll
             for (int t = 0; t < TM * TN; ++t) acc[t / TN][t % TN] += red[((q * NW + wv) * TM * TN + t) * 64 + lane];
     }
+    if constexpr (sizeof(OUT) == 2 && TN % 2 == 0) {
+        // 16 bytes per lane, 64 of a row, after a lane swap (8 and 32 without: 16384 x 16384 x 256 238 us instead of 181,
+        // 2000 x 1544 x 512 7.0 instead of 6.5); no faster where rows start anywhere
+        if (a.N % 8 == 0) {
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int m = m0 + ar + 16 * i + l16;
+#pragma unroll
+                for (int j = 0; j < TN; j += 2) {
+                    // lanes of even g take tile j, of odd g tile j + 1: features 8 (g / 2) .. + 7 of it
+                    const f32x4 v = acc[i][j], w = acc[i][j + 1];
+                    const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0], v[1]), pack_bf16(w[0], w[1]), false, false);
+                    const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2], v[3]), pack_bf16(w[2], w[3]), false, false);
+                    const int n = n0 + br + 16 * (j + (g & 1)) + 8 * (g >> 1);
+                    if (m < a.M && n < a.N)
+                        *reinterpret_cast<u32x4 *>(static_cast<OUT *>(a.out) + (size_t)m * a.N + n) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                }
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int m = m0 + ar + 16 * i + l16;
@@ -667,43 +689,43 @@ __global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_bod
 // A kernel's time is close to max(f0 + f1 nkb, T (t0 + t1 nkb)): a lone
 // tile's latency, and the chip's throughput over T tiles, T rounded up to
 // what fills the CUs evenly.  The constants (us) are least-squares fits to
-// times over 480 random sizes (9 .. 16384 tokens, 64 .. 16384 features, a
+// times over 600 random sizes (9 .. 16384 tokens, 64 .. 16384 features, a
 // contraction of 256 .. 16384; B by rows and by squares alike), for bf16 and
-// for fp32 output; taking the smallest costs 1.2% over the best kernel of each
-// size.  Groups of waves that share a tile's blocks, and stages further ahead,
-// pay where there are few tiles; small LDS, so more workgroups per CU, where
-// there are many.  Times in us, bf16 output (32 x 32 by four groups | by one
-// | 32 x 64 | 64 x 64 by two | by one | 128 x 64 | 128 x 128 | 128 x 64 with
-// four stages | 256 x 256):
-//   64 x 4096 x 4096        6.0 |  8.5 |  7.8 | 10.3 |      |      |      | 15.0 |
-//   64 x 8192 x 4096       12.5 | 11.0 |  8.9 | 11.8 |      |      |      | 16.5 |
-//   100 x 8192 x 4096      20.5 | 16.1 | 12.5 | 11.8 |      |      |      | 16.9 |
-//   256 x 8192 x 4096      44.9 | 33.4 | 24.6 | 22.9 | 22.5 | 25.9 | 27.9 | 19.4 |  47
-//   4096 x 2048 x 2048      112 |   62 |   51 |   51 |   38 |   30 |   24 |   38 |  31
-//   4096 x 4096 x 4096      338 |  220 |  167 |  162 |  134 |  105 |   84 |  136 |  67
-//   16384 x 8192 x 4096    2620 | 1740 | 1320 | 1290 | 1040 |  868 |  648 | 1070 | 481
+// for fp32 output; taking the smallest costs 1.8% (1.0%) over the best kernel
+// of each size.  Groups of waves that share a tile's blocks, and stages
+// further ahead, pay where there are few tiles; small LDS, so more workgroups
+// per CU, where there are many.  Times in us, bf16 output (32 x 32 by four
+// groups | by one | 32 x 64 | 64 x 64 by two | by one | 128 x 64 | 128 x 128
+// | 128 x 64 with four stages | 256 x 256):
+//   64 x 4096 x 4096        6.7 |  9.2 |  8.3 | 10.7 | 12.9 | 15.6 | 21.9 | 15.4 |  45
+//   64 x 8192 x 4096       12.9 | 11.2 |  9.2 | 12.0 | 19.9 | 22.3 | 25.0 | 16.6 |  45
+//   100 x 8192 x 4096      21.3 | 16.5 | 13.1 | 12.4 | 19.6 | 23.2 | 25.8 | 17.0 |  45
+//   256 x 8192 x 4096      43.6 | 32.5 | 24.2 | 22.9 | 21.8 | 25.6 | 27.1 | 19.0 |  47
+//   4096 x 2048 x 2048      113 |   61 |   49 |   50 |   37 |   29 |   23 |   37 |  30
+//   4096 x 4096 x 4096      328 |  217 |  164 |  159 |  133 |  102 |   78 |  136 |  65
+//   16384 x 8192 x 4096    2609 | 1722 | 1303 | 1273 | 1039 |  834 |  598 | 1052 | 459
 struct Fit {
     int rows, cols, round;
     double f0, f1, t0, t1;
 };
 // the last two are for bf16 output alone
 constexpr int kConfigs = 9;
-constexpr Fit kFit[2][kConfigs] = {{{32, 32, 256, 3.04, 0.0956, 0.00824, 0.000466},
-                                    {32, 32, 256, 2.62, 0.186, 0.00194, 0.000498},
-                                    {32, 64, 256, 2.89, 0.166, 0.00486, 0.00069},
-                                    {64, 64, 256, 3.33, 0.22, 0.00872, 0.00109},
-                                    {64, 64, 256, 2.58, 0.294, 0.0029, 0.00109},
-                                    {128, 64, 256, 2.43, 0.545, 0.00623, 0.00153},
-                                    {128, 128, 256, 4.34, 0.747, 0.0116, 0.00227},
-                                    {128, 64, 256, 3.28, 0.447, 0.0114, 0.00186},
-                                    {256, 256, 256, 9.42, 1.51, 0.0322, 0.00594}},
-                                   {{32, 32, 256, 3.05, 0.127, 0.00853, 0.000532},
-                                    {32, 32, 512, 2.47, 0.319, 0.00266, 0.00048},
-                                    {32, 64, 256, 2.99, 0.236, 0.00615, 0.000751},
-                                    {64, 64, 256, 3.35, 0.35, 0.0109, 0.0014},
-                                    {64, 64, 256, 2.67, 0.446, 0.00577, 0.00119},
-                                    {128, 64, 256, 3.29, 0.731, 0.00863, 0.00206},
-                                    {128, 128, 256, 4.99, 1.08, 0.0121, 0.00347},
+constexpr Fit kFit[2][kConfigs] = {{{32, 32, 256, 3, 0.0938, 0.00793, 0.000448},
+                                    {32, 32, 256, 2.55, 0.192, 0.00197, 0.000487},
+                                    {32, 64, 256, 2.79, 0.168, 0.00498, 0.000628},
+                                    {64, 64, 256, 3.25, 0.213, 0.00868, 0.00107},
+                                    {64, 64, 256, 2.5, 0.279, 0.00217, 0.00105},
+                                    {128, 64, 256, 2.26, 0.532, 0.00448, 0.00155},
+                                    {128, 128, 256, 3.3, 0.737, 0.00873, 0.00229},
+                                    {128, 64, 256, 3.14, 0.431, 0.0103, 0.00182},
+                                    {256, 256, 256, 9.53, 1.59, 0.0319, 0.00664}},
+                                   {{32, 32, 256, 3.03, 0.127, 0.00864, 0.000543},
+                                    {32, 32, 512, 2.48, 0.328, 0.00269, 0.000454},
+                                    {32, 64, 256, 2.92, 0.249, 0.00615, 0.000716},
+                                    {64, 64, 256, 3.3, 0.358, 0.0115, 0.00134},
+                                    {64, 64, 256, 2.61, 0.457, 0.00588, 0.00118},
+                                    {128, 64, 256, 3.36, 0.713, 0.00979, 0.00203},
+                                    {128, 128, 256, 4.84, 1.09, 0.0154, 0.00335},
                                     {},
                                     {}}};
 

@@ -331,8 +331,10 @@ def test_scaled_matmul_positions(out):
 
 
 # the larger tiles: 32 x 64, 64 x 64, 128 x 64 (four stages, two stages), 128 x 128, 256 x 256, with ends inside a tile
-LSIZES = [(700, 701, 2048), (90, 8190, 1152), (70, 8190, 2048), (1000, 1100, 4096), (300, 6001, 512), (1025, 1990, 256), (250, 8184, 4096), (2040, 1545, 640), (4101, 4100, 512),
-          (2561, 2050, 1024), (3001, 4100, 256), (4010, 8200, 512), (4010, 8200, 640), (8300, 8200, 1024), (3000, 5003, 640), (4099, 8194, 1152)]
+LSIZES = [(700, 701, 2048), (704, 704, 2048), (90, 8190, 1152), (70, 8190, 2048), (70, 8192, 2048), (1000, 1100, 4096),
+          (300, 6001, 512), (1025, 1990, 256), (1025, 1992, 256), (250, 8184, 4096), (2040, 1545, 640), (2040, 1544, 640),
+          (4101, 4100, 512), (4101, 4104, 512), (2561, 2050, 1024), (3001, 4100, 256), (3000, 5003, 640),
+          (4010, 8200, 640), (5000, 8200, 640), (3000, 8200, 1024), (3001, 8195, 2176), (8300, 8203, 1152)]
 
 
 def product64(qa, sa, qb, sb, block):
@@ -380,7 +382,7 @@ def test_scaled_matmul_large_tiles_positions(m, n, k):
             assert torch.equal(msr.msr_scaled_matmul(qa, sa, qb, sb, out_dtype=dt), r.float().to(dt)), (block, dt)
 
 
-@pytest.mark.parametrize("m,n,k", [(2040, 1545, 640), (2561, 2050, 1024), (4010, 8200, 512)])
+@pytest.mark.parametrize("m,n,k", [(2040, 1545, 640), (2561, 2050, 1024), (5000, 8200, 512), (3001, 8195, 1152)])
 def test_scaled_matmul_large_tiles_non_finite(m, n, k):
     torch, dev = torch_dev()
     msr = _msr()
