@@ -147,6 +147,15 @@ __device__ __forceinline__ void store_row4(OUT *row, int n, int N, f32x4 v) {
     }
 }
 
+// Results v, w of two neighbouring column tiles as bf16: lanes of even g get eight features of the first tile, of odd g
+// of the second, 8 (g / 2) .. + 7.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ u32x4 pack_pair(f32x4 v, f32x4 w) {
+    const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0], v[1]), pack_bf16(w[0], w[1]), false, false);
+    const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2], v[3]), pack_bf16(w[2], w[3]), false, false);
+    return u32x4{lo[0], hi[0], lo[1], hi[1]};
+}
+
 // Tile id -> (row tile, column tile).  Ids are dealt round-robin over the 8
 // XCDs; each takes a contiguous range of an order in which groups of 8 row
 // tiles sweep the column tiles, so what runs together on an XCD shares rows
@@ -303,22 +312,18 @@ __device__ __forceinline__ void tile_body(const MatArgs &a) {
             for (int t = 0; t < TM * TN; ++t) acc[t / TN][t % TN] += red[((q * NW + wv) * TM * TN + t) * 64 + lane];
     }
     if constexpr (sizeof(OUT) == 2 && TN % 2 == 0) {
-        // 16 bytes per lane, 64 of a row, after a lane swap (8 and 32 without: 16384 x 16384 x 256 238 us instead of 181,
-        // 2000 x 1544 x 512 7.0 instead of 6.5); no faster where rows start anywhere
+        // 16 bytes per lane, 64 of a row, after a lane swap (8 and 32 without: 16384 x 16384 x 256 238 us instead of
+        // 181, 2000 x 1544 x 512 7.0 instead of 6.5); no faster where rows start anywhere
         if (a.N % 8 == 0) {
-            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int m = m0 + ar + 16 * i + l16;
+                OUT *row = static_cast<OUT *>(a.out) + (size_t)m * a.N;
 #pragma unroll
                 for (int j = 0; j < TN; j += 2) {
-                    // lanes of even g take tile j, of odd g tile j + 1: features 8 (g / 2) .. + 7 of it
-                    const f32x4 v = acc[i][j], w = acc[i][j + 1];
-                    const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0], v[1]), pack_bf16(w[0], w[1]), false, false);
-                    const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2], v[3]), pack_bf16(w[2], w[3]), false, false);
+                    const u32x4 x = pack_pair(acc[i][j], acc[i][j + 1]);
                     const int n = n0 + br + 16 * (j + (g & 1)) + 8 * (g >> 1);
-                    if (m < a.M && n < a.N)
-                        *reinterpret_cast<u32x4 *>(static_cast<OUT *>(a.out) + (size_t)m * a.N + n) = u32x4{lo[0], hi[0], lo[1], hi[1]};
+                    if (m < a.M && n < a.N) *reinterpret_cast<u32x4 *>(row + n) = x;
                 }
             }
             return;
@@ -370,7 +375,8 @@ __device__ __forceinline__ void stream_body(const MatArgs &a) {
         bp[j] = a.b + (size_t)min(n0 + 16 * j + l16, a.N - 1) * a.K + 16 * g;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-            sbp[j][r] = a.sb + (BROW ? (size_t)min(n0 + 16 * j + 4 * g + r, a.N - 1) : (size_t)(min(n0 + 16 * j, a.N - 1) >> 7)) * a.nkb;
+            sbp[j][r] = a.sb + (size_t)a.nkb * (BROW ? min(n0 + 16 * j + 4 * g + r, a.N - 1)
+                                                     : min(n0 + 16 * j, a.N - 1) >> 7);
     }
     f32x4 acc[MT][NT];
 #pragma unroll
@@ -478,7 +484,6 @@ struct BigTile {
 template <bool BROW>
 __device__ __forceinline__ void big_body(const MatArgs &a) {
     constexpr int BM = 256, BN = 256, NW = 8, TM = 4, TN = 8, LAG = 2, AHEAD = 3;
-    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     __shared__ __attribute__((aligned(1024))) char As0[BM * 128];
     __shared__ __attribute__((aligned(1024))) char As1[BM * 128];
     __shared__ __attribute__((aligned(1024))) char Bs0[BN * 128];
@@ -515,7 +520,8 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
         const int part = (wv & 1) + (wv >> 2) * 2;  // of four waves
         xo = (pulls_a ? 16 * part + (lane & 15) : 8 * part + (lane & 7)) * K;
     }
-    const auto ry = wv < 4 ? rsrc(a.sa, (uint32_t)((size_t)a.M * nkb * 4)) : rsrc(a.sb, (uint32_t)((size_t)a.N * nkb * 4));
+    const auto ry = wv < 4 ? rsrc(a.sa, (uint32_t)((size_t)a.M * nkb * 4))
+                           : rsrc(a.sb, (uint32_t)((size_t)a.N * nkb * 4));
     const int yo = (64 * (wv & 3) + lane) * nkb * 4;
     const int xstep = scales ? 4 : 128, xahead = scales ? 2 : AHEAD;
     auto xbase = [&](const BigTile &x) __attribute__((always_inline)) {
@@ -547,7 +553,8 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
         if constexpr (BROW) {
             const int ks = max(kb + 2, 0);
             const bool past = ks >= nkb;
-            load_lds4(ry, reinterpret_cast<char *>(&Ss[(gs + 2) & (RING - 1)][64 * wv]), yo, (past ? s1 : s0) + (past ? ks - nkb : ks) * 4);
+            load_lds4(ry, reinterpret_cast<char *>(&Ss[(gs + 2) & (RING - 1)][64 * wv]), yo,
+                      (past ? s1 : s0) + (past ? ks - nkb : ks) * 4);
         }
         load_lds4(rx, reinterpret_cast<char *>(dst), xo, (over ? x1 : x0) + (over ? kk - nkb : kk) * xstep);
     };
@@ -604,7 +611,8 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
             if constexpr (BROW) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    sb[ph & 1][j] = *reinterpret_cast<const f32x4 *>(&Ss[gs & (RING - 1)][BM + br + 16 * (2 * ph + j) + 4 * g]);
+                    sb[ph & 1][j] =
+                        *reinterpret_cast<const f32x4 *>(&Ss[gs & (RING - 1)][BM + br + 16 * (2 * ph + j) + 4 * g]);
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j)
@@ -637,19 +645,17 @@ __device__ __forceinline__ void big_body(const MatArgs &a) {
         ++kb;
     };
     auto tile_end = [&]() __attribute__((always_inline)) {
-        const auto ro = rsrc(static_cast<uint16_t *>(a.out) + (size_t)cur.m0 * a.N, (uint32_t)(min(BM, a.M - cur.m0) * a.N * 2));
+        const auto ro = rsrc(static_cast<uint16_t *>(a.out) + (size_t)cur.m0 * a.N,
+                             (uint32_t)(min(BM, a.M - cur.m0) * a.N * 2));
         if (a.N % 8 == 0) {
 #pragma unroll
             for (int i = 0; i < TM; ++i)
 #pragma unroll
                 for (int j = 0; j < TN; j += 2) {
-                    // lanes of even g take tile j, of odd g tile j + 1: features 8 (g / 2) .. + 7 of it
-                    const f32x4 v = acc[i][j], w = acc[i][j + 1];
-                    const auto lo = __builtin_amdgcn_permlane16_swap(pack_bf16(v[0], v[1]), pack_bf16(w[0], w[1]), false, false);
-                    const auto hi = __builtin_amdgcn_permlane16_swap(pack_bf16(v[2], v[3]), pack_bf16(w[2], w[3]), false, false);
+                    const u32x4 x = pack_pair(acc[i][j], acc[i][j + 1]);
                     const int m = ar + 16 * i + l16, n = cur.n0 + br + 16 * (j + (g & 1)) + 8 * (g >> 1);
-                    const int off = n < a.N ? (m * a.N + n) * 2 : 0x7fffffff;  // rows and columns past the end are dropped
-                    __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, off, 0, 0);
+                    const int off = n < a.N ? (m * a.N + n) * 2 : 0x7fffffff;  // rows, columns past the end: dropped
+                    __builtin_amdgcn_raw_buffer_store_b128(x, ro, off, 0, 0);
                 }
         } else {  // rows that start anywhere
 #pragma unroll

@@ -137,7 +137,8 @@ msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, con
     if (m < 0 || n < 0 || k < 0 || m > INT32_MAX - 1024 || n > INT32_MAX - 1024 || k > INT32_MAX)
         return set_error(MSR_ERR_SHAPE, "m=%lld, n=%lld, k=%lld outside 0..2^31-1025", (long long)m, (long long)n,
                          (long long)k);
-    if (k > (1 << 24) - MSR_BLOCK) return set_error(MSR_ERR_SHAPE, "k=%lld exceeds 2^24 - 128", (long long)k);  // 32-bit offsets within a tile
+    // 32-bit offsets within a tile
+    if (k > (1 << 24) - MSR_BLOCK) return set_error(MSR_ERR_SHAPE, "k=%lld exceeds 2^24 - 128", (long long)k);
     if (k % MSR_BLOCK) return set_error(MSR_ERR_SHAPE, "k=%lld must be a multiple of %d", (long long)k, MSR_BLOCK);
     if (b_block_rows != 1 && b_block_rows != MSR_BLOCK)
         return set_error(MSR_ERR_INVALID_ARG, "b_block_rows=%d is neither 1 nor %d", b_block_rows, MSR_BLOCK);

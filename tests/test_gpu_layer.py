@@ -62,7 +62,9 @@ def check_blocks(q, s, x, block_rows, err, name):
 
 SIZES = [(1, 1), (1, 64), (3, 128), (5, 136), (64, 200), (7, 511), (130, 512), (9, 1000), (33, 1024), (6, 2047),
          (17, 2048), (5, 4096), (3, 4100), (4, 8192), (2, 16384), (2, 20001), (1, 32768),
-         (9, 2), (10, 6), (11, 517), (300, 1002), (5, 2067), (4, 6006), (3, 16381), (1001, 128), (67, 256), (1003, 86), (21, 130)]  # rows that end 2, 3, 5 or 6 past a group
+         # rows that end 2, 3, 5 or 6 past a group of eight, and rows that share a wave
+         (9, 2), (10, 6), (11, 517), (300, 1002), (5, 2067), (4, 6006), (3, 16381), (1001, 128), (67, 256), (1003, 86),
+         (21, 130)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -133,8 +135,9 @@ def test_add_rmsnorm_zero_tiny_and_non_finite_rows(d):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,d", SIZES + [(2500, 64), (1200, 520), (700, 4096), (64, 100), (65, 128), (33, 129), (32, 256), (3001, 256),
-                                          (5001, 86), (16, 300), (17, 512), (4, 4096), (8, 1024), (9, 1024)])
+@pytest.mark.parametrize("rows,d", SIZES + [(2500, 64), (1200, 520), (700, 4096), (64, 100), (65, 128), (33, 129),
+                                            (32, 256), (3001, 256), (5001, 86), (16, 300), (17, 512), (4, 4096),
+                                            (8, 1024), (9, 1024)])
 def test_add_rmsnorm_backward(rows, d, dtype):
     torch, dev = torch_dev()
     msr = _msr()
