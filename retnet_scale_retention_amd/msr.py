@@ -161,6 +161,21 @@ def _stream(t, stream):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _empty(shape, dtype, device, stream, kept=True):
+    """Memory that a call on `stream` (None: the current one) writes, taken from that stream's pool: a block of the current
+    stream's pool could still be in use there when `stream` writes it, and a workspace of that pool would go back to it on
+    return, to be handed out again while `stream` still uses it.  `kept`: the caller gets it, and may drop it while the
+    current stream still reads it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if kept:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _prep(q, k, v):
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not t.is_cuda or not t.is_contiguous():
@@ -192,14 +207,14 @@ def _form(fn, form, q, k, v, gamma, chunk, theta, scale, eps, pos0, flags, state
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, form, chunk, ctypes.byref(n)))
     if workspace is None or workspace.numel() < n.value:
-        workspace = torch.empty(max(int(n.value), 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty((max(int(n.value), 1),), torch.uint8, q.device, stream, kept=False)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=q.device)
+        out = _empty((B, T, H, dv), q.dtype, q.device, stream)
     if state_in is not None and (state_in.dtype != torch.float32 or not state_in.is_contiguous()
                                  or tuple(state_in.shape) != (B, H, dk, dv)):
         raise ValueError("state_in must be a contiguous float32 [B, H, dk, dv] tensor")
     if state_out is None and return_state:
-        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        state_out = _empty((B, H, dk, dv), torch.float32, q.device, stream)
     args = [d.ref]
     if form == MSR_FORM_CHUNKWISE:
         args.append(int(chunk))
@@ -270,9 +285,9 @@ def msr_chunkwise_backward(q, k, v, gamma, chunk, grad_out, *, grad_state=None, 
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, MSR_FORM_BACKWARD, chunk, ctypes.byref(n)))
     if workspace is None or workspace.numel() < n.value:
-        workspace = torch.empty(max(int(n.value), 1), dtype=torch.uint8, device=q.device)
-    dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ds = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device) if want_state_grad else None
+        workspace = _empty((max(int(n.value), 1),), torch.uint8, q.device, stream, kept=False)
+    dq, dk_, dv_ = (_empty(t.shape, t.dtype, t.device, stream) for t in (q, k, v))
+    ds = _empty((B, H, dk, dv), torch.float32, q.device, stream) if want_state_grad else None
     _check(load().msr_chunkwise_backward(d.ref, int(chunk), _ptr(q), _ptr(k), _ptr(v), _ptr(state_in),
                                          _ptr(grad_out), _ptr(grad_state), _ptr(dq), _ptr(dk_), _ptr(dv_),
                                          _ptr(ds), _ptr(workspace), ctypes.c_size_t(workspace.numel()),
@@ -296,14 +311,11 @@ def msr_qkv_projection(x, wq, wk, wv, H, *, theta=None, scale=0.0, pos0=0, flags
                        out=None, stream=None):
     """Q = R(x wq^T), K = s R(x wk^T), V = x wv^T as [B, T, H, d] bf16
     (x [B, T, d_model] bf16, weights [H d, d_model]).  Returns (Q, K, V)."""
-    torch = _torch()
     B, T, dm, dk, dv = _qkv_args(x, wq, wk, wv, H)
     d = _Desc(B, T, H, dk, dv, _dtype_code(x), np.ones(H, np.float32), theta, scale, 1e-5, pos0, flags,
               _pos_rows(pos_rows, B, x.device))
     if out is None:
-        out = (torch.empty((B, T, H, dk), dtype=x.dtype, device=x.device),
-               torch.empty((B, T, H, dk), dtype=x.dtype, device=x.device),
-               torch.empty((B, T, H, dv), dtype=x.dtype, device=x.device))
+        out = tuple(_empty((B, T, H, w), x.dtype, x.device, stream) for w in (dk, dk, dv))
     _check(load().msr_qkv_projection(d.ref, int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv),
                                      *(_ptr(t) for t in out), _stream(x, stream)))
     return out
@@ -322,11 +334,11 @@ def msr_qkv_chunkwise(x, wq, wk, wv, gamma, chunk, *, theta=None, scale=0.0, eps
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, MSR_FORM_QKV_CHUNKWISE, chunk, ctypes.byref(n)))
     if workspace is None or workspace.numel() < n.value:
-        workspace = torch.empty(max(int(n.value), 1), dtype=torch.uint8, device=x.device)
+        workspace = _empty((max(int(n.value), 1),), torch.uint8, x.device, stream, kept=False)
     if out is None:
-        out = torch.empty((B, T, H, dv), dtype=x.dtype, device=x.device)
+        out = _empty((B, T, H, dv), x.dtype, x.device, stream)
     if state_out is None and return_state:
-        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=x.device)
+        state_out = _empty((B, H, dk, dv), torch.float32, x.device, stream)
     _check(load().msr_qkv_chunkwise(d.ref, int(chunk), int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv),
                                     _ptr(out), _ptr(state_in), _ptr(state_out), _ptr(workspace),
                                     ctypes.c_size_t(workspace.numel()), _stream(x, stream)))
@@ -353,7 +365,7 @@ def msr_recurrent_step(q, k, v, state, gamma, pos, *, theta=None, scale=0.0, eps
     else:
         d = _Desc(B, 1, H, dk, dv, _dtype_code(q), gamma, theta, scale, eps, pos, flags)
     if out is None:
-        out = torch.empty((B, H, dv), dtype=q.dtype, device=q.device)
+        out = _empty((B, H, dv), q.dtype, q.device, stream)
     _check(load().msr_recurrent_step(d.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state),
                                      _stream(q, stream)))
     return out
@@ -369,7 +381,7 @@ class _Torch:
 
     def __init__(self):
         torch = _torch()
-        self.f32, self.f8, self.u8, self.empty = torch.float32, torch.float8_e4m3fn, torch.uint8, torch.empty
+        self.f32, self.f8, self.u8 = torch.float32, torch.float8_e4m3fn, torch.uint8
         self.codes = {torch.float32: MSR_F32, torch.bfloat16: MSR_BF16}
         self.raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -434,13 +446,13 @@ def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, wan
     else:
         rp = _expect("residual", residual, shape, dtype, dev)
         if total is None:
-            total = tc.empty(shape, dtype=dtype, device=x.device)
+            total = _empty(shape, dtype, x.device, stream)
         tp = _expect("sum", total, shape, dtype, dev)
     if weight is not None:
         wp, wcode = _weight(weight, d, dev)
     if want_y:
         if y is None:
-            y = tc.empty(shape, dtype=dtype, device=x.device)
+            y = _empty(shape, dtype, x.device, stream)
         yp = _expect("y", y, shape, dtype, dev)
     else:
         y = None
@@ -448,9 +460,9 @@ def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, wan
         blocks = (d + 127) // BLOCK
         qshape, sshape = (*shape[:-1], blocks * BLOCK), (*shape[:-1], blocks)
         if q is None:
-            q = tc.empty(qshape, dtype=tc.f8, device=x.device)
+            q = _empty(qshape, tc.f8, x.device, stream)
         if scale is None:
-            scale = tc.empty(sshape, dtype=tc.f32, device=x.device)
+            scale = _empty(sshape, tc.f32, x.device, stream)
         qp = _expect("q", q, qshape, tc.f8, dev)
         sp = _expect("scale", scale, sshape, tc.f32, dev)
     else:
@@ -476,16 +488,16 @@ def msr_add_rmsnorm_backward(h, weight, grad_y, *, grad_sum=None, eps=1e-6, want
     wp, wcode = _weight(weight, d, dev)
     dx, dw = out or (None, None)
     if dx is None:
-        dx = tc.empty(shape, dtype=dtype, device=h.device)
+        dx = _empty(shape, dtype, h.device, stream)
     xp, dwp, ws, n = _expect("dx", dx, shape, dtype, dev), None, None, 0
     if want_weight_grad:
         if dw is None:
-            dw = tc.empty((d,), dtype=tc.f32, device=h.device)
+            dw = _empty((d,), tc.f32, h.device, stream)
         dwp = _expect("dweight", dw, (d,), tc.f32, dev)
         n = _lib.msr_add_rmsnorm_backward_workspace(rows, d)
         if n:
             if workspace is None or workspace.numel() < n:
-                workspace = tc.empty(n, dtype=tc.u8, device=h.device)
+                workspace = _empty((n,), tc.u8, h.device, stream, kept=False)
             ws = workspace.data_ptr()
     else:
         dw = None
@@ -513,18 +525,18 @@ def msr_quantize(x, *, block_rows=1, want_rows=True, want_transposed=False, out=
     if want_rows:
         shape = (rb if square else R, cb)
         if q is None:
-            q = tc.empty((R, cb * BLOCK), dtype=tc.f8, device=x.device)
+            q = _empty((R, cb * BLOCK), tc.f8, x.device, stream)
         if sc is None:
-            sc = tc.empty(shape, dtype=tc.f32, device=x.device)
+            sc = _empty(shape, tc.f32, x.device, stream)
         qp, sp = _expect("q", q, (R, cb * BLOCK), tc.f8, dev), _expect("scale", sc, shape, tc.f32, dev)
     else:
         q = sc = None
     if want_transposed:
         shape = (cb if square else C, rb)
         if qt is None:
-            qt = tc.empty((C, rb * BLOCK), dtype=tc.f8, device=x.device)
+            qt = _empty((C, rb * BLOCK), tc.f8, x.device, stream)
         if st is None:
-            st = tc.empty(shape, dtype=tc.f32, device=x.device)
+            st = _empty(shape, tc.f32, x.device, stream)
         qtp, stp = _expect("qt", qt, (C, rb * BLOCK), tc.f8, dev), _expect("scale_t", st, shape, tc.f32, dev)
     else:
         qt = st = None
@@ -552,7 +564,7 @@ def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, strea
     rows = 1 if b_scale.shape == (n, kb) else BLOCK
     sp = _expect("b_scale", b_scale, (n if rows == 1 else (n + 127) // BLOCK, kb), tc.f32, dev)
     if out is None:
-        out = tc.empty((*lead, n), dtype=out_dtype or _torch().bfloat16, device=a.device)
+        out = _empty((*lead, n), out_dtype or _torch().bfloat16, a.device, stream)
     elif out_dtype is None:
         out_dtype = out.dtype
     code = tc.codes.get(out.dtype)
