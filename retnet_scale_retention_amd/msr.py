@@ -176,6 +176,16 @@ def _empty(shape, dtype, device, stream, kept=True):
     return t
 
 
+def _workspace(workspace, n, device, stream):
+    """The caller's workspace where it holds n bytes, or n bytes of the call's own."""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if workspace.nbytes >= n:
+            return workspace
+    return _empty((max(n, 1),), _torch().uint8, device, stream, kept=False)
+
+
 def _prep(q, k, v):
     for name, t in (("q", q), ("k", k), ("v", v)):
         if not t.is_cuda or not t.is_contiguous():
@@ -206,8 +216,7 @@ def _form(fn, form, q, k, v, gamma, chunk, theta, scale, eps, pos0, flags, state
     d = _Desc(B, T, H, dk, dv, code, gamma, theta, scale, eps, pos0, flags, _pos_rows(pos_rows, B, q.device))
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, form, chunk, ctypes.byref(n)))
-    if workspace is None or workspace.numel() < n.value:
-        workspace = _empty((max(int(n.value), 1),), torch.uint8, q.device, stream, kept=False)
+    workspace = _workspace(workspace, n.value, q.device, stream)
     if out is None:
         out = _empty((B, T, H, dv), q.dtype, q.device, stream)
     if state_in is not None and (state_in.dtype != torch.float32 or not state_in.is_contiguous()
@@ -219,7 +228,7 @@ def _form(fn, form, q, k, v, gamma, chunk, theta, scale, eps, pos0, flags, state
     if form == MSR_FORM_CHUNKWISE:
         args.append(int(chunk))
     args += [_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state_in), _ptr(state_out),
-             _ptr(workspace), ctypes.c_size_t(workspace.numel()), _stream(q, stream)]
+             _ptr(workspace), ctypes.c_size_t(workspace.nbytes), _stream(q, stream)]
     _check(fn(*args))
     return out, state_out
 
@@ -284,13 +293,12 @@ def msr_chunkwise_backward(q, k, v, gamma, chunk, grad_out, *, grad_state=None, 
               _pos_rows(pos_rows, B, q.device))
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, MSR_FORM_BACKWARD, chunk, ctypes.byref(n)))
-    if workspace is None or workspace.numel() < n.value:
-        workspace = _empty((max(int(n.value), 1),), torch.uint8, q.device, stream, kept=False)
+    workspace = _workspace(workspace, n.value, q.device, stream)
     dq, dk_, dv_ = (_empty(t.shape, t.dtype, t.device, stream) for t in (q, k, v))
     ds = _empty((B, H, dk, dv), torch.float32, q.device, stream) if want_state_grad else None
     _check(load().msr_chunkwise_backward(d.ref, int(chunk), _ptr(q), _ptr(k), _ptr(v), _ptr(state_in),
                                          _ptr(grad_out), _ptr(grad_state), _ptr(dq), _ptr(dk_), _ptr(dv_),
-                                         _ptr(ds), _ptr(workspace), ctypes.c_size_t(workspace.numel()),
+                                         _ptr(ds), _ptr(workspace), ctypes.c_size_t(workspace.nbytes),
                                          _stream(q, stream)))
     return dq, dk_, dv_, ds
 
@@ -333,15 +341,14 @@ def msr_qkv_chunkwise(x, wq, wk, wv, gamma, chunk, *, theta=None, scale=0.0, eps
               _pos_rows(pos_rows, B, x.device))
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, MSR_FORM_QKV_CHUNKWISE, chunk, ctypes.byref(n)))
-    if workspace is None or workspace.numel() < n.value:
-        workspace = _empty((max(int(n.value), 1),), torch.uint8, x.device, stream, kept=False)
+    workspace = _workspace(workspace, n.value, x.device, stream)
     if out is None:
         out = _empty((B, T, H, dv), x.dtype, x.device, stream)
     if state_out is None and return_state:
         state_out = _empty((B, H, dk, dv), torch.float32, x.device, stream)
     _check(load().msr_qkv_chunkwise(d.ref, int(chunk), int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv),
                                     _ptr(out), _ptr(state_in), _ptr(state_out), _ptr(workspace),
-                                    ctypes.c_size_t(workspace.numel()), _stream(x, stream)))
+                                    ctypes.c_size_t(workspace.nbytes), _stream(x, stream)))
     return out, state_out
 
 
@@ -381,7 +388,7 @@ class _Torch:
 
     def __init__(self):
         torch = _torch()
-        self.f32, self.f8, self.u8 = torch.float32, torch.float8_e4m3fn, torch.uint8
+        self.f32, self.f8 = torch.float32, torch.float8_e4m3fn
         self.codes = {torch.float32: MSR_F32, torch.bfloat16: MSR_BF16}
         self.raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -496,9 +503,8 @@ def msr_add_rmsnorm_backward(h, weight, grad_y, *, grad_sum=None, eps=1e-6, want
         dwp = _expect("dweight", dw, (d,), tc.f32, dev)
         n = _lib.msr_add_rmsnorm_backward_workspace(rows, d)
         if n:
-            if workspace is None or workspace.numel() < n:
-                workspace = _empty((n,), tc.u8, h.device, stream, kept=False)
-            ws = workspace.data_ptr()
+            workspace = _workspace(workspace, n, h.device, stream)
+            ws, n = workspace.data_ptr(), workspace.nbytes
     else:
         dw = None
     s = _lib.msr_add_rmsnorm_backward(rows, d, code, h.data_ptr(), wp, wcode, eps, gp, sp, xp, dwp, ws, n,

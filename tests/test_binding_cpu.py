@@ -149,3 +149,33 @@ def test_memory_of_a_call_on_a_stream_comes_from_that_stream(world, name):
 def test_memory_of_a_call_on_the_current_stream(world, name):
     calls()[name]()
     assert world.made and all(t.pool is world.stream and not hasattr(t, "recorded") for t in world.made)
+
+
+WITH_WORKSPACE = ["add_rmsnorm_backward", "parallel", "chunkwise", "chunkwise_backward", "qkv_chunkwise"]
+
+
+@pytest.mark.parametrize("name", WITH_WORKSPACE)
+def test_workspace_that_the_kernels_cannot_write_is_refused(world, name):
+    bad = {"host": torch.zeros(8192, dtype=torch.uint8),
+           "another device": on_device(8192, dtype=torch.uint8, index=1),
+           "expanded": on_device(1, dtype=torch.uint8).expand(8192),
+           "strided": on_device(8192, 2, dtype=torch.uint8)[:, 0]}
+    for what, ws in bad.items():
+        with pytest.raises(ValueError, match="workspace"):
+            calls()[name](workspace=ws)
+        assert not world.lib.calls, what
+
+
+@pytest.mark.parametrize("name", WITH_WORKSPACE)
+def test_workspace_is_taken_by_its_bytes(world, name):
+    def passed(ws):
+        world.lib.calls.clear()
+        calls()[name](workspace=ws)
+        values = [getattr(a, "value", a) for a in world.lib.calls[0][1]]
+        return ws.data_ptr() in values, values
+    used, values = passed(on_device(1024, dtype=torch.float32))  # 4096 bytes: as many as are needed
+    assert used and 4096 in values
+    used, values = passed(on_device(9000, dtype=torch.uint8))    # the whole size is passed on
+    assert used and 9000 in values
+    used, values = passed(on_device(1023, dtype=torch.float32))  # too small: the call brings its own
+    assert not used and 4096 in values
