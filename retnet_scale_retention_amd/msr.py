@@ -155,10 +155,46 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(t, stream):
-    torch = _torch()
-    s = torch.cuda.current_stream(t.device) if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+class _Torch:
+    """What the layer's entry points use of torch, looked up once (they are called for every token, and a call's host time
+    is most of a small one's cost)."""
+
+    def __init__(self):
+        torch = _torch()
+        self.f32, self.f8 = torch.float32, torch.float8_e4m3fn
+        self.codes = {torch.float32: MSR_F32, torch.bfloat16: MSR_BF16}
+        self.raw_stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+
+_tc = None
+
+
+def _setup():
+    global _tc
+    load()
+    _tc = _Torch()
+    return _tc
+
+
+def _handle(stream, index):
+    """The stream's handle (None: device `index`'s current stream)."""
+    if stream is None:
+        return (_tc or _setup()).raw_stream(index)
+    if stream.device_index != index:
+        raise ValueError(f"stream is of device {stream.device_index}, the tensors are on device {index}")
+    return stream.cuda_stream
+
+
+def _at(index, fn):
+    """fn with device `index` the current one while it runs: the library launches on the current device, and the handle of
+    a default stream names no device."""
+    if (_tc or _setup()).device() == index:
+        return fn
+
+    def moved(*args):
+        with _torch().cuda.device(index):
+            return fn(*args)
+    return moved
 
 
 def _empty(shape, dtype, device, stream, kept=True):
@@ -228,8 +264,8 @@ def _form(fn, form, q, k, v, gamma, chunk, theta, scale, eps, pos0, flags, state
     if form == MSR_FORM_CHUNKWISE:
         args.append(int(chunk))
     args += [_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state_in), _ptr(state_out),
-             _ptr(workspace), ctypes.c_size_t(workspace.nbytes), _stream(q, stream)]
-    _check(fn(*args))
+             _ptr(workspace), ctypes.c_size_t(workspace.nbytes), _handle(stream, q.get_device())]
+    _check(_at(q.get_device(), fn)(*args))
     return out, state_out
 
 
@@ -270,8 +306,9 @@ def msr_chunkwise_noalloc(q, k, v, gamma, chunk, *, out, state_out=None, theta=N
     for name, t in (("state_in", state_in), ("state_out", state_out)):
         if t is not None and (t.dtype != torch.float32 or not t.is_contiguous() or tuple(t.shape) != (B, H, dk, dv)):
             raise ValueError(f"{name} must be a contiguous float32 [B, H, dk, dv] tensor")
-    _check(load().msr_chunkwise_noalloc(d.ref, int(chunk), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state_in),
-                                        _ptr(state_out), _stream(q, stream)))
+    fn = _at(q.get_device(), load().msr_chunkwise_noalloc)
+    _check(fn(d.ref, int(chunk), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state_in), _ptr(state_out),
+              _handle(stream, q.get_device())))
     return out, state_out
 
 
@@ -296,10 +333,10 @@ def msr_chunkwise_backward(q, k, v, gamma, chunk, grad_out, *, grad_state=None, 
     workspace = _workspace(workspace, n.value, q.device, stream)
     dq, dk_, dv_ = (_empty(t.shape, t.dtype, t.device, stream) for t in (q, k, v))
     ds = _empty((B, H, dk, dv), torch.float32, q.device, stream) if want_state_grad else None
-    _check(load().msr_chunkwise_backward(d.ref, int(chunk), _ptr(q), _ptr(k), _ptr(v), _ptr(state_in),
-                                         _ptr(grad_out), _ptr(grad_state), _ptr(dq), _ptr(dk_), _ptr(dv_),
-                                         _ptr(ds), _ptr(workspace), ctypes.c_size_t(workspace.nbytes),
-                                         _stream(q, stream)))
+    fn = _at(q.get_device(), load().msr_chunkwise_backward)
+    _check(fn(d.ref, int(chunk), _ptr(q), _ptr(k), _ptr(v), _ptr(state_in), _ptr(grad_out), _ptr(grad_state),
+              _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(ds), _ptr(workspace), ctypes.c_size_t(workspace.nbytes),
+              _handle(stream, q.get_device())))
     return dq, dk_, dv_, ds
 
 
@@ -324,8 +361,9 @@ def msr_qkv_projection(x, wq, wk, wv, H, *, theta=None, scale=0.0, pos0=0, flags
               _pos_rows(pos_rows, B, x.device))
     if out is None:
         out = tuple(_empty((B, T, H, w), x.dtype, x.device, stream) for w in (dk, dk, dv))
-    _check(load().msr_qkv_projection(d.ref, int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv),
-                                     *(_ptr(t) for t in out), _stream(x, stream)))
+    fn = _at(x.get_device(), load().msr_qkv_projection)
+    _check(fn(d.ref, int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv), *(_ptr(t) for t in out),
+              _handle(stream, x.get_device())))
     return out
 
 
@@ -346,9 +384,9 @@ def msr_qkv_chunkwise(x, wq, wk, wv, gamma, chunk, *, theta=None, scale=0.0, eps
         out = _empty((B, T, H, dv), x.dtype, x.device, stream)
     if state_out is None and return_state:
         state_out = _empty((B, H, dk, dv), torch.float32, x.device, stream)
-    _check(load().msr_qkv_chunkwise(d.ref, int(chunk), int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv),
-                                    _ptr(out), _ptr(state_in), _ptr(state_out), _ptr(workspace),
-                                    ctypes.c_size_t(workspace.nbytes), _stream(x, stream)))
+    fn = _at(x.get_device(), load().msr_qkv_chunkwise)
+    _check(fn(d.ref, int(chunk), int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv), _ptr(out), _ptr(state_in),
+              _ptr(state_out), _ptr(workspace), ctypes.c_size_t(workspace.nbytes), _handle(stream, x.get_device())))
     return out, state_out
 
 
@@ -373,34 +411,13 @@ def msr_recurrent_step(q, k, v, state, gamma, pos, *, theta=None, scale=0.0, eps
         d = _Desc(B, 1, H, dk, dv, _dtype_code(q), gamma, theta, scale, eps, pos, flags)
     if out is None:
         out = _empty((B, H, dv), q.dtype, q.device, stream)
-    _check(load().msr_recurrent_step(d.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state),
-                                     _stream(q, stream)))
+    fn = _at(q.get_device(), load().msr_recurrent_step)
+    _check(fn(d.ref, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state), _handle(stream, q.get_device())))
     return out
 
 
 # ------------------------------------------------- the layer around retention
 BLOCK = 128  # MSR_BLOCK
-
-
-class _Torch:
-    """What these entry points use of torch, looked up once (they are called for every token, and a call's host time is
-    most of a small one's cost)."""
-
-    def __init__(self):
-        torch = _torch()
-        self.f32, self.f8 = torch.float32, torch.float8_e4m3fn
-        self.codes = {torch.float32: MSR_F32, torch.bfloat16: MSR_BF16}
-        self.raw_stream = torch._C._cuda_getCurrentRawStream
-
-
-_tc = None
-
-
-def _setup():
-    global _tc
-    load()
-    _tc = _Torch()
-    return _tc
 
 
 def _code(name, t):
@@ -474,8 +491,9 @@ def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, wan
         sp = _expect("scale", scale, sshape, tc.f32, dev)
     else:
         q = scale = None
-    s = _lib.msr_add_rmsnorm(_rows(shape), d, code, x.data_ptr(), rp, wp, wcode, eps, tp, yp, qp, sp,
-                             tc.raw_stream(dev) if stream is None else stream.cuda_stream)
+    fn = _at(dev, _lib.msr_add_rmsnorm)
+    s = fn(_rows(shape), d, code, x.data_ptr(), rp, wp, wcode, eps, tp, yp, qp, sp,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
         _check(s)
     return y, total, q, scale
@@ -507,8 +525,9 @@ def msr_add_rmsnorm_backward(h, weight, grad_y, *, grad_sum=None, eps=1e-6, want
             ws, n = workspace.data_ptr(), workspace.nbytes
     else:
         dw = None
-    s = _lib.msr_add_rmsnorm_backward(rows, d, code, h.data_ptr(), wp, wcode, eps, gp, sp, xp, dwp, ws, n,
-                                      tc.raw_stream(dev) if stream is None else stream.cuda_stream)
+    fn = _at(dev, _lib.msr_add_rmsnorm_backward)
+    s = fn(rows, d, code, h.data_ptr(), wp, wcode, eps, gp, sp, xp, dwp, ws, n,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
         _check(s)
     return dx, dw
@@ -546,8 +565,9 @@ def msr_quantize(x, *, block_rows=1, want_rows=True, want_transposed=False, out=
         qtp, stp = _expect("qt", qt, (C, rb * BLOCK), tc.f8, dev), _expect("scale_t", st, shape, tc.f32, dev)
     else:
         qt = st = None
-    s = _lib.msr_quantize(R, C, code, block_rows, x.data_ptr(), qp, sp, qtp, stp,
-                          tc.raw_stream(dev) if stream is None else stream.cuda_stream)
+    fn = _at(dev, _lib.msr_quantize)
+    s = fn(R, C, code, block_rows, x.data_ptr(), qp, sp, qtp, stp,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
         _check(s)
     return q, sc, qt, st
@@ -577,8 +597,9 @@ def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, strea
     if code is None:
         raise TypeError(f"unsupported output dtype {out.dtype}; use float32 or bfloat16")
     op = _expect("out", out, (*lead, n), out_dtype or out.dtype, dev)
-    s = _lib.msr_scaled_matmul(m, n, k, a.data_ptr(), ap, b.data_ptr(), sp, rows, code, op,
-                               tc.raw_stream(dev) if stream is None else stream.cuda_stream)
+    fn = _at(dev, _lib.msr_scaled_matmul)
+    s = fn(m, n, k, a.data_ptr(), ap, b.data_ptr(), sp, rows, code, op,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
         _check(s)
     return out

@@ -179,3 +179,23 @@ def test_workspace_is_taken_by_its_bytes(world, name):
     assert used and 9000 in values
     used, values = passed(on_device(1023, dtype=torch.float32))  # too small: the call brings its own
     assert not used and 4096 in values
+
+
+NOALLOC = {"chunkwise_noalloc": lambda index: lambda **kw: m.msr_chunkwise_noalloc(
+    *(on_device(1, 8, 2, w, index=index) for w in (16, 16, 32)), GAMMA, 8, out=on_device(1, 8, 2, 32, index=index), **kw)}
+
+
+@pytest.mark.parametrize("name", NAMES + sorted(NOALLOC))
+def test_launches_go_to_the_tensors_device(world, name):
+    for index in (0, 1):
+        world.lib.calls.clear()
+        (NOALLOC[name](index) if name in NOALLOC else calls(index)[name])()
+        assert [c[2] for c in world.lib.calls] == [index] and world.device == 0
+
+
+@pytest.mark.parametrize("name", NAMES + sorted(NOALLOC))
+def test_a_stream_of_another_device_is_refused(world, name):
+    call = NOALLOC[name](0) if name in NOALLOC else calls(0)[name]
+    with pytest.raises(ValueError, match="stream is of device 1"):
+        call(stream=Stream("elsewhere", 1))
+    assert not world.lib.calls and world.device == 0
