@@ -398,7 +398,9 @@ size_t msr_add_rmsnorm_backward_workspace(int64_t rows, int32_t d);
  * each square of 128 x 128,
  *   scale [P(rows) / 128][P(cols) / 128],  scale_t its transpose
  * (weights; the transposed copy holds the same values).
- * The outputs must not overlap x or each other.
+ * The outputs must not overlap x or each other.  rows and cols are at most
+ * 2^31 - 128, and fewer than 2^24 squares of 128 x 128 cover x (for q alone
+ * with block_rows 1: rows * P(cols) / 128 is at most 2^30 - 64).
  */
 msr_status msr_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block_rows, const void *x, void *q,
                         float *scale, void *qt, float *scale_t, void *hip_stream);

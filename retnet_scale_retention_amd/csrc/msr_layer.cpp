@@ -108,7 +108,11 @@ msr_status msr_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block
     if (rows < 0 || cols < 0 || padded(rows) > INT32_MAX || padded(cols) > INT32_MAX)
         return set_error(MSR_ERR_SHAPE, "rows=%lld and cols=%lld must be in 0..2^31-128", (long long)rows,
                          (long long)cols);
-    if (padded(rows) / MSR_BLOCK * (padded(cols) / MSR_BLOCK) > INT32_MAX)
+    // a launch holds fewer than 2^32 threads, here in workgroups of 256: a 128 x 128 tile each, or (own order alone,
+    // blocks within a row) 64 blocks
+    const bool by_rows = block_rows == 1 && !qt;
+    const int64_t blocks = rows * (padded(cols) / MSR_BLOCK);
+    if ((by_rows ? (blocks + 63) / 64 : padded(rows) / MSR_BLOCK * (padded(cols) / MSR_BLOCK)) >= 1 << 24)
         return set_error(MSR_ERR_SHAPE, "rows=%lld x cols=%lld is too large", (long long)rows, (long long)cols);
     if (block_rows != 1 && block_rows != MSR_BLOCK)
         return set_error(MSR_ERR_INVALID_ARG, "block_rows=%d is neither 1 nor %d", block_rows, MSR_BLOCK);

@@ -185,3 +185,26 @@ def test_binding_refuses_what_it_cannot_pass_on():
                  lambda: msr.msr_quantize(x), lambda: msr.msr_scaled_matmul(x, x, x, x)):
         with pytest.raises(ValueError):  # host tensors
             call()
+
+
+def test_quantize_refuses_what_a_launch_cannot_hold():
+    # workgroups of 256 threads, fewer than 2^32 threads in a launch; what is just small enough gets to the next check
+    f = msr.load().msr_quantize
+    misaligned = P(0x3000004)
+
+    def rows_only(rows, cols):
+        return f(rows, cols, 1, 1, A, B, misaligned, NULL, NULL, NULL)
+
+    def tiles(rows, cols, block_rows):
+        return f(rows, cols, 1, block_rows, A, NULL, NULL, B, misaligned, NULL)
+
+    for cols in (1, 8, 128):
+        refused(rows_only((1 << 30) - 63, cols), "MSR_ERR_SHAPE", "too large")
+        refused(rows_only((1 << 30) - 64, cols), "MSR_ERR_INVALID_ARG", "scale is not 16-byte aligned")
+    refused(rows_only(1 << 20, 129 * 1024), "MSR_ERR_SHAPE", "too large")
+    refused(rows_only(1 << 20, 127 * 1024), "MSR_ERR_INVALID_ARG", "scale is not 16-byte aligned")
+    for block_rows in (1, 128):
+        refused(tiles(129, (1 << 31) - 128, block_rows), "MSR_ERR_SHAPE", "too large")
+        refused(tiles(128, (1 << 31) - 128, block_rows), "MSR_ERR_INVALID_ARG", "scale_t is not 16-byte aligned")
+        refused(tiles(1 << 19, 1 << 19, block_rows), "MSR_ERR_SHAPE", "too large")
+        refused(tiles(1 << 19, (1 << 19) - 128, block_rows), "MSR_ERR_INVALID_ARG", "scale_t is not 16-byte aligned")
