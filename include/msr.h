@@ -421,6 +421,8 @@ msr_status msr_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block
  *   dx = dy w    A = dy by rows, B = the weight's transposed copy
  *   dw = dy^T x  A, B = the transposed copies of dy and x, b_block_rows 1
  * m or n of 0 launches nothing, k of 0 writes zeros; k is at most 2^24 - 128.
+ * m and n are at most 2^31 - 1025, and at most 2^25 - 8 tiles of 32 x 32 cover
+ * out (m n up to about 2^35).
  * out must not overlap an input.  Needs no workspace.
  */
 msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, const float *a_scale, const void *b,

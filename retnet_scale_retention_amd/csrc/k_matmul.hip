@@ -711,27 +711,27 @@ __global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_bod
 //   4096 x 4096 x 4096      328 |  217 |  164 |  159 |  133 |  102 |   78 |  136 |  65
 //   16384 x 8192 x 4096    2609 | 1722 | 1303 | 1273 | 1039 |  834 |  598 | 1052 | 459
 struct Fit {
-    int rows, cols, round;
+    int rows, cols, threads, round;
     double f0, f1, t0, t1;
 };
 // the last two are for bf16 output alone
 constexpr int kConfigs = 9;
-constexpr Fit kFit[2][kConfigs] = {{{32, 32, 256, 3, 0.0938, 0.00793, 0.000448},
-                                    {32, 32, 256, 2.55, 0.192, 0.00197, 0.000487},
-                                    {32, 64, 256, 2.79, 0.168, 0.00498, 0.000628},
-                                    {64, 64, 256, 3.25, 0.213, 0.00868, 0.00107},
-                                    {64, 64, 256, 2.5, 0.279, 0.00217, 0.00105},
-                                    {128, 64, 256, 2.26, 0.532, 0.00448, 0.00155},
-                                    {128, 128, 256, 3.3, 0.737, 0.00873, 0.00229},
-                                    {128, 64, 256, 3.14, 0.431, 0.0103, 0.00182},
-                                    {256, 256, 256, 9.53, 1.59, 0.0319, 0.00664}},
-                                   {{32, 32, 256, 3.03, 0.127, 0.00864, 0.000543},
-                                    {32, 32, 512, 2.48, 0.328, 0.00269, 0.000454},
-                                    {32, 64, 256, 2.92, 0.249, 0.00615, 0.000716},
-                                    {64, 64, 256, 3.3, 0.358, 0.0115, 0.00134},
-                                    {64, 64, 256, 2.61, 0.457, 0.00588, 0.00118},
-                                    {128, 64, 256, 3.36, 0.713, 0.00979, 0.00203},
-                                    {128, 128, 256, 4.84, 1.09, 0.0154, 0.00335},
+constexpr Fit kFit[2][kConfigs] = {{{32, 32, 512, 256, 3, 0.0938, 0.00793, 0.000448},
+                                    {32, 32, 128, 256, 2.55, 0.192, 0.00197, 0.000487},
+                                    {32, 64, 256, 256, 2.79, 0.168, 0.00498, 0.000628},
+                                    {64, 64, 512, 256, 3.25, 0.213, 0.00868, 0.00107},
+                                    {64, 64, 256, 256, 2.5, 0.279, 0.00217, 0.00105},
+                                    {128, 64, 256, 256, 2.26, 0.532, 0.00448, 0.00155},
+                                    {128, 128, 256, 256, 3.3, 0.737, 0.00873, 0.00229},
+                                    {128, 64, 256, 256, 3.14, 0.431, 0.0103, 0.00182},
+                                    {256, 256, 512, 256, 9.53, 1.59, 0.0319, 0.00664}},
+                                   {{32, 32, 512, 256, 3.03, 0.127, 0.00864, 0.000543},
+                                    {32, 32, 128, 512, 2.48, 0.328, 0.00269, 0.000454},
+                                    {32, 64, 256, 256, 2.92, 0.249, 0.00615, 0.000716},
+                                    {64, 64, 512, 256, 3.3, 0.358, 0.0115, 0.00134},
+                                    {64, 64, 256, 256, 2.61, 0.457, 0.00588, 0.00118},
+                                    {128, 64, 256, 256, 3.36, 0.713, 0.00979, 0.00203},
+                                    {128, 128, 256, 256, 4.84, 1.09, 0.0154, 0.00335},
                                     {},
                                     {}}};
 
@@ -768,7 +768,12 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
         if (i == 8 && (a.nkb < (a.N % 8 ? 8 : 4) || (int64_t)(a.M + 256) * a.K > INT32_MAX ||
                        (int64_t)(a.N + 256) * a.K > INT32_MAX || (int64_t)a.N * 512 > INT32_MAX))
             break;
-        const double x = fitted_us(kFit[wide][i], a.M, a.N, a.nkb);
+        const Fit &f = kFit[wide][i];
+        // a launch holds fewer than 2^32 threads (the large kernel's is 256 workgroups whatever the size); the caller sees
+        // to it that the 32 x 32 tiles of 128 threads fit
+        if (i < 8 && ((int64_t)(a.M + f.rows - 1) / f.rows * ((a.N + f.cols - 1) / f.cols) + 7) * f.threads > UINT32_MAX)
+            continue;
+        const double x = fitted_us(f, a.M, a.N, a.nkb);
         if (x < us) us = x, best = i;
     }
     const Fit &f = kFit[wide][best];

@@ -208,3 +208,15 @@ def test_quantize_refuses_what_a_launch_cannot_hold():
         refused(tiles(128, (1 << 31) - 128, block_rows), "MSR_ERR_INVALID_ARG", "scale_t is not 16-byte aligned")
         refused(tiles(1 << 19, 1 << 19, block_rows), "MSR_ERR_SHAPE", "too large")
         refused(tiles(1 << 19, (1 << 19) - 128, block_rows), "MSR_ERR_INVALID_ARG", "scale_t is not 16-byte aligned")
+
+
+def test_matmul_refuses_what_a_launch_cannot_hold():
+    # at most 2^25 - 8 tiles of 32 x 32; what is just small enough gets to the next check
+    f = msr.load().msr_scaled_matmul
+    misaligned = P(0x3000008)
+    for big, small in ((1 << 30, 32), (1 << 29, 64), (1 << 18, 1 << 17)):
+        for m_, n_, swap in ((big, small, False), (small, big, True)):
+            call = lambda m, n: f(*((n, m) if swap else (m, n)), 256, A, B, misaligned, D, 128, 1, E, NULL)
+            m_, n_ = (n_, m_) if swap else (m_, n_)
+            refused(call(m_, n_), "MSR_ERR_SHAPE", "too large")
+            refused(call(m_ - 256, n_), "MSR_ERR_INVALID_ARG", "b is not 16-byte aligned")
