@@ -161,7 +161,7 @@ class _Torch:
 
     def __init__(self):
         torch = _torch()
-        self.f32, self.f8 = torch.float32, torch.float8_e4m3fn
+        self.f32, self.f8, self.u8, self.empty = torch.float32, torch.float8_e4m3fn, torch.uint8, torch.empty
         self.codes = {torch.float32: MSR_F32, torch.bfloat16: MSR_BF16}
         self.raw_stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
@@ -202,24 +202,27 @@ def _empty(shape, dtype, device, stream, kept=True):
     stream's pool could still be in use there when `stream` writes it, and a workspace of that pool would go back to it on
     return, to be handed out again while `stream` still uses it.  `kept`: the caller gets it, and may drop it while the
     current stream still reads it."""
-    torch = _torch()
+    tc = _tc or _setup()
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return tc.empty(shape, dtype=dtype, device=device)
+    torch = _torch()
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = tc.empty(shape, dtype=dtype, device=device)
     if kept:
         t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
-def _workspace(workspace, n, device, stream):
-    """The caller's workspace where it holds n bytes, or n bytes of the call's own."""
+def _workspace(workspace, n, like, stream):
+    """The caller's workspace where it holds n bytes, or one of the call's own, on the device of `like`; and its bytes."""
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
-        if workspace.nbytes >= n:
-            return workspace
-    return _empty((max(n, 1),), _torch().uint8, device, stream, kept=False)
+        if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+        size = workspace.nbytes
+        if size >= n:
+            return workspace, size
+    n = max(n, 1)
+    return _empty((n,), (_tc or _setup()).u8, like.device, stream, kept=False), n
 
 
 def _prep(q, k, v):
@@ -252,7 +255,7 @@ def _form(fn, form, q, k, v, gamma, chunk, theta, scale, eps, pos0, flags, state
     d = _Desc(B, T, H, dk, dv, code, gamma, theta, scale, eps, pos0, flags, _pos_rows(pos_rows, B, q.device))
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, form, chunk, ctypes.byref(n)))
-    workspace = _workspace(workspace, n.value, q.device, stream)
+    workspace, ws_bytes = _workspace(workspace, n.value, q, stream)
     if out is None:
         out = _empty((B, T, H, dv), q.dtype, q.device, stream)
     if state_in is not None and (state_in.dtype != torch.float32 or not state_in.is_contiguous()
@@ -264,7 +267,7 @@ def _form(fn, form, q, k, v, gamma, chunk, theta, scale, eps, pos0, flags, state
     if form == MSR_FORM_CHUNKWISE:
         args.append(int(chunk))
     args += [_ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(state_in), _ptr(state_out),
-             _ptr(workspace), ctypes.c_size_t(workspace.nbytes), _handle(stream, q.get_device())]
+             _ptr(workspace), ws_bytes, _handle(stream, q.get_device())]
     _check(_at(q.get_device(), fn)(*args))
     return out, state_out
 
@@ -330,12 +333,12 @@ def msr_chunkwise_backward(q, k, v, gamma, chunk, grad_out, *, grad_state=None, 
               _pos_rows(pos_rows, B, q.device))
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, MSR_FORM_BACKWARD, chunk, ctypes.byref(n)))
-    workspace = _workspace(workspace, n.value, q.device, stream)
+    workspace, ws_bytes = _workspace(workspace, n.value, q, stream)
     dq, dk_, dv_ = (_empty(t.shape, t.dtype, t.device, stream) for t in (q, k, v))
     ds = _empty((B, H, dk, dv), torch.float32, q.device, stream) if want_state_grad else None
     fn = _at(q.get_device(), load().msr_chunkwise_backward)
     _check(fn(d.ref, int(chunk), _ptr(q), _ptr(k), _ptr(v), _ptr(state_in), _ptr(grad_out), _ptr(grad_state),
-              _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(ds), _ptr(workspace), ctypes.c_size_t(workspace.nbytes),
+              _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(ds), _ptr(workspace), ws_bytes,
               _handle(stream, q.get_device())))
     return dq, dk_, dv_, ds
 
@@ -379,14 +382,14 @@ def msr_qkv_chunkwise(x, wq, wk, wv, gamma, chunk, *, theta=None, scale=0.0, eps
               _pos_rows(pos_rows, B, x.device))
     n = ctypes.c_size_t(0)
     _check(load().msr_workspace_size(d.ref, MSR_FORM_QKV_CHUNKWISE, chunk, ctypes.byref(n)))
-    workspace = _workspace(workspace, n.value, x.device, stream)
+    workspace, ws_bytes = _workspace(workspace, n.value, x, stream)
     if out is None:
         out = _empty((B, T, H, dv), x.dtype, x.device, stream)
     if state_out is None and return_state:
         state_out = _empty((B, H, dk, dv), torch.float32, x.device, stream)
     fn = _at(x.get_device(), load().msr_qkv_chunkwise)
     _check(fn(d.ref, int(chunk), int(dm), _ptr(x), _ptr(wq), _ptr(wk), _ptr(wv), _ptr(out), _ptr(state_in),
-              _ptr(state_out), _ptr(workspace), ctypes.c_size_t(workspace.nbytes), _handle(stream, x.get_device())))
+              _ptr(state_out), _ptr(workspace), ws_bytes, _handle(stream, x.get_device())))
     return out, state_out
 
 
@@ -491,7 +494,7 @@ def msr_add_rmsnorm(x, weight=None, residual=None, *, eps=1e-6, want_y=True, wan
         sp = _expect("scale", scale, sshape, tc.f32, dev)
     else:
         q = scale = None
-    fn = _at(dev, _lib.msr_add_rmsnorm)
+    fn = _lib.msr_add_rmsnorm if tc.device() == dev else _at(dev, _lib.msr_add_rmsnorm)
     s = fn(_rows(shape), d, code, x.data_ptr(), rp, wp, wcode, eps, tp, yp, qp, sp,
            tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
@@ -521,11 +524,14 @@ def msr_add_rmsnorm_backward(h, weight, grad_y, *, grad_sum=None, eps=1e-6, want
         dwp = _expect("dweight", dw, (d,), tc.f32, dev)
         n = _lib.msr_add_rmsnorm_backward_workspace(rows, d)
         if n:
-            workspace = _workspace(workspace, n, h.device, stream)
-            ws, n = workspace.data_ptr(), workspace.nbytes
+            if workspace is None and stream is None:
+                workspace = tc.empty(n, dtype=tc.u8, device=h.device)
+            else:
+                workspace, n = _workspace(workspace, n, h, stream)
+            ws = workspace.data_ptr()
     else:
         dw = None
-    fn = _at(dev, _lib.msr_add_rmsnorm_backward)
+    fn = _lib.msr_add_rmsnorm_backward if tc.device() == dev else _at(dev, _lib.msr_add_rmsnorm_backward)
     s = fn(rows, d, code, h.data_ptr(), wp, wcode, eps, gp, sp, xp, dwp, ws, n,
            tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
@@ -565,7 +571,7 @@ def msr_quantize(x, *, block_rows=1, want_rows=True, want_transposed=False, out=
         qtp, stp = _expect("qt", qt, (C, rb * BLOCK), tc.f8, dev), _expect("scale_t", st, shape, tc.f32, dev)
     else:
         qt = st = None
-    fn = _at(dev, _lib.msr_quantize)
+    fn = _lib.msr_quantize if tc.device() == dev else _at(dev, _lib.msr_quantize)
     s = fn(R, C, code, block_rows, x.data_ptr(), qp, sp, qtp, stp,
            tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
@@ -597,7 +603,7 @@ def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, strea
     if code is None:
         raise TypeError(f"unsupported output dtype {out.dtype}; use float32 or bfloat16")
     op = _expect("out", out, (*lead, n), out_dtype or out.dtype, dev)
-    fn = _at(dev, _lib.msr_scaled_matmul)
+    fn = _lib.msr_scaled_matmul if tc.device() == dev else _at(dev, _lib.msr_scaled_matmul)
     s = fn(m, n, k, a.data_ptr(), ap, b.data_ptr(), sp, rows, code, op,
            tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
