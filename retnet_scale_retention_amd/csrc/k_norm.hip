@@ -179,7 +179,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
             dwl[64 * (2 * (v * W + w)) + lane] = dwl[64 * (2 * (v * W + w) + 1) + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
-    const float inv_d = 1.f / (float)a.d;
+    const float dims = (float)a.d;
     for (int64_t t = 0; t < turns; ++t) {
         const int64_t row = t * teams + team;
         const int64_t at = (row < a.rows ? row : a.rows - 1) * a.d;
@@ -227,8 +227,11 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
                 gh += rd[2 * (tm * W + i) + 1];
             }
         }
-        const float rstd = 1.f / sqrtf(ss * inv_d + a.eps);
-        const float c = rstd * rstd * (gh * inv_d);
+        // rstd^2 = d / (sum(h^2) + d eps): no mean is formed, since a product with 1 / d, rounded itself, shifts every row of
+        // a width alike, and a division by d takes longer (16384 x 4096 bf16 94.5 us, 94.1 so)
+        const float t2 = fmaf(a.eps, dims, ss);
+        const float rstd = sqrtf(dims / t2);
+        const float c = gh / t2;
         if (row >= a.rows) continue;  // the last turn of this team
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -318,7 +321,9 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 }
 
 // out[c] = sum_p part[p][c] for 32 columns: p in order within each of 64
-// slices (eight loads of four columns under way), the slices in order
+// slices (eight loads of four columns under way), the slices in pairs, pairs
+// of pairs, ... (one after the other, the last sums' roundings were most of
+// the weight gradient's error: 1.7e-7 of its norm for 3001 x 1000 fp32, not 1.0e-7)
 __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out, int parts, int d) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     __shared__ float red[64][33];
@@ -345,11 +350,15 @@ __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, floa
     for (int i = 0; i < 4; ++i) red[sl][q + i] = s[i];
     __syncthreads();
     if (threadIdx.x < 32) {
-        float t = 0.f;
+        float t[64];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) t += red[i][threadIdx.x];
+        for (int i = 0; i < 64; ++i) t[i] = red[i][threadIdx.x];
+#pragma unroll
+        for (int n = 32; n > 0; n /= 2)
+#pragma unroll
+            for (int i = 0; i < n; ++i) t[i] += t[i + n];
         const int o = (int)blockIdx.x * 32 + threadIdx.x;
-        if (o < d) out[o] = t;
+        if (o < d) out[o] = t[0];
     }
 }
 
