@@ -365,6 +365,8 @@ msr_status msr_set_exchange(int32_t mode);
  *            neither): n in 8 bits, taken from the unrounded n.
  * Other overlaps of outputs with inputs or each other are not allowed.
  * 1 <= d <= MSR_MAX_NORM_DIM.
+ * Squares are summed in fp32: a row whose sum of squares plus d eps lies past
+ * its largest number (magnitudes from about 2^64 / sqrt(d) on) has n = 0.
  */
 msr_status msr_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, const void *x, const void *residual,
                            const void *weight, int32_t weight_dtype, float eps, void *sum, void *y, void *q,
@@ -379,7 +381,9 @@ msr_status msr_add_rmsnorm(int64_t rows, int32_t d, int32_t dtype, const void *x
  *   dweight = sum over the rows of dy h rstd      (fp32 [d]; NULL: skipped)
  * dx (dtype) is the gradient of x and of the residual alike; it may be dy or
  * dsum.  Nothing else from the forward call is needed.  The sums over rows
- * run in a fixed order.  With a dweight it needs a workspace of
+ * run in a fixed order.  A row whose sum of squares plus d eps lies past
+ * fp32's largest number, with n = 0, has dx = dsum and adds nothing to
+ * dweight.  With a dweight it needs a workspace of
  * msr_add_rmsnorm_backward_workspace(rows, d) bytes (0 for few rows).
  */
 msr_status msr_add_rmsnorm_backward(int64_t rows, int32_t d, int32_t dtype, const void *h, const void *weight,

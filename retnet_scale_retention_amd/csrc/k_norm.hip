@@ -231,7 +231,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
         // a width alike, and a division by d takes longer (16384 x 4096 bf16 94.5 us, 94.1 so)
         const float t2 = fmaf(a.eps, dims, ss);
         const float rstd = sqrtf(dims / t2);
-        const float c = gh / t2;
+        const float c = rstd == 0.f ? 0.f : gh / t2;  // squares past fp32: n is 0, whatever the sum beside them came to
         if (row >= a.rows) continue;  // the last turn of this team
 #pragma unroll
         for (int v = 0; v < V; ++v) {

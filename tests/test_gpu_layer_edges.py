@@ -28,3 +28,27 @@ def test_weight_gradient_rounding(rows, d):
     err = np.linalg.norm(down(dw) - want) / np.linalg.norm(want)
     note(f"dweight {rows}x{d}: {err:.3g} of its norm")
     assert err <= 1.3e-7
+
+
+@pytest.mark.parametrize("rows,d", [(6, 96), (40, 512), (9, 4096), (4, 9001), (5, 20000)])
+def test_gradients_of_rows_whose_squares_overflow(rows, d):
+    # the forward pass gives n = 0 for such a row, whatever h: its gradient is the residual stream's alone, and the other
+    # rows' gradients are those without it
+    torch, dev = torch_dev()
+    msr = _msr()
+    note(f"overflowing rows {rows}x{d}")
+    h, _ = values(torch, dev, (rows, d), "f32", 63, spread=False)
+    dy, _ = values(torch, dev, (rows, d), "f32", 64, spread=False)
+    ds, _ = values(torch, dev, (rows, d), "f32", 65, spread=False)
+    h[1] *= 1e25                      # its squares overflow
+    h[2], dy[2] = 3e38, 4.0           # and so does the sum of h dy
+    h[3] = 3e38
+    h[3, ::2], dy[3] = -3e38, 4.0     # as a difference of infinities
+    y, _, _, _ = msr.msr_add_rmsnorm(h, eps=EPS)
+    assert not y[1:4].any()
+    dx, dw = msr.msr_add_rmsnorm_backward(h, None, dy, grad_sum=ds, eps=EPS)
+    assert torch.equal(dx[1:4], ds[1:4])
+    keep = [0, *range(4, rows)]
+    rdx, rdw, mx, mw = ol.add_rmsnorm_backward(down(h)[keep], None, down(dy)[keep], down(ds)[keep], EPS)
+    assert np.all(np.abs(down(dx)[keep] - rdx) <= 64 * U["f32"] * mx + U["f32"] * np.abs(rdx))
+    assert np.all(np.abs(down(dw) - rdw) <= (rows + 192) * U["f32"] * mw)
