@@ -348,76 +348,46 @@ __global__ __launch_bounds__(64 * KG * WM * WN) void matmul_tile_kernel(MatArgs 
 }
 
 // A few tokens against all of B (a decode step): B is read once, straight
-// into registers, two blocks at a time.  A workgroup of KW waves takes 16 NT
-// features and up to 16 MT tokens; the waves split the contraction's blocks
-// and their sums meet in LDS, so that 4096 features already give 256
-// workgroups with 2048 waves' loads under way.  1 x 4096 x 4096: 4.6 us, of
-// which 17 MB at the caches' 7.2 TB/s are 2.3 and a launch's start and end
-// most of the rest (32 x 32 tiles: 6.0).
-template <int MT, int NT, int KW, typename OUT, bool BROW>
-__device__ __forceinline__ void stream_body(const MatArgs &a) {
-    constexpr int COLS = 16 * NT, LD = COLS + 4;
-    __shared__ __attribute__((aligned(16))) float red[KW][16 * MT][LD];
+// into registers, two blocks at a time.  A workgroup of eight waves takes 16
+// features and up to 16 tokens; the waves split the contraction's blocks and
+// their sums meet in LDS, so that 4096 features already give 256 workgroups
+// with 2048 waves' loads under way.  1 x 4096 x 4096: 4.6 us, of which 17 MB
+// at the caches' 7.2 TB/s are 2.3 and a launch's start and end most of the
+// rest (32 x 32 tiles: 6.0).
+template <typename OUT, bool BROW>
+__global__ __launch_bounds__(512) void matmul_stream_kernel(MatArgs a) {
+    constexpr int KW = 8;
+    __shared__ __attribute__((aligned(16))) float red[KW][16][20];
     const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int l16 = lane & 15, g = lane >> 4;
-    const int n0 = blockIdx.x * COLS, m0 = blockIdx.y * 16 * MT;
+    const int l16 = lane & 15, g = lane >> 4, n0 = blockIdx.x * 16;
     const int k0 = (int)((int64_t)a.nkb * wv / KW), k1 = (int)((int64_t)a.nkb * (wv + 1) / KW);
-    const uint8_t *ap[MT], *bp[NT];
-    const float *sap[MT], *sbp[NT][4];
+    const size_t m = min(l16, a.M - 1);
+    const uint8_t *ap = a.a + m * a.K + 16 * g, *bp = a.b + (size_t)min(n0 + l16, a.N - 1) * a.K + 16 * g;
+    const float *sap = a.sa + m * a.nkb, *sbp[4];
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-        const size_t row = min(m0 + 16 * i + l16, a.M - 1);
-        ap[i] = a.a + row * a.K + 16 * g;
-        sap[i] = a.sa + row * a.nkb;
-    }
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        bp[j] = a.b + (size_t)min(n0 + 16 * j + l16, a.N - 1) * a.K + 16 * g;
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            sbp[j][r] = a.sb + (size_t)a.nkb * (BROW ? min(n0 + 16 * j + 4 * g + r, a.N - 1)
-                                                     : min(n0 + 16 * j, a.N - 1) >> 7);
-    }
-    f32x4 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < 4; ++r)
+        sbp[r] = a.sb + (size_t)a.nkb * (BROW ? min(n0 + 4 * g + r, a.N - 1) : min(n0, a.N - 1) >> 7);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     struct Blk {
-        Frag a[MT], b[NT];
-        float sa[MT], sb[NT][4];
+        Frag a, b;
+        float sa, sb[4];
     };
     auto load = [&](int kb) __attribute__((always_inline)) {
         Blk x;
         const size_t o = (size_t)kb * 128;
+        x.b.lo = *reinterpret_cast<const i32x4 *>(bp + o);
+        x.b.hi = *reinterpret_cast<const i32x4 *>(bp + o + 64);
+        x.a.lo = *reinterpret_cast<const i32x4 *>(ap + o);
+        x.a.hi = *reinterpret_cast<const i32x4 *>(ap + o + 64);
+        x.sa = sap[kb];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            x.b[j].lo = *reinterpret_cast<const i32x4 *>(bp[j] + o);
-            x.b[j].hi = *reinterpret_cast<const i32x4 *>(bp[j] + o + 64);
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            x.a[i].lo = *reinterpret_cast<const i32x4 *>(ap[i] + o);
-            x.a[i].hi = *reinterpret_cast<const i32x4 *>(ap[i] + o + 64);
-            x.sa[i] = sap[i][kb];
-        }
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int r = 0; r < (BROW ? 4 : 1); ++r) x.sb[j][r] = sbp[j][r][kb];
+        for (int r = 0; r < (BROW ? 4 : 1); ++r) x.sb[r] = sbp[r][kb];
         return x;
     };
     auto use = [&](const Blk &x) __attribute__((always_inline)) {
+        const f32x4 p = block_product(operand<OUT>(x.b), operand<OUT>(x.a));
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const OperandOf<OUT> fb = operand<OUT>(x.b[j]);
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const f32x4 p = block_product(fb, operand<OUT>(x.a[i]));
-#pragma unroll
-                for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(p[r], x.sa[i] * x.sb[j][BROW ? r : 0], acc[i][j][r]);
-            }
-        }
+        for (int r = 0; r < 4; ++r) acc[r] = fmaf(p[r], x.sa * x.sb[BROW ? r : 0], acc[r]);
     };
     if (k0 < k1) {
         Blk x = load(k0);
@@ -429,23 +399,16 @@ __device__ __forceinline__ void stream_body(const MatArgs &a) {
             use(y);
         }
     }
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4 *>(&red[wv][16 * i + l16][16 * j + 4 * g]) = acc[i][j];
+    *reinterpret_cast<f32x4 *>(&red[wv][l16][4 * g]) = acc;
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * MT * COLS / 4; e += 64 * KW) {
-        const int m = e / (COLS / 4), n = 4 * (e % (COLS / 4));
-        if (m0 + m >= a.M || n0 + n >= a.N) continue;
-        f32x4 s = *reinterpret_cast<const f32x4 *>(&red[0][m][n]);
+    if (threadIdx.x < 64) {
+        const int row = threadIdx.x >> 2, n = 4 * (threadIdx.x & 3);
+        if (row >= a.M || n0 + n >= a.N) return;
+        f32x4 s = *reinterpret_cast<const f32x4 *>(&red[0][row][n]);
 #pragma unroll
-        for (int w = 1; w < KW; ++w) s += *reinterpret_cast<const f32x4 *>(&red[w][m][n]);
-        store_row4(static_cast<OUT *>(a.out) + (size_t)(m0 + m) * a.N, n0 + n, a.N, s);
+        for (int w = 1; w < KW; ++w) s += *reinterpret_cast<const f32x4 *>(&red[w][row][n]);
+        store_row4(static_cast<OUT *>(a.out) + (size_t)row * a.N, n0 + n, a.N, s);
     }
-}
-template <int MT, int NT, int KW, typename OUT, bool BROW>
-__global__ __launch_bounds__(64 * KW) void matmul_stream_kernel(MatArgs a) {
-    stream_body<MT, NT, KW, OUT, BROW>(a);
 }
 
 // The whole chip on a large product (bf16 output).  256 workgroups of 8
@@ -756,7 +719,7 @@ hipError_t matmul(MatArgs a, hipStream_t st) {
         // few tokens and no more workgroups than CUs: one 16-token operand per wave, B straight from memory
         // (1 x 4096 x 4096: 4.6 us, 32 x 32 tiles 6.0; but 8 x 8192 x 8192 16.7 against 12.2, 16 x 4096 x 4096 6.8
         // against 6.1: every wave reads A's rows again)
-        hipLaunchKernelGGL((matmul_stream_kernel<1, 1, 8, OUT, BROW>), dim3((a.N + 15) / 16, 1), dim3(512), 0, st, a);
+        hipLaunchKernelGGL((matmul_stream_kernel<OUT, BROW>), dim3((a.N + 15) / 16), dim3(512), 0, st, a);
         return hipGetLastError();
     }
     int best = 0;

@@ -6,7 +6,7 @@ import pytest
 
 from oracle import layer as ol
 from tests.gpu_util import down, note, torch_dev
-from tests.test_gpu_layer import EPS, U, _msr, values
+from tests.test_gpu_layer import EPS, U, _msr, check_product, operands, product64, values
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,32 @@ def test_gradients_of_rows_whose_squares_overflow(rows, d):
     rdx, rdw, mx, mw = ol.add_rmsnorm_backward(down(h)[keep], None, down(dy)[keep], down(ds)[keep], EPS)
     assert np.all(np.abs(down(dx)[keep] - rdx) <= 64 * U["f32"] * mx + U["f32"] * np.abs(rdx))
     assert np.all(np.abs(down(dw) - rdw) <= (rows + 192) * U["f32"] * mw)
+
+
+# few tokens: eight waves share the contraction's blocks, so these have 4, 3, 2 or 3, 5 or 6, 16 and 1 or 2 blocks per wave
+FEW = [(1, 4096, 4096), (8, 1000, 3072), (3, 130, 2176), (7, 4095, 5248), (2, 17, 16384), (5, 33, 1152)]
+
+
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [128, 1])
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_few_tokens_over_many_blocks(m, n, k, block, out):
+    torch, dev = torch_dev()
+    msr = _msr()
+    note(f"few tokens {m}x{n}x{k} block {block} {out}")
+    dt = torch.float32 if out == "f32" else torch.bfloat16
+    ops = operands(torch, dev, msr, m, n, k, block, 66)
+    c = msr.msr_scaled_matmul(*ops, out_dtype=dt)
+    check_product(c, *ops, block, "product")
+    # whole quarters that fp32 holds exactly, rounded once: any misplaced row, block or scale shows
+    g = torch.Generator(device=dev).manual_seed(k)
+    pick = lambda *s: torch.randint(-1, 2, s, generator=g, device=dev).float()
+    qa, qb = pick(m, k).to(torch.float8_e4m3fn), pick(n, k).to(torch.float8_e4m3fn)
+    sa, sb = torch.exp2(pick(m, k // 128)), torch.exp2(pick(n if block == 1 else -(-n // 128), k // 128))
+    assert torch.equal(msr.msr_scaled_matmul(qa, sa, qb, sb, out_dtype=dt), product64(qa, sa, qb, sb, block)[0].float().to(dt))
+    # a NaN in the last block stays in its row and its column
+    qa.view(torch.uint8)[m - 1, k - 1], sb[0, k // 128 - 1] = 0x7F, float("nan")
+    c2 = msr.msr_scaled_matmul(qa, sa, qb, sb, out_dtype=dt)
+    columns = 1 if block == 1 else min(n, 128)
+    assert torch.isnan(c2[m - 1]).all() and torch.isnan(c2[:, :columns]).all()
+    assert torch.isfinite(c2[:m - 1, columns:]).all()
