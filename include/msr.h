@@ -40,7 +40,8 @@
  *     no pointer after it returns and allocates no device memory.
  *   - Work is enqueued on `hip_stream` (a hipStream_t; NULL = the default
  *     stream) and the call returns without synchronising.  Buffers must stay
- *     valid until the stream has passed the call.
+ *     valid until the stream has passed the call.  Launches go to the current
+ *     device, which has to be that of the stream and the buffers.
  *   - All validation happens before anything is launched; on a non-OK status
  *     nothing has been written.  msr_last_error() then describes the
  *     problem.  A failed launch returns MSR_ERR_HIP.  Device faults surface
@@ -342,7 +343,8 @@ msr_status msr_set_exchange(int32_t mode);
  *
  * 8-bit arrays hold e4m3 values (sign, 4 exponent bits, 3 fraction bits; the
  * largest is 448, no infinity, NaN 0x7f / 0xff), one byte each, in rows that
- * are padded with zeros to P(cols) = cols rounded up to a multiple of 128.
+ * are padded with zeros to P(cols) = cols rounded up to a multiple of 128
+ * (in a block that stands for NaN, see below, the padding does too).
  * Each block of 128 consecutive values of a row (or each square of 128 rows
  * by 128 columns, see block_rows) has one fp32 scale and stands for
  * scale * value.  The operators that write them choose
@@ -351,7 +353,7 @@ msr_status msr_set_exchange(int32_t mode);
  * a block that holds an infinity or a NaN stands for NaN.
  */
 #define MSR_BLOCK 128
-#define MSR_MAX_NORM_DIM 32768 /* d limit of the norm: a row stays in registers */
+#define MSR_MAX_NORM_DIM 32768 /* d limit of the norm: one workgroup holds a row */
 
 /*
  * h = x + residual (residual NULL: h = x) and its root-mean-square norm
@@ -420,7 +422,10 @@ msr_status msr_quantize(int64_t rows, int64_t cols, int32_t dtype, int32_t block
  * fp32's accuracy (the values are widened to bf16, which is exact, for the
  * matrix cores); an MSR_BF16 output uses the 8-bit matrix instruction, which
  * adds groups of 8 products aligned to the largest of them and drops their
- * bits below 2^-13 of it.  The product of two scales is formed in fp32.
+ * bits below 2^-13 of it: far below bf16's rounding of the sum of the
+ * products' magnitudes, but a result that nearly cancels loses accuracy
+ * relative to itself; MSR_F32 is for those.  The product of two scales is
+ * formed in fp32.
  * The gradients of y = x w^T are products of the same kind:
  *   dx = dy w    A = dy by rows, B = the weight's transposed copy
  *   dw = dy^T x  A, B = the transposed copies of dy and x, b_block_rows 1

@@ -178,16 +178,18 @@ __device__ __forceinline__ bool tile_of(int block, int mt, int nt, int &tm, int 
 // ST - 1 blocks ahead, with one barrier per block.  The stages are separate
 // arrays: the compiler then knows that reads of one do not wait for the loads
 // into the others (in one array it drained every load before each block's
-// first read: 787 us against 645 for 16384 x 8192 x 4096).
+// first read: 787 us against 645 for 16384 x 8192 x 4096, which take 605 with
+// the stores of today; the large kernel below 470).
 // With fp32 output the vector instructions bind it: a bf16 matrix instruction
 // takes 8 cycles of a SIMD's issue and 16 of its matrix core, a vector
 // instruction 4.3, and at 128 x 128 (64 x 64 per wave) each matrix instruction
 // comes with two conversions and, B scaled by rows, a scale product and a
-// fold: 26 cycles at best, 30 measured (4096 x 4096 x 16384: 511 us = 1075
-// TFLOP/s, the clock at 1.94 GHz by the chip's power; without the
-// conversions 486 us, over zeros 433).  Reading the operands half a block
-// ahead, or spreading all vector work evenly between the matrix
-// instructions, changed nothing (539, 543 us).
+// fold: 26 cycles at best, 30 measured (4096 x 4096 x 16384: 505-511 us = 1080
+// TFLOP/s in a loop over one set of operands, 525-548 a call on changing ones,
+// the clock at 1.94 GHz by the chip's power; in the loop 486 us without the
+// conversions, 433 over zeros).  Reading the operands half a block ahead, or
+// spreading all vector work evenly between the matrix instructions, won
+// nothing (539, 543 us where this took 515).
 template <int BM, int BN, int KG, int WM, int WN, int ST, typename OUT, bool BROW>
 __device__ __forceinline__ void tile_body(const MatArgs &a) {
     constexpr int NW = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -433,12 +435,13 @@ __global__ __launch_bounds__(512) void matmul_stream_kernel(MatArgs a) {
 //     B's) and lines.
 //   - After a lane swap every lane stores 16 bytes of a row (8 where rows
 //     start anywhere; 16 at a time were no faster there).
-// 16384 x 8192 x 4096: 485 us = 2270 TFLOP/s.  It is bound by the chip's power:
+// 16384 x 8192 x 4096: 470 us = 2340 TFLOP/s in a loop over one set of operands
+// (477-501 a call on changing ones).  It is bound by the chip's power:
 // the same kernel over zeros takes 388 us, and its blocks without loads 1.05
 // us each, the products' own rate (1.6 with random bytes and all).  The
 // tiles' ends cost 70 us, 45 of them the 268 MB of results, which all
-// workgroups write at the same time.  With B scaled by rows 625 us (128 x 128
-// tiles 732): the scales' products double the vector instructions, which then
+// workgroups write at the same time.  With B scaled by rows 640 us (128 x 128
+// tiles 715): the scales' products double the vector instructions, which then
 // take longer than the matrix instructions beside them.
 struct BigTile {
     int m0, n0, share;  // share: first of the rows whose lines this wave pulls into L2
@@ -663,9 +666,9 @@ __global__ __launch_bounds__(512, 1) void matmul_big_kernel(MatArgs a) { big_bod
 // for fp32 output; taking the smallest costs 1.8% (1.0%) over the best kernel
 // of each size.  Groups of waves that share a tile's blocks, and stages
 // further ahead, pay where there are few tiles; small LDS, so more workgroups
-// per CU, where there are many.  Times in us, bf16 output (32 x 32 by four
-// groups | by one | 32 x 64 | 64 x 64 by two | by one | 128 x 64 | 128 x 128
-// | 128 x 64 with four stages | 256 x 256):
+// per CU, where there are many.  Times in us of that sweep (loops over one set
+// of operands), bf16 output (32 x 32 by four groups | by one | 32 x 64 | 64 x
+// 64 by two | by one | 128 x 64 | 128 x 128 | 128 x 64 with four stages | 256 x 256):
 //   64 x 4096 x 4096        6.7 |  9.2 |  8.3 | 10.7 | 12.9 | 15.6 | 21.9 | 15.4 |  45
 //   64 x 8192 x 4096       12.9 | 11.2 |  9.2 | 12.0 | 19.9 | 22.3 | 25.0 | 16.6 |  45
 //   100 x 8192 x 4096      21.3 | 16.5 | 13.1 | 12.4 | 19.6 | 23.2 | 25.8 | 17.0 |  45

@@ -6,7 +6,9 @@
 // Everything is fp32 between the loads and the stores; n is taken from the
 // unrounded h, so the stored sum's rounding does not reach it.
 //
-// A row is held in registers by W waves, V groups of 8 elements per lane:
+// A row is held in registers by W waves, V groups of 8 elements per lane (but
+// for the gradients of rows beyond 16384, or beyond 8192 of a width that is no
+// multiple of 8, which are read twice):
 // group v of lane l of wave w starts at element 8 (64 (v W + w) + l), so a
 // wave reads contiguous kilobytes and a block of 128 is one row of 16 lanes
 // (its largest magnitude needs four lane-row rotations, no LDS).  Rows of up
@@ -14,8 +16,11 @@
 // of them to a wave.
 //
 // Bound by memory: 16384 x 4096 bf16 with the residual's addition and 8-bit
-// output 70 us (6.7 TB/s of the 472 MB, part of them from the last-level
-// cache; a 1 GiB copy reaches 5.1 TB/s), its gradients 93 us (5.7 TB/s).
+// output 79 us a call on changing inputs (6.0 TB/s of the 472 MB; 69 us in a
+// loop over one set, part of it then in the last-level cache; a 1 GiB copy
+// reaches 5.1 TB/s), its gradients 95 us (5.7 TB/s; 94 in a loop).  fp32
+// 16384 x 2048: 95 us with the residual (537 MB), 41 without (268 MB), in
+// a loop.  Times of variants below are of such loops.
 #include <algorithm>
 
 #include "msr_quant.hpp"
@@ -231,7 +236,7 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
         // a width alike, and a division by d takes longer (16384 x 4096 bf16 94.5 us, 94.1 so)
         const float t2 = fmaf(a.eps, dims, ss);
         const float rstd = sqrtf(dims / t2);
-        const float c = rstd == 0.f ? 0.f : gh / t2;  // squares past fp32: n is 0, whatever the sum beside them came to
+        const float c = rstd == 0.f ? 0.f : gh / t2;  // squares past fp32: n is 0, whatever gh came to
         if (row >= a.rows) continue;  // the last turn of this team
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -365,11 +370,11 @@ __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, floa
 template <int N>
 using C = std::integral_constant<int, N>;
 
-// (waves, groups per lane, lanes of a wave) that hold a row of d <= 8 L W V values.  Twice the
-// waves with one group each (ONE) suit the gradients (16384 x 4096: 93 us
-// against 98, f32 16384 x 2048 94 against 101) and f32 forwards (77 against
-// 79), whose lanes have 32 bytes of each array under way all the same; bf16
-// forwards want two (70 against 76).
+// (waves, groups per lane, lanes of a wave) that hold a row of d <= 8 L W V
+// values.  Twice the waves with one group each (ONE) suit the gradients (16384
+// x 4096: 93 us against 98, f32 16384 x 2048 94 against 101) and f32 forwards
+// (16384 x 2048 with 8-bit output 77 against 79), whose lanes have 32 bytes of
+// each array under way all the same; bf16 forwards want two (70 against 76).
 template <bool ONE, typename F>
 hipError_t by_width(int d, F f) {
     constexpr int m = ONE ? 2 : 1;

@@ -3,10 +3,12 @@
 // elements, and reductions over a row of 16 lanes.
 //
 // A block's scale is s = max(amax / 448, 2^-126) (448 is e4m3's largest
-// value; the floor keeps 1 / s finite) and its values are rne(v * (1 / s)).
+// value; the floor keeps 1 / s finite) and its values are rne(v / s), from
+// the quotient rounded to fp32 (quotient() below, not a product with 1 / s).
 // amax is taken on the bit patterns of |v|, which order as the numbers do,
 // with infinity above every number and NaN above infinity: a block that
-// holds one gets an infinite or NaN scale, and stands for NaN as a whole.
+// holds either gets a NaN scale, and stands for NaN as a whole, zeros of a
+// row's padding that lie in it included.
 #pragma once
 
 #include "msr_device.hpp"
