@@ -438,6 +438,148 @@ msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, con
                              const float *b_scale, int32_t b_block_rows, int32_t out_dtype, void *out,
                              void *hip_stream);
 
+/* ==== next to retention: head norms, a gated recurrence, clipping ============
+ * The operators of a layer's serving and training step that stand beside the
+ * forms above (jsqmd.com sections 2, 4.2 and 5: the rotated query and key, the
+ * recurrence, normalisation).  They came after 6 as well.
+ */
+
+/*
+ * Root-mean-square norms of the query and key heads with the position
+ * rotation of the forms, in one pass.  For each row x of dk values (a token's
+ * head) at position pos:
+ *   n = x / sqrt(mean(x^2) + eps) * w,   y = s R(pos theta) n,
+ * s = 1 for Q and p->scale (0 => dk^-0.5) for K, R turning the pairs
+ * (x[2i], x[2i+1]) by pos * theta[i].  The results feed the forms with
+ * MSR_FLAG_NO_ROTATE and scale 1.
+ *   Q [B][T][H][dk], K [B][T][key_heads][dk] of p->dtype, the heads of a token
+ *     side by side and q_stride (k_stride) elements from one token to the next
+ *     (0 => H * dk: packed), as for one projection that writes Q, K and V side
+ *     by side; wq, wk [dk] of type weight_dtype (NULL: ones);
+ *   QO, KO as Q and K, packed, written.
+ * key_heads (0..MSR_MAX_HEADS) may differ from p->H; 0: there is no K, and its
+ * arguments are NULL.  Of p, B, T, H, dk, dtype, theta, scale, pos0, pos_rows
+ * and the flag MSR_FLAG_NO_ROTATE (no rotation; the scale stays) are used, the
+ * rest is ignored.  B * T is at most 2^31 - 1.  Q and K, and the pointers of
+ * the backward call that have strides, need only their type's alignment; rows
+ * of 16-byte alignment (pointer, stride and dk) are faster.  QO may be Q where
+ * that is packed, KO K; otherwise outputs must not overlap anything.
+ * Rows of which every value is zero give zeros; rows whose squares overflow
+ * fp32 give zeros too.
+ */
+msr_status msr_qk_norm_rotate(const msr_problem *p, int32_t key_heads, float eps, const void *Q, int64_t q_stride,
+                              const void *K, int64_t k_stride, const void *wq, const void *wk, int32_t weight_dtype,
+                              void *QO, void *KO, void *hip_stream);
+
+/* Workspace bytes of the gradients below (0 for sizes that they refuse). */
+size_t msr_qk_norm_rotate_backward_workspace(int64_t tokens, int32_t heads, int32_t key_heads, int32_t dk);
+
+/*
+ * Gradients of msr_qk_norm_rotate: with u = s R(-pos theta) dy,
+ *   g = w u,  r = 1 / sqrt(mean(x^2) + eps),
+ *   dx = r (g - x r^2 mean(g x)),   dw = sum over rows of u x r.
+ * dQO, dKO [B][T][heads][dk] packed, of p->dtype; dQ, dK like Q and K, with
+ * strides of their own (0 => packed), so that they may lie side by side in the
+ * gradient of a fused projection; dwq, dwk [dk] fp32 (NULL: not wanted; the
+ * weight may be NULL, the gradient is then that of a weight of ones).
+ * Sums run in a fixed order: equal calls give equal results.  dQ may be dQO
+ * and dK dKO where they are packed; outputs otherwise must not overlap
+ * anything, except that dQ and dK of one stride may interleave.
+ * The workspace of msr_qk_norm_rotate_backward_workspace(B * T, H, key_heads,
+ * dk) bytes is needed where dwq or dwk is given.
+ */
+msr_status msr_qk_norm_rotate_backward(const msr_problem *p, int32_t key_heads, float eps, const void *Q,
+                                       int64_t q_stride, const void *K, int64_t k_stride, const void *wq,
+                                       const void *wk, int32_t weight_dtype, const void *dQO, const void *dKO, void *dQ,
+                                       int64_t dq_stride, void *dK, int64_t dk_stride, float *dwq, float *dwk, void *ws,
+                                       size_t ws_bytes, void *hip_stream);
+
+/*
+ * A recurrence of D channels whose decay depends on the data: per batch row
+ * and channel, from h_0 = state_in (NULL: zeros),
+ *   a_t = exp(-rate sigmoid(g_t)),   h_t = a_t h_(t-1) + m_t x_t,
+ *   m_t = sqrt(1 - a_t^2) if normalize is not 0 (inputs of unit variance keep
+ *   the state at unit variance), else 1.
+ *   x, g, h [B][T][D] of type dtype; rate [D] fp32, finite and >= 0 (device
+ *   values, not checked); state_in, state_out [B][D] fp32 (state_out NULL: not
+ *   wanted; it may be state_in); h may be NULL;
+ *   carry (NULL: not wanted) [B][ceil(T / 64)][D] fp32: the states before the
+ *   tokens 0, 64, 128, ..., for the backward pass.
+ * Everything between loads and stores is fp32.  T = 0 copies the state.
+ * B, T and D are at most 2^31 - 1, and B * ceil(T / 64) * ceil(D / 128) below
+ * 2^24.  Outputs must not overlap anything else.  The workspace is that of
+ * msr_gated_recurrence_workspace(B, T, D, 0).  Equal calls give equal
+ * results.
+ */
+#define MSR_GATE_BLOCK 64
+msr_status msr_gated_recurrence(int64_t B, int64_t T, int64_t D, int32_t dtype, int32_t normalize, const void *x,
+                                const void *g, const float *rate, const float *state_in, void *h, float *state_out,
+                                float *carry, void *ws, size_t ws_bytes, void *hip_stream);
+
+/*
+ * Workspace bytes of msr_gated_recurrence (pass 0), of its backward pass with
+ * the forward pass's carry (1) and without (2); 0 for sizes that they refuse.
+ */
+size_t msr_gated_recurrence_workspace(int64_t B, int64_t T, int64_t D, int32_t pass);
+
+/*
+ * One token of the gated recurrence: x, g, h [B][D]; state [B][D] fp32 is the
+ * state before it, state_out the one after (state_out may be state).
+ * No workspace.
+ */
+msr_status msr_gated_recurrence_step(int64_t B, int64_t D, int32_t dtype, int32_t normalize, const void *x,
+                                     const void *g, const float *rate, const float *state, float *state_out, void *h,
+                                     void *hip_stream);
+
+/*
+ * Gradients of msr_gated_recurrence: x, g, rate, state_in as there, dh [B][T][D]
+ * of type dtype the gradient of h, dstate_out [B][D] fp32 that of the last state
+ * (NULL: zeros).  Writes dx, dg [B][T][D] of type dtype and, where given, drate
+ * [D] and dstate_in [B][D], fp32:
+ *   lam_t = dh_t + a_(t+1) lam_(t+1),   dx = m lam,
+ *   dl_t = a_t lam_t h_(t-1) - lam_t x_t a_t^2 / m_t (second term: normalize),
+ *   dg = -rate s (1 - s) dl,   drate = -sum s dl,   s = sigmoid(g).
+ * Where m is 0 (rate or s is 0) that second term is left out.  carry is the
+ * forward call's (NULL: the forward pass runs again for it).  Workspace:
+ * msr_gated_recurrence_workspace(B, T, D, carry ? 1 : 2).  Outputs must not
+ * overlap anything else.
+ */
+msr_status msr_gated_recurrence_backward(int64_t B, int64_t T, int64_t D, int32_t dtype, int32_t normalize,
+                                         const void *x, const void *g, const float *rate, const float *state_in,
+                                         const float *carry, const void *dh, const float *dstate_out, void *dx, void *dg,
+                                         float *drate, float *dstate_in, void *ws, size_t ws_bytes, void *hip_stream);
+
+/* A gradient tensor of n elements of type dtype, aligned to its type. */
+typedef struct {
+    const void *grad; /* [device] */
+    void *out;        /* [device] the clipped gradient (msr_clip_gradients; may be grad) */
+    int64_t n;
+    int64_t dtype; /* msr_dtype */
+} msr_gradient;
+
+/* Workspace bytes of the two calls below for these tensors ([host], read during the call). */
+size_t msr_gradient_norm_workspace(const msr_gradient *grads, int64_t count);
+
+/*
+ * *norm (fp32, device) = the square root of the sum of the squares of all
+ * elements of `count` tensors.  Squares and sums are fp64, in a fixed order.
+ */
+msr_status msr_gradient_norm(const msr_gradient *grads, int64_t count, float *norm, void *ws, size_t ws_bytes,
+                             void *hip_stream);
+
+/*
+ * out = grad * min(1, max_norm / norm) for every tensor.  norm (fp32, device)
+ * NULL: the tensors' own norm, as above; given: that one (for gradients that
+ * are spread over processes, whose norms the caller has joined), and no
+ * workspace is needed.  norm_out (NULL where norm is given, or where
+ * it is not wanted) receives the norm.  Where
+ * the norm is infinite or NaN the gradients are left as they are (out is a
+ * copy): the caller sees it in norm_out and skips the step.  An output must
+ * not overlap another tensor.
+ */
+msr_status msr_clip_gradients(const msr_gradient *grads, int64_t count, float max_norm, const float *norm,
+                              float *norm_out, void *ws, size_t ws_bytes, void *hip_stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,226 @@
+// k_clip.hip -- the norm of many gradient tensors together, and their
+// scaling to a largest norm: norm = sqrt(sum of squares),
+// out = g min(1, max / norm).
+//
+// Tensors travel as a table in the kernel's arguments (kTable of them per
+// launch) and are cut into chunks that the workgroups take in turn.  Squares
+// are formed and added in fp64, so that no finite gradient overflows or
+// vanishes; each workgroup writes one sum, and whoever needs the total adds
+// the sums in the same order (no atomics, the same norm on every run).
+#include <algorithm>
+
+#include "msr_quant.hpp"
+
+namespace {
+
+using namespace msr;
+
+constexpr int kTable = 96, kThreads = 256, kGroups = 4, kChunk = kThreads * 8 * kGroups;
+
+struct Entry {
+    const void *g;
+    void *out;
+    int64_t n;
+    int32_t start, bf16;  // first chunk
+};
+
+struct ClipArgs {
+    Entry t[kTable];
+    int count, chunks;
+    // norm: where the sums go.  clip: the total is that of `sums` of them, or of *norm where that is given
+    double *sums;
+    int n_sums;
+    const float *norm;
+    float *norm_out;
+    float max_norm;
+};
+
+static_assert(sizeof(ClipArgs) <= 4096, "a kernel's arguments");
+
+__device__ __forceinline__ double block_sum64(double x, double *red) {
+#pragma unroll
+    for (int o = 32; o > 0; o /= 2) x += __shfl_xor(x, o, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// the total of n sums, the same in every workgroup that forms it
+__device__ __forceinline__ double total(const double *sums, int n, double *red) {
+    double x = 0.0;
+    for (int i = threadIdx.x; i < n; i += kThreads) x += sums[i];
+    return block_sum64(x, red);
+}
+
+template <typename T>
+__device__ __forceinline__ double squares(const T *p, int64_t left) {
+    double s[2] = {0.0, 0.0};
+    if (left >= kChunk) {
+        Raw8<T, kAny> r[kGroups];
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) r[u].load(p + (u * kThreads + threadIdx.x) * 8, 8);
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            float v[8];
+            r[u].get(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i & 1] = fma((double)v[i], (double)v[i], s[i & 1]);
+        }
+    } else {
+        for (int i = threadIdx.x; i < left; i += kThreads) {
+            const double v = load(p, i);
+            s[0] = fma(v, v, s[0]);
+        }
+    }
+    return s[0] + s[1];
+}
+
+template <typename T>
+__device__ __forceinline__ void scale(const T *p, T *o, int64_t left, double f) {
+    // fp32: one rounding of the product with the fp64 factor; bf16: the fp32 product's rounding is far below its own
+    auto one = [&](float v) { return sizeof(T) == 4 ? (float)((double)v * f) : v * (float)f; };
+    if (left >= kChunk) {
+        Raw8<T, kAny> r[kGroups];
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) r[u].load(p + (u * kThreads + threadIdx.x) * 8, 8);
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            float v[8];
+            r[u].get(v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = one(v[i]);
+            store8<kAny>(o + (u * kThreads + threadIdx.x) * 8, 8, v);
+        }
+    } else {
+        for (int i = threadIdx.x; i < left; i += kThreads) store(o, i, one(load(p, i)));
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void gradient_norm_kernel(ClipArgs a) {
+    __shared__ double red[4];
+    double s = 0.0;
+    int e = 0;
+    for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+        while (e + 1 < a.count && c >= a.t[e + 1].start) ++e;
+        const int64_t at = (int64_t)(c - a.t[e].start) * kChunk, left = a.t[e].n - at;
+        s += a.t[e].bf16 ? squares(static_cast<const uint16_t *>(a.t[e].g) + at, left)
+                         : squares(static_cast<const float *>(a.t[e].g) + at, left);
+    }
+    s = block_sum64(s, red);
+    if (threadIdx.x == 0) a.sums[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kThreads) void gradient_total_kernel(double *sums, int n, double *out, float *norm) {
+    __shared__ double red[4];
+    const double s = total(sums, n, red);
+    if (threadIdx.x == 0) {
+        if (out) *out = s;
+        if (norm) *norm = (float)sqrt(s);
+    }
+}
+
+// From the last chunk to the first: what the norm read last may still lie in the caches.
+__global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
+    __shared__ double red[4];
+    const double norm = a.norm ? (double)*a.norm : sqrt(total(a.sums, a.n_sums, red));
+    if (a.norm_out && blockIdx.x == 0 && threadIdx.x == 0) *a.norm_out = (float)norm;
+    const bool clip = norm > (double)a.max_norm && norm <= 3.40282347e38;  // neither infinity, as fp32, nor NaN
+    const double f = clip ? (double)a.max_norm / norm : 1.0;
+    int e = a.count - 1;
+    for (int c = a.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+        while (c < a.t[e].start) --e;
+        if (!clip && a.t[e].g == a.t[e].out) continue;
+        const int64_t at = (int64_t)(c - a.t[e].start) * kChunk, left = a.t[e].n - at;
+        if (a.t[e].bf16)
+            scale(static_cast<const uint16_t *>(a.t[e].g) + at, static_cast<uint16_t *>(a.t[e].out) + at, left, f);
+        else
+            scale(static_cast<const float *>(a.t[e].g) + at, static_cast<float *>(a.t[e].out) + at, left, f);
+    }
+}
+
+constexpr int kSums = 1024;  // workgroups, and so sums, of a norm launch
+
+// The launches that cover the tensors: f(args) for each, whose chunks are counted in 31 bits.
+template <typename F>
+hipError_t batches(const msr_gradient *t, int64_t count, F f) {
+    ClipArgs a{};
+    int64_t chunks = 0;
+    auto flush = [&] {
+        a.chunks = (int)chunks;
+        const hipError_t e = a.count > 0 ? f(a) : hipSuccess;
+        a.count = 0, chunks = 0;
+        return e;
+    };
+    for (int64_t i = 0; i < count; ++i) {
+        const size_t e = t[i].dtype == MSR_BF16 ? 2 : 4;
+        // a tensor of more chunks than a launch counts goes in pieces
+        for (int64_t at = 0; at < t[i].n;) {
+            constexpr int64_t most = (int64_t)1 << 30;
+            const int64_t n = std::min(t[i].n - at, most * kChunk), c = (n + kChunk - 1) / kChunk;
+            if (a.count == kTable || chunks + c > most) {
+                const hipError_t r = flush();
+                if (r != hipSuccess) return r;
+            }
+            a.t[a.count++] = {static_cast<const char *>(t[i].grad) + at * e,
+                              t[i].out ? static_cast<char *>(t[i].out) + at * e : nullptr, n, (int32_t)chunks,
+                              t[i].dtype == MSR_BF16};
+            chunks += c;
+            at += n;
+        }
+    }
+    return flush();
+}
+
+hipError_t sum_squares(const msr_gradient *t, int64_t count, double *sums, int64_t &n, hipStream_t st) {
+    n = 0;
+    return batches(t, count, [&](ClipArgs &a) {
+        const int g = std::min(a.chunks, kSums);
+        a.sums = sums + n;
+        n += g;
+        hipLaunchKernelGGL(gradient_norm_kernel, dim3(g), dim3(kThreads), 0, st, a);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace
+
+// one double per workgroup of the norm, and one for their total
+size_t gradient_norm_workspace(const msr_gradient *t, int64_t count) {
+    int64_t n = 0;
+    (void)batches(t, count, [&](ClipArgs &a) {
+        n += std::min(a.chunks, kSums);
+        return hipSuccess;
+    });
+    return (size_t)(n + 1) * sizeof(double);
+}
+
+hipError_t launch_gradient_norm(const msr_gradient *t, int64_t count, float *norm, double *ws, hipStream_t st) {
+    int64_t n = 0;
+    const hipError_t e = sum_squares(t, count, ws + 1, n, st);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(gradient_total_kernel, dim3(1), dim3(kThreads), 0, st, ws + 1, (int)n, nullptr, norm);
+    return hipGetLastError();
+}
+
+hipError_t launch_clip_gradients(const msr_gradient *t, int64_t count, float max_norm, const float *norm, float *norm_out,
+                                 double *ws, hipStream_t st) {
+    int64_t n = 0;
+    hipError_t e;
+    double *sums = ws + 1;
+    if (!norm) {
+        if ((e = sum_squares(t, count, sums, n, st)) != hipSuccess) return e;
+        // every workgroup adds up to 2048 sums by itself; more of them are added once
+        if (n > 2048 || n == 0) {
+            hipLaunchKernelGGL(gradient_total_kernel, dim3(1), dim3(kThreads), 0, st, sums, (int)n, ws, n ? nullptr : norm_out);
+            if ((e = hipGetLastError()) != hipSuccess || n == 0) return e;
+            sums = ws, n = 1;
+        }
+    }
+    return batches(t, count, [&](ClipArgs &a) {
+        a.sums = sums, a.n_sums = (int)n, a.norm = norm, a.norm_out = norm_out, a.max_norm = max_norm;
+        norm_out = nullptr;  // the first launch writes it
+        hipLaunchKernelGGL(clip_kernel, dim3(std::min(a.chunks, 2048)), dim3(kThreads), 0, st, a);
+        return hipGetLastError();
+    });
+}

@@ -328,11 +328,15 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 // out[c] = sum_p part[p][c] for 32 columns: p in order within each of 64
 // slices (eight loads of four columns under way), the slices in pairs, pairs
 // of pairs, ... (one after the other, the last sums' roundings were most of
-// the weight gradient's error: 1.7e-7 of its norm for 3001 x 1000 fp32, not 1.0e-7)
-__global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out, int parts, int d) {
+// the weight gradient's error: 1.7e-7 of its norm for 3001 x 1000 fp32, not 1.0e-7).
+// The second row of workgroups takes the second array of parts to out1.
+__global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out0, float *out1, int parts, int d) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     __shared__ float red[64][33];
     const int q = 4 * (threadIdx.x & 7), c = (int)blockIdx.x * 32 + q, sl = threadIdx.x >> 3;
+    float *out = blockIdx.y ? out1 : out0;
+    if (!out) return;
+    part += (size_t)blockIdx.y * parts * d;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (c + 4 <= d) {
         for (int p0 = sl; p0 < parts; p0 += 512) {
@@ -455,9 +459,11 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h
     };
     hipError_t e = hipSuccess;
     if (parts > 0) e = dtype == MSR_BF16 ? by_rows<true, uint16_t>(d, launch) : by_rows<true, float>(d, launch);
-    if (e == hipSuccess && dw && parts != 1) {
-        hipLaunchKernelGGL(column_sum_kernel, dim3((d + 31) / 32), dim3(512), 0, st, part, dw, parts, d);
-        e = hipGetLastError();
-    }
+    if (e == hipSuccess && dw && parts != 1) e = launch_column_sum(part, dw, nullptr, parts, d, st);
     return e;
+}
+
+hipError_t launch_column_sum(const float *part, float *out0, float *out1, int parts, int d, hipStream_t st) {
+    hipLaunchKernelGGL(column_sum_kernel, dim3((d + 31) / 32, out1 ? 2 : 1), dim3(512), 0, st, part, out0, out1, parts, d);
+    return hipGetLastError();
 }

@@ -102,6 +102,45 @@ hipError_t launch_quantize(int64_t R, int64_t C, int dtype, int block_rows, cons
 hipError_t launch_scaled_matmul(int m, int n, int k, const void *A, const float *sa, const void *B, const float *sb,
                                 int b_rows, int out_dtype, void *out, hipStream_t st);
 
+// out0[c] (and out1[c], where given) = the sum over `parts` rows of part[0] (part[1]) [parts][d], in a fixed order; no
+// parts: zeros
+hipError_t launch_column_sum(const float *part, float *out0, float *out1, int parts, int d, hipStream_t st);
+
+// ---- head norms with the rotation (k_qknorm.hip) ---------------------------
+struct QkNorm {
+    const void *x[2], *dy[2], *w[2];  // Q and K, their results' gradients (backward), weights (NULL: ones)
+    void *y[2];                       // results, or the gradients of Q and K
+    int64_t xs[2], ys[2];             // elements from a token of x (of y) to the next
+    float *dw[2], *part;              // backward: weight gradients (may be NULL), workspace
+    const int64_t *pos_rows;
+    int64_t pos0, tokens;
+    int H[2], dk, T, dtype, w_dtype, rotate;  // H[1] may be 0
+    float scale, eps;
+    const float *theta;
+};
+hipError_t launch_qk_norm(const QkNorm &q, bool backward, hipStream_t st);
+size_t qk_norm_backward_workspace(int64_t tokens, int H, int Hk, int dk);
+
+// ---- gated recurrence (k_gate.hip) ------------------------------------------
+struct Gate {
+    const void *x, *g, *dh;
+    const float *rate, *state_in, *dstate_out;
+    void *h, *dx, *dg;
+    float *state_out, *carry, *drate, *dstate_in;
+    int B, T, D, dtype, normalize;
+};
+size_t gate_workspace(int B, int T, int D, bool backward, bool carry_given);
+hipError_t launch_gate(const Gate &q, char *ws, hipStream_t st);
+hipError_t launch_gate_step(const Gate &q, hipStream_t st);
+hipError_t launch_gate_backward(const Gate &q, char *ws, hipStream_t st);
+
+// ---- gradient norm and clipping (k_clip.hip) --------------------------------
+size_t gradient_norm_workspace(const msr_gradient *t, int64_t count);
+hipError_t launch_gradient_norm(const msr_gradient *t, int64_t count, float *norm, double *ws, hipStream_t st);
+// norm NULL: the tensors' own
+hipError_t launch_clip_gradients(const msr_gradient *t, int64_t count, float max_norm, const float *norm, float *norm_out,
+                                 double *ws, hipStream_t st);
+
 // Sets this thread's msr_last_error text and returns s.
 msr_status set_error(msr_status s, const char *fmt, ...);
 

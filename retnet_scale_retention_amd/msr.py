@@ -10,6 +10,7 @@ fallback implementation.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import math
 from pathlib import Path
@@ -32,7 +33,10 @@ EXPORTS = ("msr_abi_version", "msr_last_error", "msr_workspace_size", "msr_works
            "msr_chunkwise", "msr_chunkwise_noalloc", "msr_chunkwise_backward", "msr_qkv_projection", "msr_qkv_chunkwise",
            "msr_recurrent_step", "msr_set_kernel_events", "msr_set_exchange",
            "msr_add_rmsnorm", "msr_add_rmsnorm_backward", "msr_add_rmsnorm_backward_workspace", "msr_quantize",
-           "msr_scaled_matmul")
+           "msr_scaled_matmul",
+           "msr_qk_norm_rotate", "msr_qk_norm_rotate_backward", "msr_qk_norm_rotate_backward_workspace",
+           "msr_gated_recurrence", "msr_gated_recurrence_workspace", "msr_gated_recurrence_step",
+           "msr_gated_recurrence_backward", "msr_gradient_norm", "msr_gradient_norm_workspace", "msr_clip_gradients")
 
 
 class MsrError(RuntimeError):
@@ -101,6 +105,23 @@ def load():
     lib.msr_quantize.restype = ctypes.c_int
     lib.msr_scaled_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp]
     lib.msr_scaled_matmul.restype = ctypes.c_int
+    # msr_problem by address: the head norms' callers fill it with addresses (_HeadProblem)
+    lib.msr_qk_norm_rotate.argtypes = [vp, i32, f32, vp, i64, vp, i64, vp, vp, i32, vp, vp, vp]
+    lib.msr_qk_norm_rotate_backward.argtypes = [vp, i32, f32, vp, i64, vp, i64, vp, vp, i32, vp, vp, vp, i64, vp, i64,
+                                                vp, vp, vp, sz, vp]
+    lib.msr_qk_norm_rotate_backward_workspace.argtypes = [i64, i32, i32, i32]
+    lib.msr_gated_recurrence.argtypes = [i64, i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.msr_gated_recurrence_workspace.argtypes = [i64, i64, i64, i32]
+    lib.msr_gated_recurrence_step.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+    lib.msr_gated_recurrence_backward.argtypes = [i64, i64, i64, i32, i32, *[vp] * 12, sz, vp]
+    lib.msr_gradient_norm.argtypes = [vp, i64, vp, vp, sz, vp]
+    lib.msr_gradient_norm_workspace.argtypes = [vp, i64]
+    lib.msr_clip_gradients.argtypes = [vp, i64, f32, vp, vp, vp, sz, vp]
+    for name in ("msr_qk_norm_rotate", "msr_qk_norm_rotate_backward", "msr_gated_recurrence", "msr_gated_recurrence_step",
+                 "msr_gated_recurrence_backward", "msr_gradient_norm", "msr_clip_gradients"):
+        getattr(lib, name).restype = ctypes.c_int
+    for name in ("msr_qk_norm_rotate_backward_workspace", "msr_gated_recurrence_workspace", "msr_gradient_norm_workspace"):
+        getattr(lib, name).restype = sz
     del fp
     _lib = lib
     return lib
@@ -615,6 +636,338 @@ def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, strea
     if s:
         _check(s)
     return out
+
+
+# ------------------------------------------------------- next to retention
+class _HeadProblem(ctypes.Structure):
+    """msr_problem with addresses in place of pointers to floats (the head norms use neither gamma nor dv)."""
+    _fields_ = [(n, {"gamma": ctypes.c_void_p, "theta": ctypes.c_void_p}.get(n, t)) for n, t in Problem._fields_]
+
+
+def _heads(name, t, dtype, index):
+    """(B, T, H, dk, address, elements from a token to the next) of Q or K: [B, T, H, dk], or [B, H, dk] for one token
+    each, the heads of a token packed and the tokens at one distance."""
+    shape, stride = t.shape, t.stride()
+    if not t.is_cuda or t.get_device() != index or t.dtype is not dtype or len(shape) not in (3, 4):
+        raise ValueError(f"{name} must be a {dtype} [B, T, H, dk] or [B, H, dk] tensor on device {index}")
+    H, dk = shape[-2:]
+    B, T = (shape[0], 1) if len(shape) == 3 else shape[:2]
+    step = stride[0] if T == 1 else stride[1]
+    if B * T <= 1:
+        step = H * dk
+    if (stride[-1] != 1 and dk > 1) or (stride[-2] != dk and H > 1) or (B * T and step < H * dk) or (
+            B > 1 and T > 1 and stride[0] != T * step):
+        raise ValueError(f"{name}: the heads of a token must be packed and all tokens at one distance; got strides {stride}")
+    return B, T, H, dk, t.data_ptr(), step
+
+
+def _head_problem(B, T, H, dk, code, theta, scale, pos0, flags, pos_rows, device):
+    keep = None
+    if theta is not None:
+        keep = theta if (isinstance(theta, np.ndarray) and theta.dtype == np.float32 and theta.flags.c_contiguous) else \
+            np.ascontiguousarray(theta, dtype=np.float32)
+        if keep.shape != (dk // 2,):
+            raise ValueError(f"theta must hold dk/2={dk // 2} values")
+    p = _HeadProblem(B, T, H, dk, 4, code, None, None if keep is None else keep.__array_interface__["data"][0], scale, 0.0,
+                     pos0, flags, None if pos_rows is None else _pos_rows(pos_rows, B, device))
+    return p, keep
+
+
+def _pair_weights(wq, wk, dk, index):
+    wqp, qcode = _weight(wq, dk, index)
+    wkp, kcode = _weight(wk, dk, index)
+    if wqp is not None and wkp is not None and qcode != kcode:
+        raise TypeError("wq and wk must share one dtype")
+    return wqp, wkp, qcode if wqp is not None else kcode
+
+
+def msr_qk_norm_rotate(q, k=None, wq=None, wk=None, *, eps=1e-6, theta=None, scale=0.0, pos0=0, flags=0, pos_rows=None,
+                       out=None, stream=None):
+    """Root-mean-square norms of the query and key heads with the position rotation in the same pass:
+    R(pos theta) (q / sqrt(mean(q^2) + eps) * wq), and the same of k times scale (0: dk^-0.5).  q [B, T, H, dk], k
+    [B, T, Hk, dk] (or [B, H, dk] for one token each) float32 or bfloat16; views of one fused projection are fine: the
+    heads of a token packed, tokens at any one distance.  wq, wk [dk] or None.  pos0 or pos_rows as in the forms,
+    MSR_FLAG_NO_ROTATE for the norms alone.  Returns (q', k') packed (out: tensors to write; q' may be q); the forms take
+    them with flags=MSR_FLAG_NO_ROTATE and scale=1."""
+    tc = _tc or _setup()
+    dtype, dev = q.dtype, q.get_device()
+    code = tc.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} of q; use float32 or bfloat16")
+    B, T, H, dk, qp, qs = _heads("q", q, dtype, dev)
+    Hk = ks = 0
+    kp = kop = None
+    qo, ko = out or (None, None)
+    if k is not None:
+        Bk, Tk, Hk, dkk, kp, ks = _heads("k", k, dtype, dev)
+        if (Bk, Tk, dkk) != (B, T, dk):
+            raise ValueError("q and k must share B, T and dk")
+        if ko is None:
+            ko = _empty(k.shape, dtype, k.device, stream)
+        kop = _expect("out of k", ko, k.shape, dtype, dev)
+    else:
+        ko = wk = None
+    if qo is None:
+        qo = _empty(q.shape, dtype, q.device, stream)
+    qop = _expect("out of q", qo, q.shape, dtype, dev)
+    wqp, wkp, wcode = _pair_weights(wq, wk, dk, dev)
+    p, keep = _head_problem(B, T, H, dk, code, theta, scale, pos0, flags, pos_rows, q.device)
+    fn = _lib.msr_qk_norm_rotate if tc.device() == dev else _at(dev, _lib.msr_qk_norm_rotate)
+    s = fn(ctypes.byref(p), Hk, eps, qp, qs, kp, ks, wqp, wkp, wcode, qop, kop,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
+    if s:
+        _check(s)
+    return qo, ko
+
+
+def msr_qk_norm_rotate_backward(q, k, wq, wk, grad_q, grad_k, *, eps=1e-6, theta=None, scale=0.0, pos0=0, flags=0,
+                                pos_rows=None, want_weight_grad=True, out=None, workspace=None, stream=None):
+    """Gradients of msr_qk_norm_rotate: q, k, weights and the rest as there, grad_q = dL/dq', grad_k = dL/dk' packed.
+    Returns (dq, dk, dwq, dwk): dq, dk in q's type, dwq, dwk float32 [dk] (None unless want_weight_grad; that of a weight
+    of ones where the weight is None).  out: tensors to write, in the same order; dq and dk may be views like q and k, so
+    that they lie side by side in a fused projection's gradient, or grad_q and grad_k themselves."""
+    tc = _tc or _setup()
+    dtype, dev = q.dtype, q.get_device()
+    code = tc.codes.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dtype} of q; use float32 or bfloat16")
+    B, T, H, dk, qp, qs = _heads("q", q, dtype, dev)
+    gqp = _expect("grad_q", grad_q, q.shape, dtype, dev)
+    dq, dkk, dwq, dwk = out or (None, None, None, None)
+    if dq is None:
+        dq = _empty(q.shape, dtype, q.device, stream)
+    elif dq.shape != q.shape:
+        raise ValueError("dq must have q's shape")
+    dqp, dqs = _heads("dq", dq, dtype, dev)[4:]
+    Hk = ks = dks = 0
+    kp = gkp = dkp = None
+    if k is not None:
+        Bk, Tk, Hk, d2, kp, ks = _heads("k", k, dtype, dev)
+        if (Bk, Tk, d2) != (B, T, dk):
+            raise ValueError("q and k must share B, T and dk")
+        gkp = _expect("grad_k", grad_k, k.shape, dtype, dev)
+        if dkk is None:
+            dkk = _empty(k.shape, dtype, k.device, stream)
+        elif dkk.shape != k.shape:
+            raise ValueError("dk must have k's shape")
+        dkp, dks = _heads("dk", dkk, dtype, dev)[4:]
+    else:
+        dkk = dwk = wk = None
+    wqp, wkp, wcode = _pair_weights(wq, wk, dk, dev)
+    p, keep = _head_problem(B, T, H, dk, code, theta, scale, pos0, flags, pos_rows, q.device)
+    dwqp = dwkp = ws = None
+    n = 0
+    if want_weight_grad:
+        if dwq is None:
+            dwq = _empty((dk,), tc.f32, q.device, stream)
+        dwqp = _expect("dwq", dwq, (dk,), tc.f32, dev)
+        if k is not None:
+            if dwk is None:
+                dwk = _empty((dk,), tc.f32, q.device, stream)
+            dwkp = _expect("dwk", dwk, (dk,), tc.f32, dev)
+        n = _lib.msr_qk_norm_rotate_backward_workspace(B * T, H, Hk, dk)
+        workspace, n = _workspace(workspace, n, q, stream)
+        ws = workspace.data_ptr()
+    else:
+        dwq = dwk = None
+    fn = _lib.msr_qk_norm_rotate_backward if tc.device() == dev else _at(dev, _lib.msr_qk_norm_rotate_backward)
+    s = fn(ctypes.byref(p), Hk, eps, qp, qs, kp, ks, wqp, wkp, wcode, gqp, gkp, dqp, dqs, dkp, dks, dwqp, dwkp, ws, n,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
+    if s:
+        _check(s)
+    return dq, dkk, dwq, dwk
+
+
+GATE_BLOCK = 64  # MSR_GATE_BLOCK
+
+
+def _gate(x, g, rate, dims):
+    code = _code("x", x)
+    if x.dim() != dims:
+        raise ValueError("x must be [B, T, D]" if dims == 3 else "x must be [B, D]")
+    dev = x.get_device()
+    return code, dev, _expect("g", g, x.shape, x.dtype, dev), _expect("rate", rate, (x.shape[-1],), _tc.f32, dev)
+
+
+def msr_gated_recurrence(x, g, rate, *, normalize=True, state_in=None, return_state=True, want_carry=False, out=None,
+                         workspace=None, stream=None):
+    """A recurrence whose decay depends on the data and the channel: h_t = a_t h_(t-1) + m_t x_t, a_t = exp(-rate
+    sigmoid(g_t)), m_t = sqrt(1 - a_t^2) (normalize) or 1.  x, g [B, T, D] float32 or bfloat16, rate [D] float32 >= 0,
+    state_in [B, D] float32 or None (zeros).  Returns (h, state, carry), None where not wanted: h in x's type, state
+    [B, D] float32 after the last token, carry [B, ceil(T / 64), D] float32: the states before the tokens 0, 64, 128, ...,
+    which the backward pass takes.  out: tensors to write, in the same order (state may be state_in)."""
+    tc = _tc or _setup()
+    code, dev, gp, rp = _gate(x, g, rate, 3)
+    B, T, D = shape = x.shape
+    h, state, carry = out or (None, None, None)
+    if h is None:
+        h = _empty(shape, x.dtype, x.device, stream)
+    hp = _expect("h", h, shape, x.dtype, dev)
+    ip = sp = cp = None
+    if state_in is not None:
+        ip = _expect("state_in", state_in, (B, D), tc.f32, dev)
+    if return_state:
+        if state is None:
+            state = _empty((B, D), tc.f32, x.device, stream)
+        sp = _expect("state", state, (B, D), tc.f32, dev)
+    else:
+        state = None
+    if want_carry:
+        cshape = (B, (T + GATE_BLOCK - 1) // GATE_BLOCK, D)
+        if carry is None:
+            carry = _empty(cshape, tc.f32, x.device, stream)
+        cp = _expect("carry", carry, cshape, tc.f32, dev)
+    else:
+        carry = None
+    ws, n = None, _lib.msr_gated_recurrence_workspace(B, T, D, 0)
+    if n:
+        workspace, n = _workspace(workspace, n, x, stream)
+        ws = workspace.data_ptr()
+    fn = _lib.msr_gated_recurrence if tc.device() == dev else _at(dev, _lib.msr_gated_recurrence)
+    s = fn(B, T, D, code, normalize, x.data_ptr(), gp, rp, ip, hp, sp, cp, ws, n,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
+    if s:
+        _check(s)
+    return h, state, carry
+
+
+def msr_gated_recurrence_step(x, g, state, rate, *, normalize=True, state_out=None, out=None, stream=None):
+    """One token of msr_gated_recurrence: x, g [B, D]; state [B, D] float32, updated in place unless state_out is given.
+    Returns h [B, D]."""
+    tc = _tc or _setup()
+    code, dev, gp, rp = _gate(x, g, rate, 2)
+    B, D = shape = x.shape
+    ip = _expect("state", state, shape, tc.f32, dev)
+    sp = ip if state_out is None else _expect("state_out", state_out, shape, tc.f32, dev)
+    if out is None:
+        out = _empty(shape, x.dtype, x.device, stream)
+    hp = _expect("out", out, shape, x.dtype, dev)
+    fn = _lib.msr_gated_recurrence_step if tc.device() == dev else _at(dev, _lib.msr_gated_recurrence_step)
+    s = fn(B, D, code, normalize, x.data_ptr(), gp, rp, ip, sp, hp,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
+    if s:
+        _check(s)
+    return out
+
+
+def msr_gated_recurrence_backward(x, g, rate, grad_h, *, normalize=True, state_in=None, carry=None, grad_state=None,
+                                  want_rate_grad=True, want_state_grad=True, out=None, workspace=None, stream=None):
+    """Gradients of msr_gated_recurrence: x, g, rate, state_in as there, carry the forward call's (None: the forward pass
+    runs again for it), grad_h = dL/dh in x's type, grad_state = dL/dstate float32 [B, D] or None.  Returns (dx, dg,
+    drate, dstate_in): dx, dg in x's type, drate [D] and dstate_in [B, D] float32, None where not wanted.  out: tensors
+    to write, in the same order."""
+    tc = _tc or _setup()
+    code, dev, gp, rp = _gate(x, g, rate, 3)
+    B, T, D = shape = x.shape
+    dhp = _expect("grad_h", grad_h, shape, x.dtype, dev)
+    dx, dg, drate, dstate = out or (None, None, None, None)
+    if dx is None:
+        dx = _empty(shape, x.dtype, x.device, stream)
+    if dg is None:
+        dg = _empty(shape, x.dtype, x.device, stream)
+    dxp, dgp = _expect("dx", dx, shape, x.dtype, dev), _expect("dg", dg, shape, x.dtype, dev)
+    ip = cp = gsp = drp = dsp = None
+    if state_in is not None:
+        ip = _expect("state_in", state_in, (B, D), tc.f32, dev)
+    if carry is not None:
+        cp = _expect("carry", carry, (B, (T + GATE_BLOCK - 1) // GATE_BLOCK, D), tc.f32, dev)
+    if grad_state is not None:
+        gsp = _expect("grad_state", grad_state, (B, D), tc.f32, dev)
+    if want_rate_grad:
+        if drate is None:
+            drate = _empty((D,), tc.f32, x.device, stream)
+        drp = _expect("drate", drate, (D,), tc.f32, dev)
+    else:
+        drate = None
+    if want_state_grad:
+        if dstate is None:
+            dstate = _empty((B, D), tc.f32, x.device, stream)
+        dsp = _expect("dstate_in", dstate, (B, D), tc.f32, dev)
+    else:
+        dstate = None
+    ws, n = None, _lib.msr_gated_recurrence_workspace(B, T, D, 2 if carry is None else 1)
+    if n:
+        workspace, n = _workspace(workspace, n, x, stream)
+        ws = workspace.data_ptr()
+    fn = _lib.msr_gated_recurrence_backward if tc.device() == dev else _at(dev, _lib.msr_gated_recurrence_backward)
+    s = fn(B, T, D, code, normalize, x.data_ptr(), gp, rp, ip, cp, dhp, gsp, dxp, dgp, drp, dsp, ws, n,
+           tc.raw_stream(dev) if stream is None else _handle(stream, dev))
+    if s:
+        _check(s)
+    return dx, dg, drate, dstate
+
+
+def _gradients(grads, out):
+    """The C ABI's table of the tensors (msr_gradient: four 64-bit numbers each), and their device."""
+    if not grads:
+        raise ValueError("no gradients given")
+    codes, dev, table = _tc.codes, grads[0].get_device(), []
+    if out is None:
+        for t in grads:
+            code = codes.get(t.dtype)
+            if code is None:
+                raise TypeError(f"unsupported dtype {t.dtype} of a gradient; use float32 or bfloat16")
+            if t.get_device() != dev or not t.is_contiguous():
+                raise ValueError("gradients must be contiguous tensors on one device")
+            p = t.data_ptr()
+            table += (p, p, t.numel(), code)
+    else:
+        if len(out) != len(grads):
+            raise ValueError("out must hold a tensor for each gradient")
+        for t, o in zip(grads, out):
+            dtype = t.dtype
+            code = codes.get(dtype)
+            if code is None:
+                raise TypeError(f"unsupported dtype {dtype} of a gradient; use float32 or bfloat16")
+            if (t.get_device() != dev or not t.is_contiguous() or o.get_device() != dev or not o.is_contiguous()
+                    or o.dtype is not dtype or o.shape != t.shape):
+                raise ValueError("gradients must be contiguous tensors on one device, out tensors like them")
+            table += (t.data_ptr(), o.data_ptr(), t.numel(), code)
+    if not grads[0].is_cuda:
+        raise ValueError("gradients must be device tensors")
+    return array.array("q", table), dev
+
+
+def msr_gradient_norm(grads, *, out=None, workspace=None, stream=None):
+    """The square root of the sum of the squares of all elements of `grads` (contiguous float32 and bfloat16 tensors), a
+    float32 scalar on the device (out: the one to write).  Squares and sums are float64, in a fixed order."""
+    tc = _tc or _setup()
+    grads = list(grads)
+    table, dev = _gradients(grads, None)
+    at, like = table.buffer_info()[0], grads[0]
+    if out is None:
+        out = _empty((), tc.f32, like.device, stream)
+    op = _expect("out", out, (), tc.f32, dev)
+    workspace, n = _workspace(workspace, _lib.msr_gradient_norm_workspace(at, len(grads)), like, stream)
+    fn = _lib.msr_gradient_norm if tc.device() == dev else _at(dev, _lib.msr_gradient_norm)
+    s = fn(at, len(grads), op, workspace.data_ptr(), n, tc.raw_stream(dev) if stream is None else _handle(stream, dev))
+    if s:
+        _check(s)
+    return out
+
+
+def msr_clip_gradients(grads, max_norm, *, norm=None, out=None, norm_out=None, workspace=None, stream=None):
+    """g * min(1, max_norm / norm) for every tensor g of `grads` (contiguous, float32 and bfloat16), in place or to the
+    tensors `out`.  norm: a float32 scalar on the device, e.g. one joined over processes; None: that of msr_gradient_norm,
+    formed here.  Where it is infinite or NaN the gradients stay as they are.  Returns (out or grads, norm)."""
+    tc = _tc or _setup()
+    grads = list(grads)
+    table, dev = _gradients(grads, out)
+    at, like = table.buffer_info()[0], grads[0]
+    np_ = op = ws = None
+    n = 0
+    if norm is not None:
+        np_ = _expect("norm", norm, (), tc.f32, dev)
+    else:
+        norm = _empty((), tc.f32, like.device, stream) if norm_out is None else norm_out
+        op = _expect("norm_out", norm, (), tc.f32, dev)
+        workspace, n = _workspace(workspace, _lib.msr_gradient_norm_workspace(at, len(grads)), like, stream)
+        ws = workspace.data_ptr()
+    fn = _lib.msr_clip_gradients if tc.device() == dev else _at(dev, _lib.msr_clip_gradients)
+    s = fn(at, len(grads), max_norm, np_, op, ws, n, tc.raw_stream(dev) if stream is None else _handle(stream, dev))
+    if s:
+        _check(s)
+    return grads if out is None else out, norm
 
 
 def set_kernel_events(start=None, stop=None):
