@@ -30,7 +30,6 @@ namespace {
 
 using namespace msr;
 
-constexpr int kChannels = 128;  // of a tile
 constexpr uint32_t kUnset = 0xffffffffu;  // factor bits of a word that is not published yet,
 constexpr uint32_t kState = 0x80000000u;  // and of one that holds a state: f = 0
 
@@ -41,9 +40,9 @@ struct GateArgs {
     float *state_out;               // the last state, or the gradient of state_in (may be NULL)
     float *carry;                   // [B][blocks][D] states before each block of 64 tokens: written (may be NULL), or read
     float *part;                    // backward: [B tiles][D] sums of -s dl (may be NULL)
-    uint64_t *words;                // [B column blocks][tiles][128]
-    uint32_t *tickets;              // [B column blocks]
-    int B, T, D, tiles, cols, blocks;  // cols: blocks of 128 channels
+    uint64_t *words;                // [chains][tiles][channels]; chains: B cols, column blocks of a batch row
+    uint32_t *tickets;              // [groups]
+    int B, T, D, tiles, cols, blocks, groups;
 };
 
 // ---- factors ----------------------------------------------------------------
@@ -52,221 +51,287 @@ struct GateArgs {
 // one that is nearly gone loses accuracy.  -0 is f = 0.
 __device__ __forceinline__ bool far(float z) { return (int)__float_as_uint(z) < 0; }
 __device__ __forceinline__ float apply(float z, float p) { return fmaf(-z, p, far(z) ? 0.f : p); }
-__device__ __forceinline__ float both(float y, float z) {  // the product of two factors
-    const float ey = far(y) ? 1.f + y : y, ez = far(z) ? 1.f + z : z;
-    const float f = (far(y) ? -y : 1.f - y) * (far(z) ? -z : 1.f - z);
-    return f < 0.5f ? -f : fmaf(-ey, ez, ey) + ez;
-}
 
+// Exponents are kept in base 2: k = q log2(e), with log2(e) in the channel's rate.
 constexpr float kLog2e = 1.44269504f;
 
-// 1 - exp(-q): the series where it is small (the first term left out is 5e-8 of the sum at 1/4)
-__device__ __forceinline__ float lost(float q) {
-    const float p = q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, -1.f / 720.f, 1.f / 120.f), -1.f / 24.f), 1.f / 6.f), -0.5f), 1.f);
-    const float d = 1.f - __builtin_amdgcn_exp2f(-kLog2e * q);
-    return q < 0.25f ? p : d;
+// 1 - 2^-k: the series where that is small (the first term left out is 4e-7 of the sum at 1/32; 1 - 2^-k is off by 1.4e-6
+// of itself there at most, and by less above)
+__device__ __forceinline__ float lost(float k) {
+    const float p = k * fmaf(k, fmaf(k, 0.0555041087f, -0.240226507f), 0.693147181f);
+    const float d = 1.f - __builtin_amdgcn_exp2f(-k);
+    return k < 0.03125f ? p : d;
 }
 
-__device__ __forceinline__ float factor(float q) {
-    const float f = __builtin_amdgcn_exp2f(-kLog2e * q);
-    return f < 0.5f ? -f : lost(q);
+__device__ __forceinline__ float factor(float k) {
+    const float f = __builtin_amdgcn_exp2f(-k);
+    return f < 0.5f ? -f : lost(k);
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * g)); }
 
+// Tokens past the last: a gate of -infinity, whose decay is 1 and whose input counts for nothing.
+template <int ROWS>
+__device__ __forceinline__ void close_gate(Raw8<uint16_t, ROWS> &r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.u[i] = 0xff80ff80u;
+    if constexpr (ROWS == kAny) r.down = 0;
+}
+template <int ROWS>
+__device__ __forceinline__ void close_gate(Raw8<float, ROWS> &r) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.a[i] = r.b[i] = -__builtin_inff();
+    if constexpr (ROWS == kAny) r.down = 0;
+}
+
 // ---- words between tiles ------------------------------------------------------
+// Every tile has a word: its pair (f, h), which maps the state p before the tile to f p + h; then, f being 0 (kState), the
+// state after it.
 __device__ __forceinline__ void publish(uint64_t *w, float z, float h) {
     const uint32_t u = z != z ? 0x7fc00000u : __float_as_uint(z);  // no NaN that looks unpublished
     __hip_atomic_store(w, (uint64_t)u << 32 | __float_as_uint(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ uint64_t word(const uint64_t *w) {
+    return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint32_t kind(uint64_t v) { return (uint32_t)(v >> 32); }
+__device__ __forceinline__ float value(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float after(uint64_t v, float p) {  // the state after its stretch
+    return kind(v) == kState ? value(v) : apply(__uint_as_float(kind(v)), p) + value(v);
+}
 
-// The state that tile n of a chain starts from: back over the words of tiles n - 1, n - 2, ... (kChannels apart) to the
-// latest state, then forward again over the pairs since.  Where that state lies depends on how far the other workgroups
-// are; the result does not, since every tile's end state is formed from its start state by the same pair.
+constexpr int kSpins = 1 << 22;  // polls: seconds, far beyond any wait; an end for callers who share a workspace
+constexpr int kLook = 8;         // tiles looked at
+constexpr int kSleep = 8;        // between polls, in 64 clocks
+
+// The state that tile n of a chain starts from: that of the latest of the kLook tiles before it whose state is known, and
+// the pairs since (w: tile 0's word; a tile's words are CH apart).  Which one that is depends on how far the other
+// workgroups are; the result does not, since every tile's end state is formed from its start state by the same pair.
+template <int CH>
 __device__ __forceinline__ float look_back(const uint64_t *w, int n) {
-    constexpr int N = 8;  // words under way at a time
-    uint64_t v[N];
+    uint64_t v[kLook];
+    int from = -1;  // the latest state with no word missing after it
+    for (int spin = 0; spin < kSpins; ++spin) {
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) v[i] = word(w + (int64_t)max(n - 1 - i, 0) * CH);
+        bool open = false;
+#pragma unroll
+        for (int i = 0; i < kLook; ++i) {
+            if (from < 0 && !open && kind(v[i]) == kState) from = i;
+            open = open || kind(v[i]) == kUnset;
+        }
+        if (from >= 0) break;
+        __builtin_amdgcn_s_sleep(kSleep);
+    }
     float p = 0.f;
-    int j = n - 1;
-    auto fetch = [&] {
 #pragma unroll
-        for (int i = 0; i < N; ++i)
-            v[i] = __hip_atomic_load(w + (int64_t)max(j - i, 0) * kChannels, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    };
-    auto forward = [&] {
-#pragma unroll
-        for (int i = N - 1; i >= 0; --i) {
-            const uint32_t u = (uint32_t)(v[i] >> 32);
-            const float h = __uint_as_float((uint32_t)v[i]);
-            p = u == kState ? h : apply(__uint_as_float(u), p) + h;
-        }
-    };
-    for (int idle = 0; idle < (1 << 22);) {  // far beyond any wait (seconds): an end for a caller who shares the workspace
-        fetch();
-        bool found = false, open = false;  // a state; a word that is not published, after any state
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const uint32_t u = (uint32_t)(v[i] >> 32);
-            open = open || (!found && u == kUnset);
-            found = found || u == kState;
-        }
-        if (!open && found) break;
-        if (!open)
-            j -= N, idle = 0;
-        else
-            ++idle;
-    }
-    // an older word than the latest state may not be published yet: it is not used
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if ((uint32_t)(v[i] >> 32) == kUnset) v[i] = (uint64_t)kState << 32;
-    forward();
-    while (j < n - 1) {
-        j += N;
-        fetch();
-        forward();
-    }
+    for (int i = kLook - 1; i >= 0; --i)
+        if (i <= from) p = after(v[i], p);
     return p;
 }
 
-// the next tile of this workgroup's channel block
-__device__ __forceinline__ int take_tile(const GateArgs &a, uint32_t chain, int *slot) {
-    if (a.tiles == 1) return 0;
-    if (threadIdx.x == 0)
-        *slot = (int)__hip_atomic_fetch_add(a.tickets + chain, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    __syncthreads();
-    return *slot;
-}
+// The tiles are dealt out in order of time by `groups` counters: ticket q of a group's n chains is tile q / n of its chain
+// q % n.  Workgroups go to the XCDs in turn: with eight groups or more, a chain stays on one.
+struct Deal {
+    uint32_t group, n, tickets;
+    uint32_t *counter;
+    __device__ __forceinline__ explicit Deal(const GateArgs &a) {
+        n = (uint32_t)a.B * a.cols / a.groups;
+        group = blockIdx.x % a.groups;
+        tickets = n * a.tiles;
+        counter = a.tickets + group;
+    }
+    __device__ __forceinline__ uint32_t take() const {
+        return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+};
 
-template <typename T, int ROWS, int W, int S, bool NORM>
-__global__ __launch_bounds__(64 * W) void gate_kernel(GateArgs a) {
-    constexpr int NS = 4 * W, TILE = S * NS;
-    static_assert(TILE % MSR_GATE_BLOCK == 0 && MSR_GATE_BLOCK % S == 0, "");
-    __shared__ float zs[NS][kChannels], hs[NS][kChannels];
-    __shared__ int slot;
-    const uint32_t chains = (uint32_t)a.B * a.cols, chain = blockIdx.x % chains;
-    const int tile = take_tile(a, chain, &slot);
-    const int b = chain / a.cols, c0 = chain % a.cols * kChannels;
-    const int sl = threadIdx.x >> 4, e0 = 8 * (threadIdx.x & 15), left = a.D - c0 - e0;
-    const int64_t t0 = (int64_t)tile * TILE;
-    const int mine = (int)min(max((int64_t)a.T - t0 - sl * S, (int64_t)0), (int64_t)S);  // tokens of this slice
-    const int64_t at = ((int64_t)b * a.T + t0 + sl * S) * a.D + c0 + e0;
-    float rate[8], lo[S][8], u[S][8];
-    {
-        Raw8<T, ROWS> rx[S], rg[S];
+// a tile of a group's tickets
+struct Place {
+    int tile, b, c0;
+    uint32_t chain;
+    __device__ __forceinline__ Place(const GateArgs &a, const Deal &d, uint32_t q, int channels) {
+        tile = (int)(q / d.n);
+        chain = d.group + a.groups * (q - tile * d.n);
+        b = (int)(chain / a.cols);
+        c0 = (int)(chain - b * a.cols) * channels;
+    }
+};
+
+// ---- the forward pass -----------------------------------------------------------
+// a slice's tokens: 1 - e and m x of each, their sum of k, and the state that they make of 0.  raw(t, x, g) gives a
+// token's eight channels; mine: the slice's tokens that exist
+template <int S, bool NORM, typename Raw>
+__device__ __forceinline__ void slice(const Raw &raw, const float (&rate)[8], float (&keep)[S][8], float (&u)[S][8],
+                                      float (&k)[8], float (&h)[8]) {
 #pragma unroll
-        for (int t = 0; t < S; ++t) {
-            rx[t].load(static_cast<const T *>(a.x) + at + (int64_t)t * a.D, t < mine ? left : 0);
-            rg[t].load(static_cast<const T *>(a.g) + at + (int64_t)t * a.D, t < mine ? left : 0);
-        }
-        load8<ROWS>(a.rate + c0 + e0, left, rate);
-        float q[8], h[8];
+    for (int i = 0; i < 8; ++i) k[i] = h[i] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = h[i] = 0.f;
-#pragma unroll
-        for (int t = 0; t < S; ++t) {
-            float gt[8];
-            rx[t].get(u[t]);
-            rg[t].get(gt);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float qt = t < mine ? rate[i] * sigmoid(gt[i]) : 0.f, e = lost(qt);  // past the last token: kept
-                if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, 2.f * e));
-                lo[t][i] = e;
-                q[i] += qt;
-                h[i] = fmaf(-e, h[i], h[i] + u[t][i]);
-            }
-        }
+    for (int t = 0; t < S; ++t) {
+        float g[8];
+        raw(t, u[t], g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            zs[sl][e0 + i] = factor(q[i]);
-            hs[sl][e0 + i] = h[i];
+            const float kt = rate[i] * sigmoid(g[i]), e = lost(kt);
+            if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e));
+            keep[t][i] = 1.f - e;
+            k[i] += kt;
+            h[i] = fmaf(keep[t][i], h[i], u[t][i]);
         }
+    }
+}
+
+// What one thread does per channel c between a tile's barriers: from the slices' k and ends to the states that they
+// start from (in hs), by way of the tile's own.
+template <int NS, int S, int CH>
+__device__ __forceinline__ void join_slices(const GateArgs &a, const Place &pl, float (&ks)[NS][CH], float (&hs)[NS][CH], int c) {
+    const bool live = pl.c0 + c < a.D;
+    const int64_t at = (int64_t)pl.b * a.D + pl.c0 + c;
+    uint64_t *w = a.words + (uint64_t)pl.chain * a.tiles * CH + c;
+    float k = 0.f, h = 0.f, p = 0.f;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        k += ks[i][c];
+        h = fmaf(__builtin_amdgcn_exp2f(-ks[i][c]), h, hs[i][c]);
+    }
+    const float z = factor(k);
+    if (pl.tile == 0) {
+        if (a.state_in && live) p = a.state_in[at];
+    } else {
+        if (pl.tile + 1 < a.tiles) publish(w + (int64_t)pl.tile * CH, z, h);
+        p = look_back<CH>(w, pl.tile);
+    }
+    const float last = apply(z, p) + h;
+    if (pl.tile + 1 < a.tiles)
+        publish(w + (int64_t)pl.tile * CH, -0.f, last);
+    else if (a.state_out && live)
+        a.state_out[at] = last;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int64_t t = (int64_t)pl.tile * (NS * S) + i * S;
+        if (i * S % MSR_GATE_BLOCK == 0 && a.carry && live && t < a.T)
+            a.carry[((int64_t)pl.b * a.blocks + t / MSR_GATE_BLOCK) * a.D + pl.c0 + c] = p;
+        const float end = hs[i][c];
+        hs[i][c] = p;
+        p = fmaf(__builtin_amdgcn_exp2f(-ks[i][c]), p, end);
+    }
+}
+
+template <typename T, int ROWS, int LX, int W, int S, bool NORM>
+__global__ __launch_bounds__(64 * W) void gate_kernel(GateArgs a) {
+    constexpr int NS = 64 / LX * W, TILE = S * NS, CH = 8 * LX;
+    static_assert(TILE % MSR_GATE_BLOCK == 0 && MSR_GATE_BLOCK % S == 0, "");
+    __shared__ float ks[NS][CH], hs[NS][CH];
+    __shared__ uint32_t slot;
+    const Deal deal(a);
+    if (threadIdx.x == 0) slot = deal.take();
+    __syncthreads();
+    const Place pl(a, deal, __builtin_amdgcn_readfirstlane(slot), CH);
+    const int sl = threadIdx.x / LX, e0 = 8 * (threadIdx.x % LX), left = a.D - pl.c0 - e0;
+    const int64_t t0 = (int64_t)pl.tile * TILE + sl * S;
+    const int mine = (int)min(max((int64_t)a.T - t0, (int64_t)0), (int64_t)S);  // tokens of this slice
+    const int64_t at = ((int64_t)pl.b * a.T + t0) * a.D + pl.c0 + e0;
+    const bool whole = (int64_t)(pl.tile + 1) * TILE <= a.T && pl.c0 + CH <= a.D;
+    float keep[S][8], u[S][8];
+    {
+        Raw8<T, ROWS> rx[S], rg[S];
+        float rate[8], k[8], h[8];
+        const T *px = static_cast<const T *>(a.x) + at, *pg = static_cast<const T *>(a.g) + at;
+        if (whole) {
+#pragma unroll
+            for (int t = 0; t < S; ++t, px += a.D, pg += a.D) rx[t].load(px, 8), rg[t].load(pg, 8);
+        } else {
+#pragma unroll
+            for (int t = 0; t < S; ++t, px += a.D, pg += a.D) rx[t].load(px, t < mine ? left : 0), rg[t].load(pg, t < mine ? left : 0);
+        }
+        load8<ROWS>(a.rate + pl.c0 + e0, left, rate);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) rate[i] *= kLog2e;
+        if (mine < S) {
+#pragma unroll
+            for (int t = 0; t < S; ++t)
+                if (t >= mine) close_gate(rg[t]);
+        }
+        slice<S, NORM>([&](int t, float (&x)[8], float (&g)[8]) { rx[t].get(x), rg[t].get(g); }, rate, keep, u, k, h);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ks[sl][e0 + i] = k[i], hs[sl][e0 + i] = h[i];
     }
     __syncthreads();
-    if (threadIdx.x < kChannels) {
-        const int c = threadIdx.x;
-        const bool live = c0 + c < a.D;
-        uint64_t *w = a.words + (uint64_t)chain * a.tiles * kChannels + c;
-        float z = 0.f, h = 0.f, p = 0.f;
-        for (int i = 0; i < NS; ++i) {
-            z = both(z, zs[i][c]);
-            h = apply(zs[i][c], h) + hs[i][c];
-        }
-        if (tile > 0) {
-            if (tile + 1 < a.tiles) publish(w + (int64_t)tile * kChannels, z, h);
-            p = look_back(w, tile);
-        } else if (a.state_in && live) {
-            p = a.state_in[(int64_t)b * a.D + c0 + c];
-        }
-        const float last = apply(z, p) + h;
-        if (tile + 1 < a.tiles)
-            publish(w + (int64_t)tile * kChannels, -0.f, last);
-        else if (a.state_out && live)
-            a.state_out[(int64_t)b * a.D + c0 + c] = last;
-        for (int i = 0; i < NS; ++i) {
-            if (i * S % MSR_GATE_BLOCK == 0 && a.carry && live && t0 + i * S < a.T)
-                a.carry[((int64_t)b * a.blocks + (t0 + i * S) / MSR_GATE_BLOCK) * a.D + c0 + c] = p;
-            const float end = hs[i][c];
-            hs[i][c] = p;
-            p = apply(zs[i][c], p) + end;
-        }
-    }
+    if (threadIdx.x < CH) join_slices<NS, S, CH>(a, pl, ks, hs, threadIdx.x);
     if (!a.y) return;
     __syncthreads();
     float h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = hs[sl][e0 + i];
+    T *y = static_cast<T *>(a.y) + at;
 #pragma unroll
-    for (int t = 0; t < S; ++t) {
+    for (int t = 0; t < S; ++t, y += a.D) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = fmaf(-lo[t][i], h[i], h[i] + u[t][i]);
-        if (t < mine) store8<ROWS>(static_cast<T *>(a.y) + at + (int64_t)t * a.D, left, h);
+        for (int i = 0; i < 8; ++i) h[i] = fmaf(keep[t][i], h[i], u[t][i]);
+        if (whole)
+            store8<ROWS>(y, 8, h);
+        else if (t < mine)
+            store8<ROWS>(y, left, h);
     }
 }
 
 // The tiles from the last to the first: h again from the state before the
 // tile's first token, mu by looking back over the later tiles.
-template <typename T, int ROWS, int W, int S, bool NORM>
+template <typename T, int ROWS, int LX, int W, int S, bool NORM>
 __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
-    constexpr int NS = 4 * W, TILE = S * NS;
-    static_assert(TILE % MSR_GATE_BLOCK == 0, "");
-    __shared__ float zs[NS][kChannels], hs[NS][kChannels], ms[NS][kChannels];
-    __shared__ int slot;
-    const uint32_t chains = (uint32_t)a.B * a.cols, chain = blockIdx.x % chains;
-    const int n = take_tile(a, chain, &slot), tile = a.tiles - 1 - n;
-    const int b = chain / a.cols, c0 = chain % a.cols * kChannels;
-    const int sl = threadIdx.x >> 4, e0 = 8 * (threadIdx.x & 15), left = a.D - c0 - e0;
+    constexpr int NS = 64 / LX * W, TILE = S * NS, CH = 8 * LX;
+    static_assert(TILE % MSR_GATE_BLOCK == 0 && 2 * CH <= 64 * W, "");
+    __shared__ float ks[NS][CH], hs[NS][CH], ms[NS][CH];
+    __shared__ uint32_t slot;
+    const Deal deal(a);
+    if (threadIdx.x == 0) slot = deal.take();
+    __syncthreads();
+    const Place pl(a, deal, __builtin_amdgcn_readfirstlane(slot), CH);
+    const int n = pl.tile, tile = a.tiles - 1 - n, b = pl.b, c0 = pl.c0;
+    const int sl = threadIdx.x / LX, e0 = 8 * (threadIdx.x % LX), left = a.D - c0 - e0;
     const int64_t t0 = (int64_t)tile * TILE;
     const int mine = (int)min(max((int64_t)a.T - t0 - sl * S, (int64_t)0), (int64_t)S);
     const int64_t at = ((int64_t)b * a.T + t0 + sl * S) * a.D + c0 + e0;
-    Raw8<T, ROWS> rx[S], rd[S];
-    float rate[8], lo[S][8], sg[S][8];
+    const bool whole = t0 + TILE <= a.T && c0 + CH <= a.D;
+    float start = 0.f;  // the state before the tile, for the thread that needs it
+    if (threadIdx.x >= CH && threadIdx.x < 2 * CH && c0 + (int)threadIdx.x - CH < a.D)
+        start = a.carry[((int64_t)b * a.blocks + t0 / MSR_GATE_BLOCK) * a.D + c0 + threadIdx.x - CH];
+    Raw8<T, ROWS> rd[S];
+    float rate[8], lo[S][8], sg[S][8], u[S][8];
     {
-        Raw8<T, ROWS> rg[S];
+        Raw8<T, ROWS> rx[S], rg[S];
+        const T *px = static_cast<const T *>(a.x) + at, *pg = static_cast<const T *>(a.g) + at, *pd = static_cast<const T *>(a.dh) + at;
+        if (whole) {
 #pragma unroll
-        for (int t = 0; t < S; ++t) {
-            rx[t].load(static_cast<const T *>(a.x) + at + (int64_t)t * a.D, t < mine ? left : 0);
-            rg[t].load(static_cast<const T *>(a.g) + at + (int64_t)t * a.D, t < mine ? left : 0);
-            rd[t].load(static_cast<const T *>(a.dh) + at + (int64_t)t * a.D, t < mine ? left : 0);
+            for (int t = 0; t < S; ++t, px += a.D, pg += a.D, pd += a.D) rx[t].load(px, 8), rg[t].load(pg, 8), rd[t].load(pd, 8);
+        } else {
+#pragma unroll
+            for (int t = 0; t < S; ++t, px += a.D, pg += a.D, pd += a.D) {
+                const int l = t < mine ? left : 0;
+                rx[t].load(px, l), rg[t].load(pg, l), rd[t].load(pd, l);
+            }
         }
         load8<ROWS>(a.rate + c0 + e0, left, rate);
-        float q[8], h[8], mu[8];
+        if (mine < S) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[i] = h[i] = mu[i] = 0.f;
+            for (int t = 0; t < S; ++t)
+                if (t >= mine) close_gate(rg[t]);
+        }
+        float k[8], h[8], mu[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) k[i] = h[i] = mu[i] = 0.f;
 #pragma unroll
         for (int t = 0; t < S; ++t) {
-            float x[8];
-            rx[t].get(x);
+            rx[t].get(u[t]);
             rg[t].get(sg[t]);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sg[t][i] = t < mine ? sigmoid(sg[t][i]) : 0.f;
-                const float qt = rate[i] * sg[t][i], e = lost(qt);
-                if constexpr (NORM) x[i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, 2.f * e));
+                sg[t][i] = sigmoid(sg[t][i]);
+                const float kt = rate[i] * kLog2e * sg[t][i], e = lost(kt);
+                if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e));
                 lo[t][i] = e;
-                q[i] += qt;
-                h[i] = fmaf(-e, h[i], h[i] + x[i]);
+                k[i] += kt;
+                h[i] = fmaf(1.f - e, h[i], u[t][i]);
             }
         }
 #pragma unroll
@@ -274,98 +339,108 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
             float d[8];
             rd[t].get(d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float lam = d[i] + mu[i];
-                mu[i] = fmaf(-lo[t][i], lam, lam);
-            }
+            for (int i = 0; i < 8; ++i) mu[i] = (1.f - lo[t][i]) * (d[i] + mu[i]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            zs[sl][e0 + i] = factor(q[i]);
+            ks[sl][e0 + i] = k[i];
             hs[sl][e0 + i] = h[i];
             ms[sl][e0 + i] = mu[i];
         }
     }
     __syncthreads();
-    if (threadIdx.x < kChannels) {
+    if (threadIdx.x < CH) {
         const int c = threadIdx.x;
         const bool live = c0 + c < a.D;
-        uint64_t *w = a.words + (uint64_t)chain * a.tiles * kChannels + c;
-        float z = 0.f, m = 0.f, p = 0.f;
+        uint64_t *w = a.words + (uint64_t)pl.chain * a.tiles * CH + c;
+        float k = 0.f, m = 0.f, p = 0.f;
+#pragma unroll
         for (int i = NS - 1; i >= 0; --i) {
-            z = both(z, zs[i][c]);
-            m = apply(zs[i][c], m) + ms[i][c];
+            k += ks[i][c];
+            m = fmaf(__builtin_amdgcn_exp2f(-ks[i][c]), m, ms[i][c]);
         }
-        if (n > 0 && tile > 0) publish(w + (int64_t)n * kChannels, z, m);
-        if (live) p = a.carry[((int64_t)b * a.blocks + t0 / MSR_GATE_BLOCK) * a.D + c0 + c];
-        for (int i = 0; i < NS; ++i) {
-            const float end = hs[i][c];
-            hs[i][c] = p;
-            p = apply(zs[i][c], p) + end;
+        const float z = factor(k);
+        if (n == 0) {
+            if (a.state_in && live) p = a.state_in[(int64_t)b * a.D + c0 + c];
+        } else {
+            if (tile > 0) publish(w + (int64_t)n * CH, z, m);
+            p = look_back<CH>(w, n);
         }
-        p = 0.f;
-        if (n > 0)
-            p = look_back(w, n);
-        else if (a.state_in && live)
-            p = a.state_in[(int64_t)b * a.D + c0 + c];
         const float last = apply(z, p) + m;
         if (tile > 0)
-            publish(w + (int64_t)n * kChannels, -0.f, last);
+            publish(w + (int64_t)n * CH, -0.f, last);
         else if (a.state_out && live)
             a.state_out[(int64_t)b * a.D + c0 + c] = last;
+#pragma unroll
         for (int i = NS - 1; i >= 0; --i) {
             const float end = ms[i][c];
             ms[i][c] = p;
-            p = apply(zs[i][c], p) + end;
+            p = fmaf(__builtin_amdgcn_exp2f(-ks[i][c]), p, end);
+        }
+    } else if (threadIdx.x - CH < CH) {  // the states, from the one before the tile, in the other waves
+        const int c = threadIdx.x - CH;
+        float p = start;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const float end = hs[i][c];
+            hs[i][c] = p;
+            p = fmaf(__builtin_amdgcn_exp2f(-ks[i][c]), p, end);
         }
     }
     __syncthreads();
+    // what was formed of these is formed again: kept across the barriers, it would not fit the registers
+#pragma unroll
+    for (int t = 0; t < S; ++t) {
+        rd[t].forget();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(lo[t][i]));
+    }
     float before[S][8], mu[8], dr[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) before[0][i] = hs[sl][e0 + i], mu[i] = ms[sl][e0 + i], dr[i] = 0.f;
 #pragma unroll
-    for (int t = 0; t + 1 < S; ++t) {
-        float x[8];
-        rx[t].get(x);
+    for (int t = 0; t + 1 < S; ++t)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float e = lo[t][i];
-            if constexpr (NORM) x[i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, 2.f * e));
-            before[t + 1][i] = fmaf(-e, before[t][i], before[t][i] + x[i]);
-        }
-    }
+        for (int i = 0; i < 8; ++i) before[t + 1][i] = fmaf(1.f - lo[t][i], before[t][i], u[t][i]);
+    const int64_t row = (int64_t)(S - 1) * a.D;
+    T *dxp = static_cast<T *>(a.y) + at + row, *dgp = static_cast<T *>(a.dg) + at + row;
 #pragma unroll
-    for (int t = S - 1; t >= 0; --t) {
-        float x[8], dx[8], dg[8];
-        rx[t].get(x);
+    for (int t = S - 1; t >= 0; --t, dxp -= a.D, dgp -= a.D) {
+        float dx[8], dg[8];
         rd[t].get(dx);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float e = lo[t][i], lam = dx[i] + mu[i];
-            mu[i] = fmaf(-e, lam, lam);
+            const float e = lo[t][i], f = 1.f - e, lam = dx[i] + mu[i];
+            mu[i] = f * lam;
             float dl = mu[i] * before[t][i];
             dx[i] = lam;
             if constexpr (NORM) {
-                const float m2 = fmaf(-e, e, 2.f * e), r = m2 > 1e-36f ? __builtin_amdgcn_rsqf(m2) : 0.f;
+                // u = m x: x / m = u / m^2, and both are 0 where m is
+                const float m2 = fmaf(-e, e, e + e), r = __builtin_amdgcn_rsqf(fmaxf(m2, 1e-36f));
                 dx[i] = lam * (m2 * r);
-                dl = fmaf(-(mu[i] * x[i]), r * (1.f - e), dl);
+                dl = fmaf(-(mu[i] * f), u[t][i] * r * r, dl);
             }
             const float sd = sg[t][i] * dl;
             dr[i] -= sd;
             dg[i] = (sg[t][i] - 1.f) * (rate[i] * sd);
         }
-        if (t < mine) {
-            store8<ROWS>(static_cast<T *>(a.y) + at + (int64_t)t * a.D, left, dx);
-            store8<ROWS>(static_cast<T *>(a.dg) + at + (int64_t)t * a.D, left, dg);
+        if (whole) {
+            store8<ROWS>(dxp, 8, dx);
+            store8<ROWS>(dgp, 8, dg);
+        } else if (t < mine) {
+            store8<ROWS>(dxp, left, dx);
+            store8<ROWS>(dgp, left, dg);
         }
     }
     if (!a.part) return;
+    // ks is free: it was read before the last barrier
 #pragma unroll
-    for (int i = 0; i < 8; ++i) zs[sl][e0 + i] = dr[i];
+    for (int i = 0; i < 8; ++i) ks[sl][e0 + i] = dr[i];
     __syncthreads();
-    if (threadIdx.x < kChannels && c0 + threadIdx.x < a.D) {
+    if (threadIdx.x < CH && c0 + threadIdx.x < a.D) {
         float s = 0.f;
-        for (int i = 0; i < NS; ++i) s += zs[i][threadIdx.x];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) s += ks[i][threadIdx.x];
         a.part[((int64_t)b * a.tiles + tile) * a.D + c0 + threadIdx.x] = s;
     }
 }
@@ -384,19 +459,20 @@ __global__ __launch_bounds__(256) void gate_step_kernel(GateArgs a, int groups) 
     load8<ROWS>(a.rate + e0, left, rate);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float e = lost(rate[i] * sigmoid(g[i]));
-        if constexpr (NORM) x[i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, 2.f * e));
+        const float e = lost(kLog2e * rate[i] * sigmoid(g[i]));
+        if constexpr (NORM) x[i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e));
         y[i] = fmaf(-e, st[i], st[i] + x[i]);
     }
     store8<ROWS>(a.state_out + at, left, y);
     store8<ROWS>(static_cast<T *>(a.y) + at, left, y);
 }
 
-// no pair published, no tile taken
-__global__ __launch_bounds__(256) void gate_clear_kernel(uint64_t *words, int64_t n, uint32_t *tickets, int64_t chains) {
+// no word published, no tile taken: n words, then the tickets
+__global__ __launch_bounds__(256) void gate_clear_kernel(uint64_t *words, int64_t n, int64_t tickets) {
     const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x, step = (int64_t)gridDim.x * 256;
+    uint32_t *z = reinterpret_cast<uint32_t *>(words + n);
     for (int64_t i = i0; i < n; i += step) words[i] = ~0ull;
-    for (int64_t i = i0; i < chains; i += step) tickets[i] = 0;
+    for (int64_t i = i0; i < tickets; i += step) z[i] = 0;
 }
 
 __global__ __launch_bounds__(256) void gate_copy_kernel(const float *from, float *to, int64_t n) {  // from NULL: zeros
@@ -418,7 +494,11 @@ hipError_t by_type(int dtype, int D, bool norm, F f) {
     return norm ? rows(float(), std::true_type()) : rows(float(), std::false_type());
 }
 
-constexpr int kWaves = 4, kTokens = 4, kTile = 4 * kWaves * kTokens;
+constexpr int kWaves = 4, kLanes = 16, kChannels = 8 * kLanes;  // of a tile: lanes across, channels
+
+// tokens of a lane: as many as its registers hold
+constexpr int tokens_of(int dtype, bool backward) { return dtype == MSR_BF16 && !backward ? 8 : 4; }
+constexpr int tile_of(int dtype, bool backward) { return 64 / kLanes * kWaves * tokens_of(dtype, backward); }
 
 int64_t up(int64_t n, int64_t m) { return (n + m - 1) / m; }
 
@@ -430,39 +510,47 @@ hipError_t copy(const float *from, float *to, int64_t n, hipStream_t st) {
 
 // what the chains need: [words][tickets]
 struct Plan {
-    int tiles, cols, blocks;
+    int tiles, cols, blocks, groups;
     int64_t chains, words;
     size_t bytes;
 };
 
-Plan plan(int B, int T, int D) {
+constexpr int kGroups = 64;  // counters at most
+
+Plan plan(int B, int T, int D, int dtype, bool backward) {
     Plan p;
-    p.tiles = (int)up(T, kTile), p.cols = (int)up(D, kChannels), p.blocks = (int)up(T, MSR_GATE_BLOCK);
+    p.tiles = (int)up(T, tile_of(dtype, backward)), p.cols = (int)up(D, kChannels), p.blocks = (int)up(T, MSR_GATE_BLOCK);
     p.chains = (int64_t)B * p.cols, p.words = p.tiles > 1 ? p.chains * p.tiles * kChannels : 0;
-    p.bytes = p.tiles > 1 ? (size_t)(p.words * 8 + up(p.chains * 4, 256) * 256) : 0;
+    for (p.groups = kGroups; p.chains % p.groups; p.groups /= 2) {}
+    p.bytes = (size_t)p.words * 8 + kGroups * 4;
     return p;
 }
 
 hipError_t fill(GateArgs &a, const Plan &p, char *ws, hipStream_t st) {
-    a.tiles = p.tiles, a.cols = p.cols, a.blocks = p.blocks;
-    if (p.tiles <= 1) return hipSuccess;
+    a.tiles = p.tiles, a.cols = p.cols, a.blocks = p.blocks, a.groups = p.groups;
     a.words = reinterpret_cast<uint64_t *>(ws);
     a.tickets = reinterpret_cast<uint32_t *>(ws + p.words * 8);
-    const int64_t g = std::min<int64_t>(up(p.words, 1024), 2048);
-    hipLaunchKernelGGL(gate_clear_kernel, dim3((unsigned)g), dim3(256), 0, st, a.words, p.words, a.tickets, p.chains);
+    const int64_t g = std::min<int64_t>(std::max<int64_t>(up(p.words, 1024), 1), 2048);
+    hipLaunchKernelGGL(gate_clear_kernel, dim3((unsigned)g), dim3(256), 0, st, a.words, p.words, (int64_t)kGroups);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// enough for either type
 size_t gate_workspace(int B, int T, int D, bool backward, bool carry_given) {
-    const Plan p = plan(B, T, D);
-    size_t n = p.bytes;
-    if (backward) {
-        n += up((int64_t)B * p.tiles * D * 4, 256) * 256;
-        if (!carry_given) n += up((int64_t)B * p.blocks * D * 4, 256) * 256;
+    if (B == 0 || T == 0 || D == 0) return 0;
+    size_t most = 0;
+    for (int dtype : {MSR_F32, MSR_BF16}) {
+        const Plan f = plan(B, T, D, dtype, false), p = plan(B, T, D, dtype, true);
+        size_t n = f.bytes;
+        if (backward) {
+            n = up(std::max(p.bytes, carry_given ? 0 : f.bytes), 256) * 256 + up((int64_t)B * p.tiles * D * 4, 256) * 256;
+            if (!carry_given) n += up((int64_t)B * p.blocks * D * 4, 256) * 256;
+        }
+        most = std::max(most, n);
     }
-    return n;
+    return most;
 }
 
 hipError_t launch_gate(const Gate &q, char *ws, hipStream_t st) {
@@ -470,11 +558,12 @@ hipError_t launch_gate(const Gate &q, char *ws, hipStream_t st) {
     a.x = q.x, a.g = q.g, a.rate = q.rate, a.state_in = q.state_in, a.y = q.h, a.state_out = q.state_out, a.carry = q.carry;
     a.B = q.B, a.T = q.T, a.D = q.D;
     if (q.T == 0) return copy(q.state_in, q.state_out, (int64_t)q.B * q.D, st);
-    const Plan p = plan(q.B, q.T, q.D);
+    const Plan p = plan(q.B, q.T, q.D, q.dtype, false);
     hipError_t e = fill(a, p, ws, st);
     if (e != hipSuccess) return e;
     return by_type(q.dtype, q.D, q.normalize, [&](auto t, auto rows, auto norm) {
-        hipLaunchKernelGGL((gate_kernel<decltype(t), rows.value, kWaves, kTokens, norm.value>),
+        constexpr int S = tokens_of(sizeof(t) == 2 ? MSR_BF16 : MSR_F32, false);
+        hipLaunchKernelGGL((gate_kernel<decltype(t), rows.value, kLanes, kWaves, S, norm.value>),
                            dim3((unsigned)(p.chains * p.tiles)), dim3(64 * kWaves), 0, st, a);
         return hipGetLastError();
     });
@@ -497,8 +586,9 @@ hipError_t launch_gate_backward(const Gate &q, char *ws, hipStream_t st) {
         if ((e = copy(q.dstate_out, q.dstate_in, (int64_t)q.B * q.D, st)) != hipSuccess) return e;
         return copy(nullptr, q.drate, q.D, st);
     }
-    const Plan p = plan(q.B, q.T, q.D);
-    char *w = ws + p.bytes;
+    const Plan p = plan(q.B, q.T, q.D, q.dtype, true);
+    // past the words of this pass and of the forward one
+    char *w = ws + up(q.carry ? p.bytes : std::max(p.bytes, plan(q.B, q.T, q.D, q.dtype, false).bytes), 256) * 256;
     float *part = reinterpret_cast<float *>(w);
     w += up((int64_t)q.B * p.tiles * q.D * 4, 256) * 256;
     GateArgs a{};
@@ -514,7 +604,8 @@ hipError_t launch_gate_backward(const Gate &q, char *ws, hipStream_t st) {
     a.part = q.drate ? part : nullptr;
     if ((e = fill(a, p, ws, st)) != hipSuccess) return e;
     e = by_type(q.dtype, q.D, q.normalize, [&](auto t, auto rows, auto norm) {
-        hipLaunchKernelGGL((gate_backward_kernel<decltype(t), rows.value, kWaves, kTokens, norm.value>),
+        constexpr int S = tokens_of(sizeof(t) == 2 ? MSR_BF16 : MSR_F32, true);
+        hipLaunchKernelGGL((gate_backward_kernel<decltype(t), rows.value, kLanes, kWaves, S, norm.value>),
                            dim3((unsigned)(p.chains * p.tiles)), dim3(64 * kWaves), 0, st, a);
         return hipGetLastError();
     });

@@ -55,7 +55,7 @@ def blocks_of(h, state, B, D):
     return np.concatenate([first, h], 1)[:, :-1][:, ::64]
 
 
-SIZES = [(1, 1, 1), (2, 3, 5), (1, 2, 8), (1, 64, 8), (3, 65, 7), (2, 63, 128), (1, 129, 130), (2, 200, 1000), (1, 1000, 16),
+SIZES = [(1, 1, 1), (2, 3, 5), (1, 2, 8), (1, 64, 8), (3, 65, 7), (2, 63, 128), (1, 129, 130), (2, 200, 1000), (1, 1000, 16), (1, 2500, 72), (9, 1100, 40),
          (3, 777, 257), (1, 5000, 33), (64, 16, 512), (2, 2048, 128), (5, 100, 9), (1, 1025, 12), (7, 1, 300), (1, 4099, 100)]
 
 
