@@ -53,9 +53,10 @@ __device__ __forceinline__ double total(const double *sums, int n, double *red) 
     return block_sum64(x, red);
 }
 
-template <typename T>
-__device__ __forceinline__ double squares(const T *p, int64_t left) {
-    double s[2] = {0.0, 0.0};
+// A chunk's values, eight to a lane: f(group, values, how many of them exist).  Of a chunk that the tensor's end cuts, the
+// last eight are read together and moved down (Raw8), but for tensors of fewer than eight.
+template <typename T, typename F>
+__device__ __forceinline__ void for_groups(const T *p, int64_t left, bool tiny, const F &f) {
     if (left >= kChunk) {
         Raw8<T, kAny> r[kGroups];
 #pragma unroll
@@ -64,37 +65,50 @@ __device__ __forceinline__ double squares(const T *p, int64_t left) {
         for (int u = 0; u < kGroups; ++u) {
             float v[8];
             r[u].get(v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i & 1] = fma((double)v[i], (double)v[i], s[i & 1]);
+            f((u * kThreads + threadIdx.x) * 8, v, 8);
+        }
+    } else if (tiny) {
+        if (threadIdx.x == 0) {
+            float v[8];
+            load8<kTiny>(p, (int)left, v);
+            f(0, v, (int)left);
         }
     } else {
-        for (int i = threadIdx.x; i < left; i += kThreads) {
-            const double v = load(p, i);
-            s[0] = fma(v, v, s[0]);
+        Raw8<T, kAny> r[kGroups];
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            const int i = (u * kThreads + threadIdx.x) * 8;
+            r[u].load(p + i, (int)left - i);
+        }
+#pragma unroll
+        for (int u = 0; u < kGroups; ++u) {
+            const int i = (u * kThreads + threadIdx.x) * 8;
+            float v[8];
+            r[u].get(v);
+            f(i, v, (int)left - i);
         }
     }
+}
+
+template <typename T>
+__device__ __forceinline__ double squares(const T *p, int64_t left, bool tiny) {
+    double s[2] = {0.0, 0.0};
+    for_groups(p, left, tiny, [&](int, const float (&v)[8], int) {  // what does not exist is zero
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i & 1] = fma((double)v[i], (double)v[i], s[i & 1]);
+    });
     return s[0] + s[1];
 }
 
 template <typename T>
-__device__ __forceinline__ void scale(const T *p, T *o, int64_t left, double f) {
+__device__ __forceinline__ void scale(const T *p, T *o, int64_t left, bool tiny, double f) {
     // fp32: one rounding of the product with the fp64 factor; bf16: the fp32 product's rounding is far below its own
     auto one = [&](float v) { return sizeof(T) == 4 ? (float)((double)v * f) : v * (float)f; };
-    if (left >= kChunk) {
-        Raw8<T, kAny> r[kGroups];
+    for_groups(p, left, tiny, [&](int at, float (&v)[8], int n) {
 #pragma unroll
-        for (int u = 0; u < kGroups; ++u) r[u].load(p + (u * kThreads + threadIdx.x) * 8, 8);
-#pragma unroll
-        for (int u = 0; u < kGroups; ++u) {
-            float v[8];
-            r[u].get(v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = one(v[i]);
-            store8<kAny>(o + (u * kThreads + threadIdx.x) * 8, 8, v);
-        }
-    } else {
-        for (int i = threadIdx.x; i < left; i += kThreads) store(o, i, one(load(p, i)));
-    }
+        for (int i = 0; i < 8; ++i) v[i] = one(v[i]);
+        store8<kAny>(o + at, n, v);
+    });
 }
 
 __global__ __launch_bounds__(kThreads) void gradient_norm_kernel(ClipArgs a) {
@@ -104,8 +118,9 @@ __global__ __launch_bounds__(kThreads) void gradient_norm_kernel(ClipArgs a) {
     for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
         while (e + 1 < a.count && c >= a.t[e + 1].start) ++e;
         const int64_t at = (int64_t)(c - a.t[e].start) * kChunk, left = a.t[e].n - at;
-        s += a.t[e].bf16 ? squares(static_cast<const uint16_t *>(a.t[e].g) + at, left)
-                         : squares(static_cast<const float *>(a.t[e].g) + at, left);
+        const bool tiny = a.t[e].n < 8;
+        s += a.t[e].bf16 ? squares(static_cast<const uint16_t *>(a.t[e].g) + at, left, tiny)
+                         : squares(static_cast<const float *>(a.t[e].g) + at, left, tiny);
     }
     s = block_sum64(s, red);
     if (threadIdx.x == 0) a.sums[blockIdx.x] = s;
@@ -132,10 +147,11 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
         while (c < a.t[e].start) --e;
         if (!clip && a.t[e].g == a.t[e].out) continue;
         const int64_t at = (int64_t)(c - a.t[e].start) * kChunk, left = a.t[e].n - at;
+        const bool tiny = a.t[e].n < 8;
         if (a.t[e].bf16)
-            scale(static_cast<const uint16_t *>(a.t[e].g) + at, static_cast<uint16_t *>(a.t[e].out) + at, left, f);
+            scale(static_cast<const uint16_t *>(a.t[e].g) + at, static_cast<uint16_t *>(a.t[e].out) + at, left, tiny, f);
         else
-            scale(static_cast<const float *>(a.t[e].g) + at, static_cast<float *>(a.t[e].out) + at, left, f);
+            scale(static_cast<const float *>(a.t[e].g) + at, static_cast<float *>(a.t[e].out) + at, left, tiny, f);
     }
 }
 
@@ -185,14 +201,17 @@ hipError_t sum_squares(const msr_gradient *t, int64_t count, double *sums, int64
 
 }  // namespace
 
-// one double per workgroup of the norm, and one for their total
+// one double per workgroup of the norm (its launches end at kTable tensors, or sooner where one is cut), and one for their
+// total: at least as many as batches() makes
 size_t gradient_norm_workspace(const msr_gradient *t, int64_t count) {
-    int64_t n = 0;
-    (void)batches(t, count, [&](ClipArgs &a) {
-        n += std::min(a.chunks, kSums);
-        return hipSuccess;
-    });
-    return (size_t)(n + 1) * sizeof(double);
+    int64_t chunks = 0, launches = count / kTable + 1;
+    for (int64_t i = 0; i < count; ++i) {
+        const int64_t c = (t[i].n + kChunk - 1) / kChunk;
+        chunks += c;
+        launches += c >> 29;
+    }
+    launches += chunks >> 29;
+    return (size_t)(std::min(chunks, launches * kSums) + 1) * sizeof(double);
 }
 
 hipError_t launch_gradient_norm(const msr_gradient *t, int64_t count, float *norm, double *ws, hipStream_t st) {

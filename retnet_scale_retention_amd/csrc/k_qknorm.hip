@@ -10,6 +10,10 @@
 // A wave takes a token.  L lanes hold a head's row, eight values each, and a
 // wave 64 / L heads at a time: a lane meets the same four pairs in every head,
 // so their angles, most of the arithmetic of a row, are formed once per token.
+//
+// Bound by memory: Q and K of 16384 tokens, 16 heads of 256, bf16 84 us in a
+// loop over one set (537 MB; 100 us on changing inputs, 5.4 TB/s), their
+// gradients 151 us (805 MB, 5.3 TB/s); a 1 GiB copy reaches 5.1 TB/s.
 #include <algorithm>
 
 #include "msr_quant.hpp"
@@ -251,7 +255,9 @@ Split split(int64_t tokens, int H, int Hk, int dk, int64_t most) {
     return {(int)x, (groups + per - 1) / per, per};
 }
 
-constexpr int kForward = 4096, kBackward = 1024;
+// Gradients of 16384 tokens of 2 x 16 heads of 256: 512 workgroups 151 us, 1024 160, 384 157 (two rows of a wave under way;
+// with four 155 and 162); results alone: 4096 workgroups 84 us, 1024 85.
+constexpr int kForward = 4096, kBackward = 512;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

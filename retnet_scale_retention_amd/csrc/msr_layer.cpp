@@ -113,16 +113,24 @@ msr_status check_element_aligned(const Tensor *t, int n, size_t e) {
     return MSR_OK;
 }
 
-QkNorm qk_norm(const msr_problem *p, int32_t key_heads, float eps, int32_t weight_dtype, std::vector<float> &theta) {
+// frequencies: the problem's, or the default ones, formed once per width and host thread
+const float *frequencies(const msr_problem *p) {
+    if (p->theta) return p->theta;
+    static thread_local int dk = 0;
+    static thread_local float theta[MSR_MAX_DK / 2];
+    if (dk != p->dk)
+        for (int i = 0; i < p->dk / 2; ++i) theta[i] = (float)std::pow(10000.0, -2.0 * (double)i / (double)p->dk);
+    dk = p->dk;
+    return theta;
+}
+
+QkNorm qk_norm(const msr_problem *p, int32_t key_heads, float eps, int32_t weight_dtype) {
     QkNorm q{};
     q.pos_rows = p->pos_rows, q.pos0 = p->pos0, q.tokens = (int64_t)p->B * p->T;
     q.H[0] = p->H, q.H[1] = key_heads, q.dk = p->dk, q.T = p->T, q.dtype = p->dtype, q.w_dtype = weight_dtype;
     q.rotate = !(p->flags & MSR_FLAG_NO_ROTATE), q.eps = eps;
     q.scale = p->scale != 0.f ? p->scale : (float)(1.0 / std::sqrt((double)p->dk));
-    theta.resize(p->dk / 2);
-    for (int i = 0; i < p->dk / 2; ++i)
-        theta[i] = p->theta ? p->theta[i] : (float)std::pow(10000.0, -2.0 * (double)i / (double)p->dk);
-    q.theta = theta.data();
+    q.theta = frequencies(p);
     return q;
 }
 
@@ -338,13 +346,10 @@ msr_status msr_qk_norm_rotate(const msr_problem *p, int32_t key_heads, float eps
     if ((s = check_element_aligned(t, 2, elem(p->dtype))) != MSR_OK || (s = check_aligned(t + 2, 4)) != MSR_OK ||
         (s = check_overlap(t, 6, 4, same)) != MSR_OK)
         return s;
-    return guarded([&] {
-        std::vector<float> theta;
-        QkNorm q = qk_norm(p, key_heads, eps, weight_dtype, theta);
-        q.x[0] = Q, q.x[1] = K, q.w[0] = wq, q.w[1] = wk, q.y[0] = QO, q.y[1] = KO;
-        q.xs[0] = q_stride, q.xs[1] = k_stride, q.ys[0] = qo, q.ys[1] = ko;
-        return done(launch_qk_norm(q, false, static_cast<hipStream_t>(hip_stream)), "qk norm rotate");
-    });
+    QkNorm q = qk_norm(p, key_heads, eps, weight_dtype);
+    q.x[0] = Q, q.x[1] = K, q.w[0] = wq, q.w[1] = wk, q.y[0] = QO, q.y[1] = KO;
+    q.xs[0] = q_stride, q.xs[1] = k_stride, q.ys[0] = qo, q.ys[1] = ko;
+    return done(launch_qk_norm(q, false, static_cast<hipStream_t>(hip_stream)), "qk norm rotate");
 }
 
 size_t msr_qk_norm_rotate_backward_workspace(int64_t tokens, int32_t heads, int32_t key_heads, int32_t dk) {
@@ -398,14 +403,11 @@ msr_status msr_qk_norm_rotate_backward(const msr_problem *p, int32_t key_heads, 
             return set_error(MSR_ERR_INVALID_ARG, "%s must not overlap %s", t[i].name, t[j].name);
         }
     if ((s = check_ws(ws, ws_bytes, need)) != MSR_OK) return s;
-    return guarded([&] {
-        std::vector<float> theta;
-        QkNorm q = qk_norm(p, key_heads, eps, weight_dtype, theta);
-        q.x[0] = Q, q.x[1] = K, q.w[0] = wq, q.w[1] = wk, q.y[0] = dQ, q.y[1] = dK, q.dy[0] = dQO, q.dy[1] = dKO;
-        q.xs[0] = q_stride, q.xs[1] = k_stride, q.ys[0] = dq_stride, q.ys[1] = dk_stride;
-        q.dw[0] = dwq, q.dw[1] = dwk, q.part = static_cast<float *>(ws);
-        return done(launch_qk_norm(q, true, static_cast<hipStream_t>(hip_stream)), "qk norm rotate backward");
-    });
+    QkNorm q = qk_norm(p, key_heads, eps, weight_dtype);
+    q.x[0] = Q, q.x[1] = K, q.w[0] = wq, q.w[1] = wk, q.y[0] = dQ, q.y[1] = dK, q.dy[0] = dQO, q.dy[1] = dKO;
+    q.xs[0] = q_stride, q.xs[1] = k_stride, q.ys[0] = dq_stride, q.ys[1] = dk_stride;
+    q.dw[0] = dwq, q.dw[1] = dwk, q.part = static_cast<float *>(ws);
+    return done(launch_qk_norm(q, true, static_cast<hipStream_t>(hip_stream)), "qk norm rotate backward");
 }
 
 msr_status msr_gated_recurrence(int64_t B, int64_t T, int64_t D, int32_t dtype, int32_t normalize, const void *x,

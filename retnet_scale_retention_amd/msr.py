@@ -13,6 +13,8 @@ from __future__ import annotations
 import array
 import ctypes
 import math
+import operator
+import struct
 from pathlib import Path
 
 import numpy as np
@@ -105,7 +107,7 @@ def load():
     lib.msr_quantize.restype = ctypes.c_int
     lib.msr_scaled_matmul.argtypes = [i64, i64, i64, vp, vp, vp, vp, i32, i32, vp, vp]
     lib.msr_scaled_matmul.restype = ctypes.c_int
-    # msr_problem by address: the head norms' callers fill it with addresses (_HeadProblem)
+    # msr_problem as bytes (_HEAD_PROBLEM)
     lib.msr_qk_norm_rotate.argtypes = [vp, i32, f32, vp, i64, vp, i64, vp, vp, i32, vp, vp, vp]
     lib.msr_qk_norm_rotate_backward.argtypes = [vp, i32, f32, vp, i64, vp, i64, vp, vp, i32, vp, vp, vp, i64, vp, i64,
                                                 vp, vp, vp, sz, vp]
@@ -188,6 +190,7 @@ class _Torch:
         self.f32, self.f8, self.u8, self.empty = torch.float32, torch.float8_e4m3fn, torch.uint8, torch.empty
         self.codes = {torch.float32: MSR_F32, torch.bfloat16: MSR_BF16}
         self.raw_stream, self.device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        self.tensor = torch.Tensor
 
 
 _tc = None
@@ -639,38 +642,42 @@ def msr_scaled_matmul(a, a_scale, b, b_scale, *, out_dtype=None, out=None, strea
 
 
 # ------------------------------------------------------- next to retention
-class _HeadProblem(ctypes.Structure):
-    """msr_problem with addresses in place of pointers to floats (the head norms use neither gamma nor dv)."""
-    _fields_ = [(n, {"gamma": ctypes.c_void_p, "theta": ctypes.c_void_p}.get(n, t)) for n, t in Problem._fields_]
+_HEAD_PROBLEM = struct.Struct("=6iQQffqI4xQ")  # msr_problem, its pointers as numbers (gamma and dv are not used)
 
 
 def _heads(name, t, dtype, index):
     """(B, T, H, dk, address, elements from a token to the next) of Q or K: [B, T, H, dk], or [B, H, dk] for one token
     each, the heads of a token packed and the tokens at one distance."""
-    shape, stride = t.shape, t.stride()
-    if not t.is_cuda or t.get_device() != index or t.dtype is not dtype or len(shape) not in (3, 4):
-        raise ValueError(f"{name} must be a {dtype} [B, T, H, dk] or [B, H, dk] tensor on device {index}")
-    H, dk = shape[-2:]
-    B, T = (shape[0], 1) if len(shape) == 3 else shape[:2]
-    step = stride[0] if T == 1 else stride[1]
-    if B * T <= 1:
-        step = H * dk
-    if (stride[-1] != 1 and dk > 1) or (stride[-2] != dk and H > 1) or (B * T and step < H * dk) or (
+    shape = t.shape
+    if t.get_device() != index or t.dtype is not dtype or index < 0:
+        raise ValueError(f"{name} must be a {dtype} tensor on the device of q")
+    if len(shape) == 4:
+        B, T, H, dk = shape
+    elif len(shape) == 3:
+        (B, H, dk), T = shape, 1
+    else:
+        raise ValueError(f"{name} must be [B, T, H, dk] or [B, H, dk]")
+    if t.is_contiguous() or B * T == 0:
+        return B, T, H, dk, t.data_ptr(), H * dk
+    stride = t.stride()
+    step = H * dk if B * T == 1 else stride[0] if T == 1 else stride[1]
+    if (stride[-1] != 1 and dk > 1) or (stride[-2] != dk and H > 1) or step < H * dk or (
             B > 1 and T > 1 and stride[0] != T * step):
         raise ValueError(f"{name}: the heads of a token must be packed and all tokens at one distance; got strides {stride}")
     return B, T, H, dk, t.data_ptr(), step
 
 
 def _head_problem(B, T, H, dk, code, theta, scale, pos0, flags, pos_rows, device):
-    keep = None
+    """msr_problem as bytes, and what it points to."""
+    at = 0
     if theta is not None:
-        keep = theta if (isinstance(theta, np.ndarray) and theta.dtype == np.float32 and theta.flags.c_contiguous) else \
-            np.ascontiguousarray(theta, dtype=np.float32)
-        if keep.shape != (dk // 2,):
+        if not (type(theta) is np.ndarray and theta.dtype == np.float32 and theta.flags.c_contiguous):
+            theta = np.ascontiguousarray(theta, dtype=np.float32)
+        if theta.shape != (dk // 2,):
             raise ValueError(f"theta must hold dk/2={dk // 2} values")
-    p = _HeadProblem(B, T, H, dk, 4, code, None, None if keep is None else keep.__array_interface__["data"][0], scale, 0.0,
-                     pos0, flags, None if pos_rows is None else _pos_rows(pos_rows, B, device))
-    return p, keep
+        at = theta.__array_interface__["data"][0]
+    return _HEAD_PROBLEM.pack(B, T, H, dk, 4, code, 0, at, scale, 0.0, pos0, flags,
+                              0 if pos_rows is None else _pos_rows(pos_rows, B, device)), theta
 
 
 def _pair_weights(wq, wk, dk, index):
@@ -713,7 +720,7 @@ def msr_qk_norm_rotate(q, k=None, wq=None, wk=None, *, eps=1e-6, theta=None, sca
     wqp, wkp, wcode = _pair_weights(wq, wk, dk, dev)
     p, keep = _head_problem(B, T, H, dk, code, theta, scale, pos0, flags, pos_rows, q.device)
     fn = _lib.msr_qk_norm_rotate if tc.device() == dev else _at(dev, _lib.msr_qk_norm_rotate)
-    s = fn(ctypes.byref(p), Hk, eps, qp, qs, kp, ks, wqp, wkp, wcode, qop, kop,
+    s = fn(p, Hk, eps, qp, qs, kp, ks, wqp, wkp, wcode, qop, kop,
            tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
         _check(s)
@@ -771,7 +778,7 @@ def msr_qk_norm_rotate_backward(q, k, wq, wk, grad_q, grad_k, *, eps=1e-6, theta
     else:
         dwq = dwk = None
     fn = _lib.msr_qk_norm_rotate_backward if tc.device() == dev else _at(dev, _lib.msr_qk_norm_rotate_backward)
-    s = fn(ctypes.byref(p), Hk, eps, qp, qs, kp, ks, wqp, wkp, wcode, gqp, gkp, dqp, dqs, dkp, dks, dwqp, dwkp, ws, n,
+    s = fn(p, Hk, eps, qp, qs, kp, ks, wqp, wkp, wcode, gqp, gkp, dqp, dqs, dkp, dks, dwqp, dwkp, ws, n,
            tc.raw_stream(dev) if stream is None else _handle(stream, dev))
     if s:
         _check(s)
@@ -897,34 +904,29 @@ def msr_gated_recurrence_backward(x, g, rate, grad_h, *, normalize=True, state_i
     return dx, dg, drate, dstate
 
 
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _gradients(grads, out):
-    """The C ABI's table of the tensors (msr_gradient: four 64-bit numbers each), and their device."""
+    """The C ABI's table of the tensors (msr_gradient: four 64-bit numbers each), and their device.  Column by column: a
+    call has many tensors, and this is most of its host time."""
     if not grads:
         raise ValueError("no gradients given")
-    codes, dev, table = _tc.codes, grads[0].get_device(), []
-    if out is None:
-        for t in grads:
-            code = codes.get(t.dtype)
-            if code is None:
-                raise TypeError(f"unsupported dtype {t.dtype} of a gradient; use float32 or bfloat16")
-            if t.get_device() != dev or not t.is_contiguous():
-                raise ValueError("gradients must be contiguous tensors on one device")
-            p = t.data_ptr()
-            table += (p, p, t.numel(), code)
-    else:
-        if len(out) != len(grads):
-            raise ValueError("out must hold a tensor for each gradient")
-        for t, o in zip(grads, out):
-            dtype = t.dtype
-            code = codes.get(dtype)
-            if code is None:
-                raise TypeError(f"unsupported dtype {dtype} of a gradient; use float32 or bfloat16")
-            if (t.get_device() != dev or not t.is_contiguous() or o.get_device() != dev or not o.is_contiguous()
-                    or o.dtype is not dtype or o.shape != t.shape):
-                raise ValueError("gradients must be contiguous tensors on one device, out tensors like them")
-            table += (t.data_ptr(), o.data_ptr(), t.numel(), code)
-    if not grads[0].is_cuda:
-        raise ValueError("gradients must be device tensors")
+    T, dev, n = _tc.tensor, grads[0].get_device(), len(grads)
+    both = grads if out is None else [*grads, *out]
+    if len(both) != (n if out is None else 2 * n):
+        raise ValueError("out must hold a tensor for each gradient")
+    if dev < 0 or set(map(T.get_device, both)) != {dev} or not all(map(T.is_contiguous, both)):
+        raise ValueError("gradients and out must be contiguous tensors on one device")
+    codes = list(map(_tc.codes.get, map(_dtype_of, both)))
+    if None in codes:
+        raise TypeError("unsupported dtype of a gradient; use float32 or bfloat16")
+    sizes = list(map(T.numel, both))
+    if out is not None and (codes[:n] != codes[n:] or sizes[:n] != sizes[n:]):
+        raise ValueError("a tensor of out must have its gradient's type and size")
+    at = list(map(T.data_ptr, both))
+    table = [0] * (4 * n)
+    table[0::4], table[1::4], table[2::4], table[3::4] = at[:n], at[-n:], sizes[:n], codes[:n]
     return array.array("q", table), dev
 
 
