@@ -506,7 +506,7 @@ msr_status msr_qk_norm_rotate_backward(const msr_problem *p, int32_t key_heads, 
  *   carry (NULL: not wanted) [B][ceil(T / 64)][D] fp32: the states before the
  *   tokens 0, 64, 128, ..., for the backward pass.
  * Everything between loads and stores is fp32.  T = 0 copies the state.
- * B, T and D are at most 2^31 - 1, and B * ceil(T / 256) * ceil(D / 32) below
+ * B, T and D are at most 2^31 - 1, and B * ceil(T / 64) * ceil(D / 128) below
  * 2^24.  Outputs must not overlap anything else.  The workspace is that of
  * msr_gated_recurrence_workspace(B, T, D, 0).  Equal calls give equal
  * results.

@@ -140,8 +140,8 @@ msr_status check_gate(int64_t B, int64_t T, int64_t D, int32_t dtype) {
     if (B < 0 || T < 0 || D < 0 || B > INT32_MAX || T > INT32_MAX || D > INT32_MAX)
         return set_error(MSR_ERR_SHAPE, "B=%lld, T=%lld and D=%lld must be in 0..2^31-1", (long long)B, (long long)T,
                          (long long)D);
-    // workgroups of 256 threads, each 256 tokens or more by 32 channels: fewer than 2^32 threads in a launch
-    const int64_t tiles = std::max<int64_t>((T + 255) / 256, 1), cols = std::max<int64_t>((D + 31) / 32, 1);
+    // workgroups of 256 threads, each 64 tokens or more by 128 channels: fewer than 2^32 threads in a launch
+    const int64_t tiles = std::max<int64_t>((T + 63) / 64, 1), cols = std::max<int64_t>((D + 127) / 128, 1);
     if (B * tiles >= 1 << 24 || B * tiles * cols >= 1 << 24)
         return set_error(MSR_ERR_SHAPE, "B=%lld x T=%lld x D=%lld is too large", (long long)B, (long long)T, (long long)D);
     return MSR_OK;

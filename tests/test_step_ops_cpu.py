@@ -220,6 +220,18 @@ def test_gate_refusals():
     assert call(_0=0) == 0 and call(_2=0) == 0
 
 
+def test_a_launch_of_the_gate_has_fewer_than_2_32_threads():
+    """A workgroup of 256 threads takes 64 tokens (128 of bf16 forward) by 128 channels."""
+    lib = msr.load()
+    count = lib.msr_gated_recurrence_workspace
+    most = (1 << 24) - 1
+    for most_size, more in (((1, 64 * most, 1), (1, 64 * most + 1, 1)), ((1, 1, 128 * most), (1, 1, 128 * most + 1)),
+                            ((most, 1, 1), (most + 1, 1, 1)), ((1 << 12, 64 * 4095, 128), (1 << 12, 64 * 4095 + 1, 129))):
+        assert all(count(*most_size, i) > 0 and count(*more, i) == 0 for i in (0, 1, 2)), (most_size, more)
+        call = caller(lib.msr_gated_recurrence, [*more, 1, 1, A, B, C, D, E, F, G, H, 0, NULL])
+        refused(call(), "MSR_ERR_SHAPE", "too large")
+
+
 def test_gate_step_and_backward_refusals():
     lib = msr.load()
     call = caller(lib.msr_gated_recurrence_step, [4, 200, 1, 1, A, B, C, D, E, F, NULL])
