@@ -9,19 +9,29 @@
 // 1 - a^2 = e (2 - e): a decay next to 1, rounded, would be off by the same
 // amount at every token, 3e-5 of the state after 1000 tokens.
 //
-// A workgroup takes a tile of kTile tokens by 128 channels: 16 lanes hold a
-// token's channels (eight each), and each such group a slice of S tokens.
-// A stretch of tokens maps the state p before it to f p + H; the slices'
-// factors and ends meet in LDS, one thread per channel folds them into the
-// tile's, and every slice then runs again from the state it starts with.
+// A workgroup takes a tile of tokens by 128 channels: 16 lanes hold a token's
+// channels (eight each), and each such group a slice of S tokens.  A stretch
+// of tokens maps the state p before it to f p + H, f = 2^-k; the slices' k and
+// ends meet in LDS, one thread per channel folds them into the tile's, and
+// every slice then runs again from the state it starts with.
 //
-// Tiles of one channel block follow each other by looking back: a workgroup
-// publishes its tile's (f, H) at once, goes back over the words of the tiles
-// before it to the latest that holds an end state (f = 0), applies the pairs
-// since to it, and publishes its own end state.  The input is read once.  A
-// pair travels in one 64-bit atomic word, so no fence is needed.  Workgroups take tiles in order from a counter
-// per channel block and wait for earlier ones alone: of the tiles under way
-// the first never waits, so every wait ends.
+// Tiles of one channel block (a chain) follow each other by looking back: a
+// workgroup publishes its tile's (f, H) at once, waits until one of the kLook
+// tiles before it holds an end state (f = 0), applies the pairs since to it,
+// and publishes its own end state.  The input is read once.  A pair travels
+// in one 64-bit atomic word, so no fence is needed.  Workgroups take tiles in
+// order from a counter and wait for earlier ones alone: of the tiles under
+// way the first never waits, so every wait ends.
+//
+// Memory is the floor, and the arithmetic (two exponentials, a reciprocal and
+// a root per element) is not hidden behind it whole.  2 x 8192 x 4096 bf16:
+// 96 us (403 MB, 4.2 TB/s; a 1 GiB copy reaches 5.06): 89 without the waits,
+// 79 without the gate's arithmetic, 70 without both.  131072 x 1024: 235 us
+// (814 MB, 3.5 TB/s): 174, 240 and 165; its eight chains wait for states.
+// Gradients of 2 x 8192 x 4096: 187 us (675 MB, 3.6 TB/s).  Persistent
+// workgroups that load the next tile ahead took 118 and 305 us through
+// registers, 114 and 275 through LDS; tiles of 32 channels by 512 tokens 114
+// and 253.
 #include <algorithm>
 
 #include "msr_quant.hpp"
@@ -101,8 +111,8 @@ __device__ __forceinline__ float after(uint64_t v, float p) {  // the state afte
 }
 
 constexpr int kSpins = 1 << 22;  // polls: seconds, far beyond any wait; an end for callers who share a workspace
-constexpr int kLook = 8;         // tiles looked at
-constexpr int kSleep = 8;        // between polls, in 64 clocks
+constexpr int kLook = 8;         // tiles looked at: 96 and 235 us (sizes above); with four 95 and 251, with 16 100 and 242
+constexpr int kSleep = 8;        // between polls, in 64 clocks: with two 97 and 236 us
 
 // The state that tile n of a chain starts from: that of the latest of the kLook tiles before it whose state is known, and
 // the pairs since (w: tile 0's word; a tile's words are CH apart).  Which one that is depends on how far the other
@@ -133,20 +143,22 @@ __device__ __forceinline__ float look_back(const uint64_t *w, int n) {
 // The tiles are dealt out in order of time by `groups` counters: ticket q of a group's n chains is tile q / n of its chain
 // q % n.  Workgroups go to the XCDs in turn: with eight groups or more, a chain stays on one.
 struct Deal {
-    uint32_t group, n, tickets;
+    uint32_t group, n;
     uint32_t *counter;
     __device__ __forceinline__ explicit Deal(const GateArgs &a) {
         n = (uint32_t)a.B * a.cols / a.groups;
         group = blockIdx.x % a.groups;
-        tickets = n * a.tiles;
         counter = a.tickets + group;
     }
-    __device__ __forceinline__ uint32_t take() const {
-        return __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __device__ __forceinline__ uint32_t take(const GateArgs &a, uint32_t *slot) const {  // by all threads of a workgroup
+        if (a.tiles == 1) return blockIdx.x / a.groups;  // no tile waits for another
+        if (threadIdx.x == 0) *slot = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __syncthreads();
+        return __builtin_amdgcn_readfirstlane(*slot);
     }
 };
 
-// a tile of a group's tickets
+// the tile that ticket q of a group is
 struct Place {
     int tile, b, c0;
     uint32_t chain;
@@ -160,7 +172,7 @@ struct Place {
 
 // ---- the forward pass -----------------------------------------------------------
 // a slice's tokens: 1 - e and m x of each, their sum of k, and the state that they make of 0.  raw(t, x, g) gives a
-// token's eight channels; mine: the slice's tokens that exist
+// token's eight channels
 template <int S, bool NORM, typename Raw>
 __device__ __forceinline__ void slice(const Raw &raw, const float (&rate)[8], float (&keep)[S][8], float (&u)[S][8],
                                       float (&k)[8], float (&h)[8]) {
@@ -224,9 +236,7 @@ __global__ __launch_bounds__(64 * W) void gate_kernel(GateArgs a) {
     __shared__ float ks[NS][CH], hs[NS][CH];
     __shared__ uint32_t slot;
     const Deal deal(a);
-    if (threadIdx.x == 0) slot = deal.take();
-    __syncthreads();
-    const Place pl(a, deal, __builtin_amdgcn_readfirstlane(slot), CH);
+    const Place pl(a, deal, deal.take(a, &slot), CH);
     const int sl = threadIdx.x / LX, e0 = 8 * (threadIdx.x % LX), left = a.D - pl.c0 - e0;
     const int64_t t0 = (int64_t)pl.tile * TILE + sl * S;
     const int mine = (int)min(max((int64_t)a.T - t0, (int64_t)0), (int64_t)S);  // tokens of this slice
@@ -284,9 +294,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     __shared__ float ks[NS][CH], hs[NS][CH], ms[NS][CH];
     __shared__ uint32_t slot;
     const Deal deal(a);
-    if (threadIdx.x == 0) slot = deal.take();
-    __syncthreads();
-    const Place pl(a, deal, __builtin_amdgcn_readfirstlane(slot), CH);
+    const Place pl(a, deal, deal.take(a, &slot), CH);
     const int n = pl.tile, tile = a.tiles - 1 - n, b = pl.b, c0 = pl.c0;
     const int sl = threadIdx.x / LX, e0 = 8 * (threadIdx.x % LX), left = a.D - c0 - e0;
     const int64_t t0 = (int64_t)tile * TILE;
@@ -496,7 +504,8 @@ hipError_t by_type(int dtype, int D, bool norm, F f) {
 
 constexpr int kWaves = 4, kLanes = 16, kChannels = 8 * kLanes;  // of a tile: lanes across, channels
 
-// tokens of a lane: as many as its registers hold
+// Tokens of a lane.  bf16 forward: 96 us (2 x 8192 x 4096) and 235 (131072 x 1024) with eight, 103 and 366 with four.
+// Gradients, whose registers hold more of each token: 187 us with four, 215 with eight.  fp32 holds twice the bits.
 constexpr int tokens_of(int dtype, bool backward) { return dtype == MSR_BF16 && !backward ? 8 : 4; }
 constexpr int tile_of(int dtype, bool backward) { return 64 / kLanes * kWaves * tokens_of(dtype, backward); }
 
@@ -530,7 +539,8 @@ hipError_t fill(GateArgs &a, const Plan &p, char *ws, hipStream_t st) {
     a.tiles = p.tiles, a.cols = p.cols, a.blocks = p.blocks, a.groups = p.groups;
     a.words = reinterpret_cast<uint64_t *>(ws);
     a.tickets = reinterpret_cast<uint32_t *>(ws + p.words * 8);
-    const int64_t g = std::min<int64_t>(std::max<int64_t>(up(p.words, 1024), 1), 2048);
+    if (p.tiles == 1) return hipSuccess;  // neither is used: 7.5 us for 10.0 (8 x 100 x 4096 bf16)
+    const int64_t g = std::min<int64_t>(up(p.words, 1024), 2048);
     hipLaunchKernelGGL(gate_clear_kernel, dim3((unsigned)g), dim3(256), 0, st, a.words, p.words, (int64_t)kGroups);
     return hipGetLastError();
 }
