@@ -954,6 +954,8 @@ def msr_clip_gradients(grads, max_norm, *, norm=None, out=None, norm_out=None, w
     formed here.  Where it is infinite or NaN the gradients stay as they are.  Returns (out or grads, norm)."""
     tc = _tc or _setup()
     grads = list(grads)
+    if out is not None:
+        out = list(out)
     table, dev = _gradients(grads, out)
     at, like = table.buffer_info()[0], grads[0]
     np_ = op = ws = None

@@ -114,6 +114,23 @@ def test_large_small_and_non_finite_gradients():
     assert float(norm) == float("inf") and torch.equal(out[0], over[0])
 
 
+def test_iterables_and_the_same_tensor_twice():
+    torch, dev = torch_dev()
+    msr = _msr()
+    g = [torch.randn(1000, device=dev), torch.randn(30, device=dev).bfloat16()]
+    want, norm = msr.msr_clip_gradients(g, 0.25, out=[torch.empty_like(t) for t in g])
+    out, n2 = msr.msr_clip_gradients(iter(g), 0.25, out=(torch.empty_like(t) for t in g))
+    assert torch.equal(norm, n2) and len(out) == 2 and all(torch.equal(a, b) for a, b in zip(out, want))
+    # for the norm a tensor may be there twice, also read for two outputs, but not scaled twice in place
+    both = msr.msr_gradient_norm([g[0], g[0]])
+    assert abs(float(both) - 2 ** 0.5 * float(g[0].double().norm())) <= 1e-6 * float(both)
+    out, _ = msr.msr_clip_gradients([g[0], g[0]], 0.25, out=[torch.empty_like(g[0]) for _ in range(2)])
+    assert torch.equal(out[0], out[1])
+    for args in (dict(), dict(out=[out[0], out[0]]), dict(out=[g[0], out[1]]), dict(out=[out[0], g[0]])):
+        with pytest.raises(msr.MsrError, match="overlaps"):
+            msr.msr_clip_gradients([g[0], g[0]], 0.25, **args)
+
+
 def test_more_than_two_to_the_31_elements():
     torch, dev = torch_dev()
     msr = _msr()
