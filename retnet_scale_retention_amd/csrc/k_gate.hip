@@ -236,7 +236,9 @@ __global__ __launch_bounds__(64 * W) void gate_kernel(GateArgs a) {
     __shared__ float ks[NS][CH], hs[NS][CH];
     __shared__ uint32_t slot;
     const Deal deal(a);
-    const Place pl(a, deal, deal.take(a, &slot), CH);
+    const uint32_t q = deal.take(a, &slot);
+    if (q >= deal.n * a.tiles) return;  // calls at once that share a workspace: wrong results, but nothing outside it
+    const Place pl(a, deal, q, CH);
     const int sl = threadIdx.x / LX, e0 = 8 * (threadIdx.x % LX), left = a.D - pl.c0 - e0;
     const int64_t t0 = (int64_t)pl.tile * TILE + sl * S;
     const int mine = (int)min(max((int64_t)a.T - t0, (int64_t)0), (int64_t)S);  // tokens of this slice
@@ -294,7 +296,9 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     __shared__ float ks[NS][CH], hs[NS][CH], ms[NS][CH];
     __shared__ uint32_t slot;
     const Deal deal(a);
-    const Place pl(a, deal, deal.take(a, &slot), CH);
+    const uint32_t q = deal.take(a, &slot);
+    if (q >= deal.n * a.tiles) return;  // calls at once that share a workspace: wrong results, but nothing outside it
+    const Place pl(a, deal, q, CH);
     const int n = pl.tile, tile = a.tiles - 1 - n, b = pl.b, c0 = pl.c0;
     const int sl = threadIdx.x / LX, e0 = 8 * (threadIdx.x % LX), left = a.D - c0 - e0;
     const int64_t t0 = (int64_t)tile * TILE;
