@@ -7,6 +7,12 @@
 // are formed and added in fp64, so that no finite gradient overflows or
 // vanishes; each workgroup writes one sum, and whoever needs the total adds
 // the sums in the same order (no atomics, the same norm on every run).
+//
+// Bound by memory: two reads and a write where the gradients exceed the
+// caches.  Five fp32 tensors of 403 MB together: 220 us in a loop, 231 on
+// changing inputs (1.2 GB, 5.2 TB/s; a 1 GiB copy reaches 5.06).  60 bf16
+// tensors of 25 MB together: 29 us of kernels; the call's 41 are the host's,
+// who writes the table.
 #include <algorithm>
 
 #include "msr_quant.hpp"
@@ -47,9 +53,9 @@ __device__ __forceinline__ double block_sum64(double x, double *red) {
 }
 
 // the total of n sums, the same in every workgroup that forms it
-__device__ __forceinline__ double total(const double *sums, int n, double *red) {
+__device__ __forceinline__ double total(const double *sums, int64_t n, double *red) {
     double x = 0.0;
-    for (int i = threadIdx.x; i < n; i += kThreads) x += sums[i];
+    for (int64_t i = threadIdx.x; i < n; i += kThreads) x += sums[i];
     return block_sum64(x, red);
 }
 
@@ -126,7 +132,7 @@ __global__ __launch_bounds__(kThreads) void gradient_norm_kernel(ClipArgs a) {
     if (threadIdx.x == 0) a.sums[blockIdx.x] = s;
 }
 
-__global__ __launch_bounds__(kThreads) void gradient_total_kernel(double *sums, int n, double *out, float *norm) {
+__global__ __launch_bounds__(kThreads) void gradient_total_kernel(double *sums, int64_t n, double *out, float *norm) {
     __shared__ double red[4];
     const double s = total(sums, n, red);
     if (threadIdx.x == 0) {
@@ -218,7 +224,7 @@ hipError_t launch_gradient_norm(const msr_gradient *t, int64_t count, float *nor
     int64_t n = 0;
     const hipError_t e = sum_squares(t, count, ws + 1, n, st);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(gradient_total_kernel, dim3(1), dim3(kThreads), 0, st, ws + 1, (int)n, nullptr, norm);
+    hipLaunchKernelGGL(gradient_total_kernel, dim3(1), dim3(kThreads), 0, st, ws + 1, n, nullptr, norm);
     return hipGetLastError();
 }
 
@@ -231,7 +237,7 @@ hipError_t launch_clip_gradients(const msr_gradient *t, int64_t count, float max
         if ((e = sum_squares(t, count, sums, n, st)) != hipSuccess) return e;
         // every workgroup adds up to 2048 sums by itself; more of them are added once
         if (n > 2048 || n == 0) {
-            hipLaunchKernelGGL(gradient_total_kernel, dim3(1), dim3(kThreads), 0, st, sums, (int)n, ws, n ? nullptr : norm_out);
+            hipLaunchKernelGGL(gradient_total_kernel, dim3(1), dim3(kThreads), 0, st, sums, n, ws, n ? nullptr : norm_out);
             if ((e = hipGetLastError()) != hipSuccess || n == 0) return e;
             sums = ws, n = 1;
         }

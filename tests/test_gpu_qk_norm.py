@@ -242,6 +242,43 @@ def test_the_forms_take_its_results():
     assert out_err(down(o), ro) < TOL["bf16"] and out_err(down(s)[:, None], np.asarray(rs)[:, None]) < TOL["bf16"]
 
 
+def test_offsets_past_32_bits():
+    # rows do not depend on where they lie: the same bits as in a short call
+    torch, dev = torch_dev()
+    msr = _msr()
+    T, H, dk, n = 65600, 128, 256, 40
+    assert T * H * dk > 1 << 31
+    tail, _ = heads(torch, dev, 1, n, H, dk, "bf16", 15)
+    grad, _ = heads(torch, dev, 1, n, H, dk, "bf16", 16)
+    q = torch.zeros(1, T, H, dk, dtype=torch.bfloat16, device=dev)
+    dy = torch.zeros_like(q)
+    q[:, -n:], dy[:, -n:] = tail, grad
+    y, _ = msr.msr_qk_norm_rotate(q)
+    want, _ = msr.msr_qk_norm_rotate(tail, pos0=T - n)
+    assert torch.equal(y[:, -n:], want) and not y[:, :-n].any()
+    del y
+    dx, _, dw, _ = msr.msr_qk_norm_rotate_backward(q, None, None, None, dy, None)
+    wx, _, ww, _ = msr.msr_qk_norm_rotate_backward(tail, None, None, None, grad, None, pos0=T - n)
+    assert torch.equal(dx[:, -n:], wx) and not dx[:, :-n].any()
+    # sums of the same 5120 rows in two orders: each within 5120 roundings of the sum of the terms' magnitudes, which over
+    # a row are at most |u x r| <= |dy| sqrt(dk), u being dy turned and x r of mean square 1
+    room = 2 * 5120 * U * float(grad.double().square().sum(-1).sqrt().sum()) * dk ** 0.5
+    assert float((dw - ww).abs().max()) <= room
+    del dx, q, dy
+    # three tokens, 2^30 + 24 elements from one to the next
+    step = (1 << 30) + 24
+    flat = torch.zeros(2 * step + 32, dtype=torch.bfloat16, device=dev)
+    view = torch.as_strided(flat, (1, 3, 2, 16), (3 * step, step, 16, 1))
+    x, _ = heads(torch, dev, 1, 3, 2, 16, "bf16", 17)
+    view.copy_(x)
+    out = torch.zeros_like(flat)
+    dv = torch.as_strided(out, view.shape, view.stride())
+    assert torch.equal(msr.msr_qk_norm_rotate(view)[0], msr.msr_qk_norm_rotate(x)[0])
+    gx, _ = heads(torch, dev, 1, 3, 2, 16, "bf16", 18)
+    msr.msr_qk_norm_rotate_backward(view, None, None, None, gx, None, out=(dv, None, None, None))
+    assert torch.equal(dv, msr.msr_qk_norm_rotate_backward(x, None, None, None, gx, None)[0])
+
+
 def test_in_a_graph_and_on_another_stream():
     torch, dev = torch_dev()
     msr = _msr()
