@@ -41,7 +41,21 @@ struct ClipArgs {
     float max_norm;
 };
 
-static_assert(sizeof(ClipArgs) <= 4096, "a kernel's arguments");
+static_assert(sizeof(ClipArgs) <= 4096 && kTable <= 128, "a kernel's arguments; two tensors to a lane");
+
+// The tensor of chunk c: the starts lie one to a lane (two for the first kTable - 64), and a vote counts those up to c.  A
+// walk along the table waits for a scalar load per tensor.
+struct Find {
+    int lo, hi;
+    __device__ __forceinline__ explicit Find(const ClipArgs &a) {
+        const int l = threadIdx.x & 63;
+        lo = l < a.count ? a.t[l].start : INT32_MAX;
+        hi = l + 64 < a.count ? a.t[l + 64].start : INT32_MAX;
+    }
+    __device__ __forceinline__ int operator()(int c) const {
+        return __builtin_amdgcn_readfirstlane(__popcll(__ballot(lo <= c)) + __popcll(__ballot(hi <= c)) - 1);
+    }
+};
 
 __device__ __forceinline__ double block_sum64(double x, double *red) {
 #pragma unroll
@@ -120,9 +134,9 @@ __device__ __forceinline__ void scale(const T *p, T *o, int64_t left, bool tiny,
 __global__ __launch_bounds__(kThreads) void gradient_norm_kernel(ClipArgs a) {
     __shared__ double red[4];
     double s = 0.0;
-    int e = 0;
+    const Find find(a);
     for (int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-        while (e + 1 < a.count && c >= a.t[e + 1].start) ++e;
+        const int e = find(c);
         const int64_t at = (int64_t)(c - a.t[e].start) * kChunk, left = a.t[e].n - at;
         const bool tiny = a.t[e].n < 8;
         s += a.t[e].bf16 ? squares(static_cast<const uint16_t *>(a.t[e].g) + at, left, tiny)
@@ -148,9 +162,9 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
     if (a.norm_out && blockIdx.x == 0 && threadIdx.x == 0) *a.norm_out = (float)norm;
     const bool clip = norm > (double)a.max_norm && norm <= 3.40282347e38;  // neither infinity, as fp32, nor NaN
     const double f = clip ? (double)a.max_norm / norm : 1.0;
-    int e = a.count - 1;
+    const Find find(a);
     for (int c = a.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
-        while (c < a.t[e].start) --e;
+        const int e = find(c);
         if (!clip && a.t[e].g == a.t[e].out) continue;
         const int64_t at = (int64_t)(c - a.t[e].start) * kChunk, left = a.t[e].n - at;
         const bool tiny = a.t[e].n < 8;
