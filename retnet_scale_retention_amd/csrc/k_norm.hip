@@ -329,11 +329,11 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 // slices (eight loads of four columns under way), the slices in pairs, pairs
 // of pairs, ... (one after the other, the last sums' roundings were most of
 // the weight gradient's error: 1.7e-7 of its norm for 3001 x 1000 fp32, not 1.0e-7).
-// The second row of workgroups takes the second array of parts to out1.
-__global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out0, float *out1, int parts, int d) {
+// The second row of workgroups takes the second array of parts to out1.  c0: the launch's first column.
+__global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out0, float *out1, int parts, int d, int c0) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     __shared__ float red[64][33];
-    const int q = 4 * (threadIdx.x & 7), c = (int)blockIdx.x * 32 + q, sl = threadIdx.x >> 3;
+    const int q = 4 * (threadIdx.x & 7), c = c0 + (int)blockIdx.x * 32 + q, sl = threadIdx.x >> 3;
     float *out = blockIdx.y ? out1 : out0;
     if (!out) return;
     part += (size_t)blockIdx.y * parts * d;
@@ -366,7 +366,7 @@ __global__ __launch_bounds__(512) void column_sum_kernel(const float *part, floa
         for (int n = 32; n > 0; n /= 2)
 #pragma unroll
             for (int i = 0; i < n; ++i) t[i] += t[i + n];
-        const int o = (int)blockIdx.x * 32 + threadIdx.x;
+        const int o = c0 + (int)blockIdx.x * 32 + threadIdx.x;
         if (o < d) out[o] = t[0];
     }
 }
@@ -464,6 +464,12 @@ hipError_t launch_rmsnorm_backward(int64_t rows, int d, int dtype, const void *h
 }
 
 hipError_t launch_column_sum(const float *part, float *out0, float *out1, int parts, int d, hipStream_t st) {
-    hipLaunchKernelGGL(column_sum_kernel, dim3((d + 31) / 32, out1 ? 2 : 1), dim3(512), 0, st, part, out0, out1, parts, d);
-    return hipGetLastError();
+    constexpr int most = 1 << 26;  // columns of a launch: 2^30 threads, fewer than 2^32 of both rows
+    for (int64_t c0 = 0; c0 < d; c0 += most) {
+        const int n = (int)std::min<int64_t>(d - c0, most);
+        hipLaunchKernelGGL(column_sum_kernel, dim3((n + 31) / 32, out1 ? 2 : 1), dim3(512), 0, st, part, out0, out1, parts, d, (int)c0);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }

@@ -279,6 +279,27 @@ def test_offsets_past_32_bits():
     del x, g, h, dx, dg
 
 
+def test_more_channels_than_a_launch_of_the_sums_holds():
+    # 2^28 channels and some: 2^23 workgroups of 512 threads in one launch of the rates' sums would be 2^32 threads
+    torch, dev = torch_dev()
+    msr = _msr()
+    D = (1 << 28) + 1000
+    x, g, dh = (torch.randn(1, 2, D, device=dev, dtype=torch.bfloat16) for _ in range(3))
+    r = torch.rand(D, device=dev) * 2
+    h, last, carry = msr.msr_gated_recurrence(x, g, r, want_carry=True)
+    got = msr.msr_gated_recurrence_backward(x, g, r, dh, carry=carry)
+    for c in (0, (1 << 26) - 70, (1 << 27) - 5, (1 << 28) - 60, D - 100):
+        n = slice(c, c + 100)
+        xf, gf, df, rf = down(x[..., n].contiguous()), down(g[..., n].contiguous()), down(dh[..., n].contiguous()), down(r[n])
+        want, bound = so.gate(xf, gf, rf, None)
+        close(h[..., n].contiguous(), want, bound, "bf16", "h")
+        close(last[..., n].contiguous(), want[:, -1], bound[:, -1], "f32", "state")
+        (wx, wg, wr, _), (bx, bg, br, _) = so.gate_backward(xf, gf, rf, None, df, None)
+        close(got[0][..., n].contiguous(), wx, bx, "bf16", "dx")
+        close(got[1][..., n].contiguous(), wg, bg, "bf16", "dg")
+        close(got[2][n].contiguous(), wr, br, "f32", "drate")
+
+
 @pytest.mark.parametrize("B,T,D,dtype", [(2, 1000, 200, "bf16"), (1, 3000, 64, "f32")])
 def test_in_a_graph_and_on_two_streams(B, T, D, dtype):
     torch, dev = torch_dev()
