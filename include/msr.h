@@ -465,7 +465,8 @@ msr_status msr_scaled_matmul(int64_t m, int64_t n, int64_t k, const void *a, con
  * of 16-byte alignment (pointer, stride and dk) are faster.  QO may be Q where
  * that is packed, KO K; otherwise outputs must not overlap anything.
  * Rows of which every value is zero give zeros; rows whose squares overflow
- * fp32 give zeros too.
+ * fp32 give zeros too, and with eps 0 rows whose squares vanish there (their
+ * gradients are zeros as well).
  */
 msr_status msr_qk_norm_rotate(const msr_problem *p, int32_t key_heads, float eps, const void *Q, int64_t q_stride,
                               const void *K, int64_t k_stride, const void *wq, const void *wk, int32_t weight_dtype,

@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256) void qk_norm_kernel(QkArgs a) {
                     raw[u].get(v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-                    const float r = s / sqrtf(group_sum<L>(ss) / dims + a.eps);
+                    const float ms = group_sum<L>(ss) / dims + a.eps, r = ms == 0.f ? 0.f : s / sqrtf(ms);  // NaN stays
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float p = v[2 * i] * r * w[k][2 * i], q = v[2 * i + 1] * r * w[k][2 * i + 1];
@@ -179,7 +179,7 @@ __global__ __launch_bounds__(256) void qk_norm_backward_kernel(QkArgs a) {
                         gx = fmaf(v[i], g[i] * w[k][i], gx);
                     }
                     // r^2 = d / (sum(x^2) + d eps)
-                    const float t2 = fmaf(a.eps, dims, group_sum<L>(ss)), r = sqrtf(dims / t2);
+                    const float t2 = fmaf(a.eps, dims, group_sum<L>(ss)), r = t2 == 0.f ? 0.f : sqrtf(dims / t2);
                     gx = group_sum<L>(gx);
                     const float c = r == 0.f ? 0.f : gx / t2;  // squares past fp32: n is 0, whatever the sum came to
                     if (head < H) {

@@ -191,6 +191,31 @@ def test_zero_tiny_huge_and_non_finite_rows():
     near(dw, rdw, 256 * U * mw, "f32", "dw")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_eps(dtype):
+    torch, dev = torch_dev()
+    msr = _msr()
+    q, _ = heads(torch, dev, 2, 3, 3, 40, dtype, 20)
+    q[0, 1] = 0.0
+    q[1, 2, 1] = 1e-30  # its squares are 0 in fp32
+    q[1, 0, 0, 3] = float("nan")
+    dy, _ = heads(torch, dev, 2, 3, 3, 40, dtype, 21)
+    y, _ = msr.msr_qk_norm_rotate(q, eps=0.0)
+    dq, _, dw, _ = msr.msr_qk_norm_rotate_backward(q, None, None, None, dy, None, eps=0.0)
+    for t in (y, dq):
+        assert not t[0, 1].any() and not t[1, 2, 1].any()
+        assert bool(torch.isnan(t[1, 0, 0]).all()) and int(torch.isnan(t).sum()) == 40
+    th = so.default_theta(40)
+    for b, t in ((0, 0), (0, 2), (1, 1)):
+        one = lambda x: down(x[b:b + 1, t:t + 1].contiguous())
+        want, size = so.qk_norm(one(q), None, positions(1, 1, t), th, 0.0, 1.0)
+        near(y[b:b + 1, t:t + 1].contiguous(), want, 64 * U * size, dtype, "y")
+        dx, _, mx, _ = so.qk_norm_backward(one(q), None, one(dy), positions(1, 1, t), th, 0.0, 1.0)
+        near(dq[b:b + 1, t:t + 1].contiguous(), dx, 128 * U * mx, dtype, "dx")
+    clean = torch.nan_to_num(q, 0.0)
+    assert bool(torch.isfinite(msr.msr_qk_norm_rotate_backward(clean, None, None, None, dy, None, eps=0.0)[2]).all())
+
+
 def test_far_positions():
     torch, dev = torch_dev()
     msr = _msr()
