@@ -17,7 +17,7 @@
 //
 // Tiles of one channel block (a chain) follow each other by looking back: a
 // workgroup publishes its tile's (f, H) at once, waits until one of the kLook
-// tiles before it holds an end state (f = 0), applies the pairs since to it,
+// tiles before it holds an end state, applies the pairs since to it,
 // and publishes its own end state.  The input is read once.  A pair travels
 // in one 64-bit atomic word, so no fence is needed.  Workgroups take tiles in
 // order from a counter and wait for earlier ones alone: of the tiles under
@@ -40,8 +40,8 @@ namespace {
 
 using namespace msr;
 
-constexpr uint32_t kUnset = 0xffffffffu;  // factor bits of a word that is not published yet,
-constexpr uint32_t kState = 0x80000000u;  // and of one that holds a state: f = 0
+// factor bits, of NaNs that no factor has, of a word that is not published yet and of one that holds a state
+constexpr uint32_t kUnset = 0xffffffffu, kState = 0xfffffffeu;
 
 struct GateArgs {
     const void *x, *g, *dh;         // dh: backward only
@@ -95,12 +95,15 @@ __device__ __forceinline__ void close_gate(Raw8<float, ROWS> &r) {
 }
 
 // ---- words between tiles ------------------------------------------------------
-// Every tile has a word: its pair (f, h), which maps the state p before the tile to f p + h; then, f being 0 (kState), the
-// state after it.
-__device__ __forceinline__ void publish(uint64_t *w, float z, float h) {
-    const uint32_t u = z != z ? 0x7fc00000u : __float_as_uint(z);  // no NaN that looks unpublished
+// Every tile has a word: its pair (f, h), which maps the state p before the tile to f p + h; then (kState) the state after
+// it.  A pair whose f is 0 is no state yet: 0 p is NaN where p is not finite.
+__device__ __forceinline__ void store(uint64_t *w, uint32_t u, float h) {
     __hip_atomic_store(w, (uint64_t)u << 32 | __float_as_uint(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void publish(uint64_t *w, float z, float h) {
+    store(w, z != z ? 0x7fc00000u : __float_as_uint(z), h);  // one NaN for all
+}
+__device__ __forceinline__ void publish(uint64_t *w, float state) { store(w, kState, state); }
 __device__ __forceinline__ uint64_t word(const uint64_t *w) {
     return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -215,7 +218,7 @@ __device__ __forceinline__ void join_slices(const GateArgs &a, const Place &pl, 
     }
     const float last = apply(z, p) + h;
     if (pl.tile + 1 < a.tiles)
-        publish(w + (int64_t)pl.tile * CH, -0.f, last);
+        publish(w + (int64_t)pl.tile * CH, last);
     else if (a.state_out && live)
         a.state_out[at] = last;
 #pragma unroll
@@ -380,7 +383,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
         }
         const float last = apply(z, p) + m;
         if (tile > 0)
-            publish(w + (int64_t)n * CH, -0.f, last);
+            publish(w + (int64_t)n * CH, last);
         else if (a.state_out && live)
             a.state_out[(int64_t)b * a.D + c0 + c] = last;
 #pragma unroll

@@ -221,6 +221,25 @@ def test_non_finite_values_reach_what_follows_and_nothing_else(dtype):
     assert not dx.any() and not dg.any() and not dr.any()
 
 
+@pytest.mark.parametrize("rate", [0.1, 4.0, 60.0])
+def test_a_nan_reaches_every_token_after_it(rate):
+    # also through stretches whose decay is 0 in fp32 (0 NaN is NaN), in every call
+    torch, dev = torch_dev()
+    msr = _msr()
+    T, D = 5000, 300
+    x, g, dh = (torch.randn(2, T, D, device=dev) for _ in range(3))
+    r = torch.full((D,), rate, device=dev)
+    x[0, 10], dh[1, T - 10] = float("nan"), float("nan")
+    clean = torch.nan_to_num(x, 0.0)
+    for _ in range(10):
+        h, last, _ = msr.msr_gated_recurrence(x, g, r)
+        assert bool(torch.isnan(h[0, 10:]).all()) and bool(torch.isnan(last[0]).all())
+        assert bool(torch.isfinite(h[0, :10]).all()) and bool(torch.isfinite(h[1]).all())
+        dx, dg, _, ds = msr.msr_gated_recurrence_backward(clean, g, r, dh)
+        assert bool(torch.isnan(dx[1, :T - 9]).all()) and bool(torch.isnan(ds[1]).all())
+        assert bool(torch.isfinite(dx[1, T - 9:]).all()) and bool(torch.isfinite(dx[0]).all())
+
+
 @pytest.mark.parametrize("rate", [0.0, 1e-12, 50.0])
 def test_rates_at_the_ends(rate):
     torch, dev = torch_dev()
