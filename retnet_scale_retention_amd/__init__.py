@@ -8,6 +8,7 @@ from .msr import (MSR_BF16, MSR_F32, MSR_FLAG_DECAY_ROWNORM, MSR_FLAG_NO_GROUPNO
                   msr_chunkwise, msr_chunkwise_backward,
                   msr_chunkwise_noalloc, msr_clip_gradients, msr_gated_recurrence, msr_gated_recurrence_backward,
                   msr_gated_recurrence_step, msr_gradient_norm, msr_parallel, msr_qk_norm_rotate,
-                  msr_qk_norm_rotate_backward, msr_qkv_chunkwise, msr_qkv_projection, msr_quantize, msr_recurrent_step, msr_scaled_matmul,
+                  msr_qk_norm_rotate_backward, msr_qkv_chunkwise, msr_qkv_projection, msr_quantize,
+                  msr_recurrent_step, msr_scaled_matmul,
                   set_exchange, set_kernel_events,
                   workspace_size)

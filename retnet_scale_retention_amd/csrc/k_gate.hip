@@ -199,7 +199,8 @@ __device__ __forceinline__ void slice(const Raw &raw, const float (&rate)[8], fl
 // What one thread does per channel c between a tile's barriers: from the slices' k and ends to the states that they
 // start from (in hs), by way of the tile's own.
 template <int NS, int S, int CH>
-__device__ __forceinline__ void join_slices(const GateArgs &a, const Place &pl, float (&ks)[NS][CH], float (&hs)[NS][CH], int c) {
+__device__ __forceinline__ void join_slices(const GateArgs &a, const Place &pl, float (&ks)[NS][CH], float (&hs)[NS][CH],
+                                            int c) {
     const bool live = pl.c0 + c < a.D;
     const int64_t at = (int64_t)pl.b * a.D + pl.c0 + c;
     uint64_t *w = a.words + (uint64_t)pl.chain * a.tiles * CH + c;
@@ -257,7 +258,10 @@ __global__ __launch_bounds__(64 * W) void gate_kernel(GateArgs a) {
             for (int t = 0; t < S; ++t, px += a.D, pg += a.D) rx[t].load(px, 8), rg[t].load(pg, 8);
         } else {
 #pragma unroll
-            for (int t = 0; t < S; ++t, px += a.D, pg += a.D) rx[t].load(px, t < mine ? left : 0), rg[t].load(pg, t < mine ? left : 0);
+            for (int t = 0; t < S; ++t, px += a.D, pg += a.D) {
+                const int l = t < mine ? left : 0;
+                rx[t].load(px, l), rg[t].load(pg, l);
+            }
         }
         load8<ROWS>(a.rate + pl.c0 + e0, left, rate);
 #pragma unroll
@@ -315,10 +319,12 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     float rate[8], lo[S][8], sg[S][8], u[S][8];
     {
         Raw8<T, ROWS> rx[S], rg[S];
-        const T *px = static_cast<const T *>(a.x) + at, *pg = static_cast<const T *>(a.g) + at, *pd = static_cast<const T *>(a.dh) + at;
+        const T *px = static_cast<const T *>(a.x) + at, *pg = static_cast<const T *>(a.g) + at;
+        const T *pd = static_cast<const T *>(a.dh) + at;
         if (whole) {
 #pragma unroll
-            for (int t = 0; t < S; ++t, px += a.D, pg += a.D, pd += a.D) rx[t].load(px, 8), rg[t].load(pg, 8), rd[t].load(pd, 8);
+            for (int t = 0; t < S; ++t, px += a.D, pg += a.D, pd += a.D)
+                rx[t].load(px, 8), rg[t].load(pg, 8), rd[t].load(pd, 8);
         } else {
 #pragma unroll
             for (int t = 0; t < S; ++t, px += a.D, pg += a.D, pd += a.D) {

@@ -330,7 +330,8 @@ __global__ __launch_bounds__(W < 4 ? 256 : 64 * W) void rmsnorm_backward_kernel(
 // of pairs, ... (one after the other, the last sums' roundings were most of
 // the weight gradient's error: 1.7e-7 of its norm for 3001 x 1000 fp32, not 1.0e-7).
 // The second row of workgroups takes the second array of parts to out1.  c0: the launch's first column.
-__global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out0, float *out1, int parts, int d, int c0) {
+__global__ __launch_bounds__(512) void column_sum_kernel(const float *part, float *out0, float *out1, int parts, int d,
+                                                         int c0) {
     typedef float f32x4 __attribute__((ext_vector_type(4)));
     __shared__ float red[64][33];
     const int q = 4 * (threadIdx.x & 7), c = c0 + (int)blockIdx.x * 32 + q, sl = threadIdx.x >> 3;
@@ -467,7 +468,8 @@ hipError_t launch_column_sum(const float *part, float *out0, float *out1, int pa
     constexpr int most = 1 << 26;  // columns of a launch: 2^30 threads, fewer than 2^32 of both rows
     for (int64_t c0 = 0; c0 < d; c0 += most) {
         const int n = (int)std::min<int64_t>(d - c0, most);
-        hipLaunchKernelGGL(column_sum_kernel, dim3((n + 31) / 32, out1 ? 2 : 1), dim3(512), 0, st, part, out0, out1, parts, d, (int)c0);
+        hipLaunchKernelGGL(column_sum_kernel, dim3((n + 31) / 32, out1 ? 2 : 1), dim3(512), 0, st, part, out0, out1, parts,
+                           d, (int)c0);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }

@@ -77,8 +77,8 @@ __device__ __forceinline__ void angles(const QkArgs &a, int64_t tok, const float
 template <typename T, int ROWS, int L>
 __global__ __launch_bounds__(256) void qk_norm_kernel(QkArgs a) {
     constexpr int G = 64 / L, U = sizeof(T) == 2 ? 4 : 2;  // head rows of a wave at a time, and of these under way
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), e0 = 8 * (lane % L), sub = lane / L;
-    const int left = a.dk - e0;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int e0 = 8 * (lane % L), sub = lane / L, left = a.dk - e0;
     const int n0 = (a.H[0] + G - 1) / G, n1 = (a.H[1] + G - 1) / G;
     const int it0 = blockIdx.y * a.per, it1 = min(it0 + a.per, n0 + n1);
     float w[2][8], th[4];
@@ -130,8 +130,8 @@ template <typename T, int ROWS, int L>
 __global__ __launch_bounds__(256) void qk_norm_backward_kernel(QkArgs a) {
     constexpr int G = 64 / L, U = sizeof(T) == 2 ? 2 : 1;
     __shared__ float red[3][2][8][L];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), e0 = 8 * (lane % L), sub = lane / L;
-    const int left = a.dk - e0;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int e0 = 8 * (lane % L), sub = lane / L, left = a.dk - e0;
     const int n0 = (a.H[0] + G - 1) / G, n1 = (a.H[1] + G - 1) / G;
     const int it0 = blockIdx.y * a.per, it1 = min(it0 + a.per, n0 + n1);
     float w[2][8], dw[2][8], th[4];
@@ -288,7 +288,8 @@ hipError_t launch_qk_norm(const QkNorm &q, bool backward, hipStream_t st) {
     if (q.tokens > 0) {
         err = by_type(q.dtype, q.dk, al, [&](auto t, auto rows, auto l) {
             if (backward)
-                hipLaunchKernelGGL((qk_norm_backward_kernel<decltype(t), rows.value, l.value>), dim3(s.x, s.y), dim3(256), 0, st, a);
+                hipLaunchKernelGGL((qk_norm_backward_kernel<decltype(t), rows.value, l.value>), dim3(s.x, s.y), dim3(256), 0,
+                                   st, a);
             else
                 hipLaunchKernelGGL((qk_norm_kernel<decltype(t), rows.value, l.value>), dim3(s.x, s.y), dim3(256), 0, st, a);
             return hipGetLastError();
