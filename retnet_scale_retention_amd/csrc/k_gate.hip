@@ -466,7 +466,9 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     }
 }
 
-// One token: h = a state + m x.
+// One token: h = a state + m x.  Where a >= 1/2 it is taken as two numbers, 1 - e rounded and the rest that this left out,
+// so that the state's roundings are those of the two sums alone; below, where 1 - e has few digits or none, it is the
+// exponential itself.
 template <typename T, int ROWS, bool NORM>
 __global__ __launch_bounds__(256) void gate_step_kernel(GateArgs a, int groups) {
     const int64_t i0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -480,9 +482,13 @@ __global__ __launch_bounds__(256) void gate_step_kernel(GateArgs a, int groups) 
     load8<ROWS>(a.rate + e0, left, rate);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float e = lost(kLog2e * rate[i] * sigmoid(g[i]));
-        if constexpr (NORM) x[i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e));
-        y[i] = fmaf(-e, st[i], st[i] + x[i]);
+        const float k = kLog2e * rate[i] * sigmoid(g[i]), e = lost(k);
+        const float m = NORM ? __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e)) : 1.f, f = 1.f - e;
+        const bool strong = e > 0.5f;
+        const float rest = strong ? 0.f : (1.f - f) - e;
+        // the rest of an infinite state is a number
+        const float add = fmaf(m, x[i], rest * __builtin_amdgcn_fmed3f(st[i], -3.40282347e38f, 3.40282347e38f));
+        y[i] = fmaf(strong ? __builtin_amdgcn_exp2f(-k) : f, st[i], add);
     }
     store8<ROWS>(a.state_out + at, left, y);
     store8<ROWS>(static_cast<T *>(a.y) + at, left, y);

@@ -1,0 +1,64 @@
+"""The gated recurrence, its step and its gradients where a decay is strong, a
+gate wide open or hardly open, a state infinite or a tile cut by the sequence's
+end, against the formulas in float64.
+
+Tolerances, relative to each term (u = 2^-24).  The kernels' sigmoid is off by
+es = (8 + 2 |g|) u (the argument's rounding, an exponential and a reciprocal of
+1 ulp), the exponent q = rate s by es + 4 u, a decay a = exp(-q) by
+q (es + 4 u) + 4 u of itself, and m by es + 8 u at most (half of es of its
+square).  What a result is stored in adds 2^-8 (bf16) or u (fp32)."""
+import numpy as np
+import pytest
+
+from tests.gpu_util import down, torch_dev
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+STORED = {"f32": U, "bf16": 2.0 ** -8}
+
+
+def _msr():
+    import retnet_scale_retention_amd as msr
+    return msr
+
+
+def tensor(torch, dev, a, dtype="f32"):
+    t = torch.from_numpy(np.ascontiguousarray(a, np.float32)).to(dev)
+    t = t.to({"f32": torch.float32, "bf16": torch.bfloat16}[dtype])
+    return t, down(t)
+
+
+def parts(g, rate, normalize):
+    s = 1 / (1 + np.exp(-g))
+    q = rate * s
+    return s, q, np.exp(-q), np.sqrt(-np.expm1(-2 * q)) if normalize else np.ones_like(q), (8 + 2 * np.abs(g)) * U
+
+
+def near(t, want, room, dtype, name):
+    got = down(t)
+    assert got.shape == want.shape, name
+    bad = ~(np.abs(got - want) <= room + STORED[dtype] * np.abs(want) * (1 + 1e-6) + 1e-37)
+    worst = float(np.max(np.abs(got - want) / (np.abs(want) + 1e-37)))
+    assert not bad.any(), (name, int(bad.sum()), worst)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rate", [0.01, 0.5, 5.0, 12.0, 20.0, 30.0, 60.0])
+def test_a_step_keeps_what_a_strong_decay_leaves(rate, dtype):
+    torch, dev = torch_dev()
+    msr = _msr()
+    rng = np.random.default_rng([51, int(100 * rate)])
+    B, D = 7, 301
+    x, xf = tensor(torch, dev, rng.standard_normal((B, D)) * (rng.random((B, D)) < 0.7), dtype)
+    g, gf = tensor(torch, dev, 2 + 2 * rng.standard_normal((B, D)), dtype)
+    r, rf = tensor(torch, dev, np.full(D, rate))
+    st, sf = tensor(torch, dev, 10 ** rng.uniform(0, 8, (B, D)) * rng.choice([-1, 1], (B, D)))
+    for normalize in (True, False):
+        s, q, a, m, es = parts(gf, rf, normalize)
+        want = a * sf + m * xf
+        room = (q * (es + 4 * U) + 4 * U) * np.abs(a * sf) + (es + 10 * U) * np.abs(m * xf) + U * np.abs(want)
+        room += 1.2e-38 * np.abs(sf)  # a below 2^-126 counts as 0
+        out = torch.empty_like(st)
+        h = msr.msr_gated_recurrence_step(x, g, st, r, normalize=normalize, state_out=out)
+        near(out, want, room, "f32", "state")
+        near(h, want, room, dtype, "h")
