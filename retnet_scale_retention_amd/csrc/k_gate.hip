@@ -4,10 +4,13 @@
 //   lam_t = dh_t + mu_{t+1},  mu_t = a_t lam_t,  dx_t = m_t lam_t,
 //   dl_t = mu_t h_{t-1} - lam_t x_t a_t^2 / m_t   (the gradient of log a_t)
 //   dg_t = -rate s_t (1 - s_t) dl_t,  drate = -sum s_t dl_t
-// Everything is fp32 between the loads and the stores.  A step takes away
-// e_t h with e_t = 1 - a_t = -expm1(-q_t) formed without cancellation, and
-// 1 - a^2 = e (2 - e): a decay next to 1, rounded, would be off by the same
-// amount at every token, 3e-5 of the state after 1000 tokens.
+// Everything is fp32 between the loads and the stores.  a_t next to 1 is 1 -
+// e_t rounded, e_t = 1 - exp(-q_t) formed without cancellation and m_t^2 =
+// e_t (2 - e_t); a smaller a_t is its exponential itself, since 1 - e_t would
+// leave few of its digits (none from q_t = 17 on).  A rounded decay next to 1
+// is off by the same amount at every token, 3e-5 of the state after 1000: so
+// the state after a tile comes from the tile's sum of q_t (factor() below),
+// and the rounded decays count within a tile alone.
 //
 // A workgroup takes a tile of tokens by 128 channels: 16 lanes hold a token's
 // channels (eight each), and each such group a slice of S tokens.  A stretch
@@ -65,17 +68,23 @@ __device__ __forceinline__ float apply(float z, float p) { return fmaf(-z, p, fa
 // Exponents are kept in base 2: k = q log2(e), with log2(e) in the channel's rate.
 constexpr float kLog2e = 1.44269504f;
 
-// 1 - 2^-k: the series where that is small (the first term left out is 4e-7 of the sum at 1/32; 1 - 2^-k is off by 1.4e-6
-// of itself there at most, and by less above)
-__device__ __forceinline__ float lost(float k) {
-    const float p = k * fmaf(k, fmaf(k, 0.0555041087f, -0.240226507f), 0.693147181f);
-    const float d = 1.f - __builtin_amdgcn_exp2f(-k);
-    return k < 0.03125f ? p : d;
-}
+// a = 2^-k and e = 1 - a.  Where k is small, e is a series (the first term left out is 4e-7 of the sum at 1/32) and a is 1 -
+// e; elsewhere e is 1 - a, off by the exponential's error: 1.5e-6 of itself just above 1/32 as measured (by an ulp of a, that
+// is 2.8e-6, at most), and less above.
+struct Decay {
+    float e, a;
+    __device__ __forceinline__ explicit Decay(float k) {
+        const float p = k * fmaf(k, fmaf(k, 0.0555041087f, -0.240226507f), 0.693147181f);
+        const float f = __builtin_amdgcn_exp2f(-k);
+        const bool small = k < 0.03125f;
+        e = small ? p : 1.f - f;
+        a = small ? 1.f - p : f;
+    }
+};
 
 __device__ __forceinline__ float factor(float k) {
     const float f = __builtin_amdgcn_exp2f(-k);
-    return f < 0.5f ? -f : lost(k);
+    return f < 0.5f ? -f : Decay(k).e;
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * g)); }
@@ -174,7 +183,7 @@ struct Place {
 };
 
 // ---- the forward pass -----------------------------------------------------------
-// a slice's tokens: 1 - e and m x of each, their sum of k, and the state that they make of 0.  raw(t, x, g) gives a
+// a slice's tokens: a and m x of each, their sum of k, and the state that they make of 0.  raw(t, x, g) gives a
 // token's eight channels
 template <int S, bool NORM, typename Raw>
 __device__ __forceinline__ void slice(const Raw &raw, const float (&rate)[8], float (&keep)[S][8], float (&u)[S][8],
@@ -187,9 +196,10 @@ __device__ __forceinline__ void slice(const Raw &raw, const float (&rate)[8], fl
         raw(t, u[t], g);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float kt = rate[i] * sigmoid(g[i]), e = lost(kt);
-            if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e));
-            keep[t][i] = 1.f - e;
+            const float kt = rate[i] * sigmoid(g[i]);
+            const Decay d(kt);
+            if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-d.e, d.e, d.e + d.e));
+            keep[t][i] = d.a;
             k[i] += kt;
             h[i] = fmaf(keep[t][i], h[i], u[t][i]);
         }
@@ -348,7 +358,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sg[t][i] = sigmoid(sg[t][i]);
-                const float kt = rate[i] * kLog2e * sg[t][i], e = lost(kt);
+                const float kt = rate[i] * kLog2e * sg[t][i], e = Decay(kt).e;
                 if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e));
                 lo[t][i] = e;
                 k[i] += kt;
@@ -482,13 +492,14 @@ __global__ __launch_bounds__(256) void gate_step_kernel(GateArgs a, int groups) 
     load8<ROWS>(a.rate + e0, left, rate);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float k = kLog2e * rate[i] * sigmoid(g[i]), e = lost(k);
+        const Decay d(kLog2e * rate[i] * sigmoid(g[i]));
+        const float e = d.e;
         const float m = NORM ? __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e)) : 1.f, f = 1.f - e;
         const bool strong = e > 0.5f;
         const float rest = strong ? 0.f : (1.f - f) - e;
         // the rest of an infinite state is a number
         const float add = fmaf(m, x[i], rest * __builtin_amdgcn_fmed3f(st[i], -3.40282347e38f, 3.40282347e38f));
-        y[i] = fmaf(strong ? __builtin_amdgcn_exp2f(-k) : f, st[i], add);
+        y[i] = fmaf(strong ? d.a : f, st[i], add);
     }
     store8<ROWS>(a.state_out + at, left, y);
     store8<ROWS>(static_cast<T *>(a.y) + at, left, y);

@@ -62,3 +62,35 @@ def test_a_step_keeps_what_a_strong_decay_leaves(rate, dtype):
         h = msr.msr_gated_recurrence_step(x, g, st, r, normalize=normalize, state_out=out)
         near(out, want, room, "f32", "state")
         near(h, want, room, dtype, "h")
+
+
+def mostly_closed(rng, T, D, opens):
+    """Gates open at a few tokens, closed (decay 1) at the others."""
+    g = np.full((1, T, D), -60.0)
+    for t in opens:
+        g[:, t] = rng.uniform(1, 5, D)
+    return g
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,opens", [(1, [0]), (3, [0, 1, 2]), (130, [2, 71, 129]), (700, [0, 130, 600])])
+@pytest.mark.parametrize("rate", [10.0, 15.0, 20.0])
+def test_a_prompt_keeps_what_a_strong_decay_leaves(rate, T, opens, dtype):
+    torch, dev = torch_dev()
+    msr = _msr()
+    rng = np.random.default_rng([52, T, int(rate)])
+    D = 70
+    g, gf = tensor(torch, dev, mostly_closed(rng, T, D, opens), dtype)
+    r, rf = tensor(torch, dev, np.full(D, rate))
+    st, sf = tensor(torch, dev, 1e6 * rng.standard_normal((1, D)))
+    x = torch.zeros_like(g)
+    _, q, _, _, es = parts(gf, rf, True)
+    want = np.exp(-np.cumsum(q, 1)) * sf[:, None]
+    # each open token's decay, a rounding of the state; at closed ones the state stays.  Slices' sums of exponents: at most
+    # 24 additions in a row; a slice's and a tile's factor: 2 ulp each
+    per = np.where(gf > 0, q * (es + 4 * U) + 8 * U, 0)
+    room = (np.cumsum(per, 1) + 24 * U * np.cumsum(q, 1) + 4 * U * (2 + np.arange(1, T + 1) / 4)[None, :, None]) * np.abs(want)
+    for normalize in (True, False):
+        h, last, _ = msr.msr_gated_recurrence(x, g, r, normalize=normalize, state_in=st)
+        near(last, want[:, -1], room[:, -1], "f32", "state")
+        near(h, want, room, dtype, "h")
