@@ -326,7 +326,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     if (threadIdx.x >= CH && threadIdx.x < 2 * CH && c0 + (int)threadIdx.x - CH < a.D)
         start = a.carry[((int64_t)b * a.blocks + t0 / MSR_GATE_BLOCK) * a.D + c0 + threadIdx.x - CH];
     Raw8<T, ROWS> rd[S];
-    float rate[8], lo[S][8], sg[S][8], u[S][8];
+    float rate[8], keep[S][8], m[S][8], sg[S][8], u[S][8];
     {
         Raw8<T, ROWS> rx[S], rg[S];
         const T *px = static_cast<const T *>(a.x) + at, *pg = static_cast<const T *>(a.g) + at;
@@ -358,11 +358,15 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 sg[t][i] = sigmoid(sg[t][i]);
-                const float kt = rate[i] * kLog2e * sg[t][i], e = Decay(kt).e;
-                if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e));
-                lo[t][i] = e;
+                const float kt = rate[i] * kLog2e * sg[t][i];
+                const Decay d(kt);
+                if constexpr (NORM) {
+                    m[t][i] = __builtin_amdgcn_sqrtf(fmaf(-d.e, d.e, d.e + d.e));
+                    u[t][i] *= m[t][i];
+                }
+                keep[t][i] = d.a;
                 k[i] += kt;
-                h[i] = fmaf(1.f - e, h[i], u[t][i]);
+                h[i] = fmaf(keep[t][i], h[i], u[t][i]);
             }
         }
 #pragma unroll
@@ -370,7 +374,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
             float d[8];
             rd[t].get(d);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) mu[i] = (1.f - lo[t][i]) * (d[i] + mu[i]);
+            for (int i = 0; i < 8; ++i) mu[i] = keep[t][i] * (d[i] + mu[i]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -419,20 +423,15 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
         }
     }
     __syncthreads();
-    // what was formed of these is formed again: kept across the barriers, it would not fit the registers
 #pragma unroll
-    for (int t = 0; t < S; ++t) {
-        rd[t].forget();
-#pragma unroll
-        for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(lo[t][i]));
-    }
+    for (int t = 0; t < S; ++t) rd[t].forget();  // its floats, kept across the barriers, would not fit the registers
     float before[S][8], mu[8], dr[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) before[0][i] = hs[sl][e0 + i], mu[i] = ms[sl][e0 + i], dr[i] = 0.f;
 #pragma unroll
     for (int t = 0; t + 1 < S; ++t)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) before[t + 1][i] = fmaf(1.f - lo[t][i], before[t][i], u[t][i]);
+        for (int i = 0; i < 8; ++i) before[t + 1][i] = fmaf(keep[t][i], before[t][i], u[t][i]);
     const int64_t row = (int64_t)(S - 1) * a.D;
     T *dxp = static_cast<T *>(a.y) + at + row, *dgp = static_cast<T *>(a.dg) + at + row;
 #pragma unroll
@@ -441,15 +440,15 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
         rd[t].get(dx);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float e = lo[t][i], f = 1.f - e, lam = dx[i] + mu[i];
-            mu[i] = f * lam;
+            const float lam = dx[i] + mu[i];
+            mu[i] = keep[t][i] * lam;
             float dl = mu[i] * before[t][i];
             dx[i] = lam;
             if constexpr (NORM) {
-                // u = m x: x / m = u / m^2, and both are 0 where m is
-                const float m2 = fmaf(-e, e, e + e), r = __builtin_amdgcn_rsqf(fmaxf(m2, 1e-36f));
-                dx[i] = lam * (m2 * r);
-                dl = fmaf(-(mu[i] * f), u[t][i] * r * r, dl);
+                // u = m x: x / m = u / m^2, and u is 0 where m is (an m that is not 0 is above 1e-23)
+                const float r = __builtin_amdgcn_rcpf(fmaxf(m[t][i], 1e-30f));
+                dx[i] = lam * m[t][i];
+                dl = fmaf(-(mu[i] * keep[t][i]), u[t][i] * r * r, dl);
             }
             const float sd = sg[t][i] * dl;
             dr[i] -= sd;

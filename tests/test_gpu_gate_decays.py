@@ -94,3 +94,56 @@ def test_a_prompt_keeps_what_a_strong_decay_leaves(rate, T, opens, dtype):
         h, last, _ = msr.msr_gated_recurrence(x, g, r, normalize=normalize, state_in=st)
         near(last, want[:, -1], room[:, -1], "f32", "state")
         near(h, want, room, dtype, "h")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rate", [5.0, 12.0, 20.0, 30.0])
+def test_gradients_keep_what_a_strong_decay_leaves(rate, dtype):
+    torch, dev = torch_dev()
+    msr = _msr()
+    rng = np.random.default_rng([53, int(rate)])
+    D = 1001
+    x, xf = tensor(torch, dev, rng.standard_normal((1, 1, D)) * (rng.random(D) < 0.5), dtype)
+    g, gf = tensor(torch, dev, rng.uniform(0, 4, (1, 1, D)), dtype)
+    dh, dhf = tensor(torch, dev, rng.standard_normal((1, 1, D)), dtype)
+    r, rf = tensor(torch, dev, np.full(D, rate))
+    st, sf = tensor(torch, dev, rng.standard_normal((1, D)))
+    ds, dsf = tensor(torch, dev, rng.standard_normal((1, D)))
+    for normalize in (True, False):
+        s, q, a, m, es = parts(gf, rf, normalize)
+        lam, ra = dhf + dsf[:, None], q * (es + 4 * U) + 6 * U
+        lroom = U * np.abs(lam)
+        old = a * lam * sf[:, None]
+        new = lam * xf * a * a / m if normalize else np.zeros_like(a)
+        dl = old - new
+        droom = (ra + 8 * U) * np.abs(old) + (2 * ra + es + 12 * U) * np.abs(new)
+        k = rate * s * (1 - s)
+        got = msr.msr_gated_recurrence_backward(x, g, r, dh, normalize=normalize, state_in=st, grad_state=ds)
+        near(got[0], m * lam, lroom + (es + 8 * U) * np.abs(m * lam), dtype, "dx")
+        # 1 - s as the difference: es of s
+        near(got[1], -k * dl, k * droom + (2 * es + 8 * U + (es + 2 * U) * s / (1 - s)) * k * np.abs(dl), dtype, "dg")
+        near(got[2], -(s * dl)[0, 0], (s * droom + (es + 8 * U) * s * np.abs(dl))[0, 0], "f32", "drate")
+        # formed as f dstate + (a dh), f and a each within ra of exp(-q): relative to the two terms, which may cancel
+        near(got[3], (a * lam)[:, 0], ((ra + 4 * U) * a * (np.abs(dhf) + np.abs(dsf[:, None])))[:, 0], "f32", "dstate")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["gate", "rate"])
+def test_gradients_where_the_input_hardly_counts(kind, dtype):
+    # m^2 = 2 q down to 4e-38: dx = m lam, and the input's share of dl, lam x / m
+    torch, dev = torch_dev()
+    msr = _msr()
+    rng = np.random.default_rng(55)
+    D = 203
+    gates = np.linspace(-60, -86, D) if kind == "gate" else np.zeros(D)
+    rates = np.ones(D) if kind == "gate" else 10 ** np.linspace(-30, -37, D)
+    g, gf = tensor(torch, dev, gates[None, None], dtype)
+    r, rf = tensor(torch, dev, rates)
+    x, xf = tensor(torch, dev, rng.standard_normal((1, 1, D)), dtype)
+    dh, dhf = tensor(torch, dev, rng.standard_normal((1, 1, D)), dtype)
+    s, q, a, m, es = parts(gf, rf, True)
+    dl = -dhf * xf * a * a / m
+    dx, dg, dr, _ = msr.msr_gated_recurrence_backward(x, g, r, dh)
+    near(dx, m * dhf, (es + 8 * U) * np.abs(m * dhf), dtype, "dx")
+    near(dg, -rf * s * (1 - s) * dl, (3 * es + 24 * U) * np.abs(rf * s * dl), dtype, "dg")
+    near(dr, -(s * dl)[0, 0], ((2 * es + 16 * U) * s * np.abs(dl))[0, 0], "f32", "drate")
