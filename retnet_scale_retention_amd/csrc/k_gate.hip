@@ -89,6 +89,40 @@ __device__ __forceinline__ float factor(float k) {
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * g)); }
 
+// The gradients need s (1 - s) too, and 1 - s formed of an s next to 1 has few digits (0.5% off at g = 12, none left from 17
+// on): with c the lesser of s and 1 - s, both formed of exp(-|g|), it is c (1 - c).  Where the registers allow (bf16 in rows
+// of aligned groups: 252 of them), s and s (1 - s) are kept from one pass over a tile to the other; elsewhere c is, with a
+// sign that says which it is (-0: s = 1), at five more operations.
+template <bool BOTH>
+struct Gated;
+template <>
+struct Gated<true> {
+    float s, p;
+    __device__ __forceinline__ float set(float g) {
+        const float t = __builtin_amdgcn_exp2f(-kLog2e * fabsf(g)), r = __builtin_amdgcn_rcpf(1.f + t), c = t * r;
+        p = r * c, s = g < 0.f ? c : r;
+        asm volatile("" : "+v"(s), "+v"(p));  // keeps the compiler from holding what they are formed of
+        return s;
+    }
+    __device__ __forceinline__ float sigmoid() const { return s; }
+    __device__ __forceinline__ float slope() const { return p; }
+    __device__ __forceinline__ void forget() {}
+};
+template <>
+struct Gated<false> {
+    float w;  // s, or s - 1
+    __device__ __forceinline__ float set(float g) {
+        const float t = __builtin_amdgcn_exp2f(-kLog2e * fabsf(g));
+        w = copysignf(t * __builtin_amdgcn_rcpf(1.f + t), -g);
+        forget();
+        return sigmoid();
+    }
+    __device__ __forceinline__ float sigmoid() const { return far(w) ? 1.f + w : w; }
+    __device__ __forceinline__ float slope() const { return fmaf(-w, w, fabsf(w)); }
+    // the same for w and what is formed of it
+    __device__ __forceinline__ void forget() { asm volatile("" : "+v"(w)); }
+};
+
 // Tokens past the last: a gate of -infinity, whose decay is 1 and whose input counts for nothing.
 template <int ROWS>
 __device__ __forceinline__ void close_gate(Raw8<uint16_t, ROWS> &r) {
@@ -326,7 +360,8 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     if (threadIdx.x >= CH && threadIdx.x < 2 * CH && c0 + (int)threadIdx.x - CH < a.D)
         start = a.carry[((int64_t)b * a.blocks + t0 / MSR_GATE_BLOCK) * a.D + c0 + threadIdx.x - CH];
     Raw8<T, ROWS> rd[S];
-    float rate[8], keep[S][8], m[S][8], sg[S][8], u[S][8];
+    float rate[8], keep[S][8], m[S][8], u[S][8];
+    Gated<sizeof(T) == 2 && ROWS != kAny> sg[S][8];
     {
         Raw8<T, ROWS> rx[S], rg[S];
         const T *px = static_cast<const T *>(a.x) + at, *pg = static_cast<const T *>(a.g) + at;
@@ -353,12 +388,12 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
         for (int i = 0; i < 8; ++i) k[i] = h[i] = mu[i] = 0.f;
 #pragma unroll
         for (int t = 0; t < S; ++t) {
+            float g[8];
             rx[t].get(u[t]);
-            rg[t].get(sg[t]);
+            rg[t].get(g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sg[t][i] = sigmoid(sg[t][i]);
-                const float kt = rate[i] * kLog2e * sg[t][i];
+                const float kt = rate[i] * kLog2e * sg[t][i].set(g[i]);
                 const Decay d(kt);
                 if constexpr (NORM) {
                     m[t][i] = __builtin_amdgcn_sqrtf(fmaf(-d.e, d.e, d.e + d.e));
@@ -423,8 +458,13 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
         }
     }
     __syncthreads();
+    // what was formed of these is formed again: kept across the barriers, it would not fit the registers
 #pragma unroll
-    for (int t = 0; t < S; ++t) rd[t].forget();  // its floats, kept across the barriers, would not fit the registers
+    for (int t = 0; t < S; ++t) {
+        rd[t].forget();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sg[t][i].forget();
+    }
     float before[S][8], mu[8], dr[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) before[0][i] = hs[sl][e0 + i], mu[i] = ms[sl][e0 + i], dr[i] = 0.f;
@@ -442,17 +482,17 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
         for (int i = 0; i < 8; ++i) {
             const float lam = dx[i] + mu[i];
             mu[i] = keep[t][i] * lam;
-            float dl = mu[i] * before[t][i];
             dx[i] = lam;
+            float by = before[t][i];
             if constexpr (NORM) {
                 // u = m x: x / m = u / m^2, and u is 0 where m is (an m that is not 0 is above 1e-23)
                 const float r = __builtin_amdgcn_rcpf(fmaxf(m[t][i], 1e-30f));
                 dx[i] = lam * m[t][i];
-                dl = fmaf(-(mu[i] * keep[t][i]), u[t][i] * r * r, dl);
+                by = fmaf(-keep[t][i], u[t][i] * r * r, by);
             }
-            const float sd = sg[t][i] * dl;
-            dr[i] -= sd;
-            dg[i] = (sg[t][i] - 1.f) * (rate[i] * sd);
+            const float dl = mu[i] * by;
+            dr[i] = fmaf(-sg[t][i].sigmoid(), dl, dr[i]);
+            dg[i] = -sg[t][i].slope() * (rate[i] * dl);
         }
         if (whole) {
             store8<ROWS>(dxp, 8, dx);

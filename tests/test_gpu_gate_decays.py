@@ -128,6 +128,29 @@ def test_gradients_keep_what_a_strong_decay_leaves(rate, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_gradient_of_a_gate_that_is_wide_open(dtype):
+    # 1 - s = exp(-g) / (1 + exp(-g)), off by es of itself, not of 1
+    torch, dev = torch_dev()
+    msr = _msr()
+    rng = np.random.default_rng(54)
+    D = 801
+    g, gf = tensor(torch, dev, np.linspace(-10, 80, D)[None, None], dtype)
+    x, xf = tensor(torch, dev, rng.standard_normal((1, 1, D)) * (rng.random(D) < 0.5), dtype)
+    dh, dhf = tensor(torch, dev, rng.standard_normal((1, 1, D)), dtype)
+    r, rf = tensor(torch, dev, np.full(D, 0.5))
+    st, sf = tensor(torch, dev, rng.standard_normal((1, D)))
+    for normalize in (True, False):
+        s, q, a, m, es = parts(gf, rf, normalize)
+        c = np.exp(-gf) / (1 + np.exp(-gf))
+        old = a * dhf * sf[:, None]
+        new = dhf * xf * a * a / m if normalize else np.zeros_like(a)
+        k = 0.5 * s * c
+        room = k * ((3 * es + 24 * U) * np.abs(old) + (5 * es + 32 * U) * np.abs(new))
+        dg = msr.msr_gated_recurrence_backward(x, g, r, dh, normalize=normalize, state_in=st)[1]
+        near(dg, -k * (old - new), room, dtype, "dg")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["gate", "rate"])
 def test_gradients_where_the_input_hardly_counts(kind, dtype):
     # m^2 = 2 q down to 4e-38: dx = m lam, and the input's share of dl, lam x / m
