@@ -476,7 +476,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     T *dxp = static_cast<T *>(a.y) + at + row, *dgp = static_cast<T *>(a.dg) + at + row;
 #pragma unroll
     for (int t = S - 1; t >= 0; --t, dxp -= a.D, dgp -= a.D) {
-        float dx[8], dg[8];
+        float dx[8], dg[8], dl[8];
         rd[t].get(dx);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -490,9 +490,12 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
                 dx[i] = lam * m[t][i];
                 by = fmaf(-keep[t][i], u[t][i] * r * r, by);
             }
-            const float dl = mu[i] * by;
-            dr[i] = fmaf(-sg[t][i].sigmoid(), dl, dr[i]);
-            dg[i] = -sg[t][i].slope() * (rate[i] * dl);
+            dl[i] = mu[i] * by;
+            dg[i] = -sg[t][i].slope() * (rate[i] * dl[i]);
+        }
+        if (whole || t < mine) {  // past the last token s is 0, but dl is not where the last state is not finite
+#pragma unroll
+            for (int i = 0; i < 8; ++i) dr[i] = fmaf(-sg[t][i].sigmoid(), dl[i], dr[i]);
         }
         if (whole) {
             store8<ROWS>(dxp, 8, dx);

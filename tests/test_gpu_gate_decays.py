@@ -170,3 +170,24 @@ def test_gradients_where_the_input_hardly_counts(kind, dtype):
     near(dx, m * dhf, (es + 8 * U) * np.abs(m * dhf), dtype, "dx")
     near(dg, -rf * s * (1 - s) * dl, (3 * es + 24 * U) * np.abs(rf * s * dl), dtype, "dg")
     near(dr, -(s * dl)[0, 0], ((2 * es + 16 * U) * s * np.abs(dl))[0, 0], "f32", "drate")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 5, 64, 70, 129, 192])
+def test_the_last_input_without_normalize_is_in_no_gradient(T, dtype):
+    # h_T alone holds x_T, and no gradient holds h_T: tokens behind the sequence's end count for nothing
+    torch, dev = torch_dev()
+    msr = _msr()
+    gen = torch.Generator(device=dev).manual_seed(T)
+    kind = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    x, g, dh = (torch.randn(2, T, 40, generator=gen, device=dev).to(kind) for _ in range(3))
+    r, st = torch.rand(40, generator=gen, device=dev), torch.randn(2, 40, generator=gen, device=dev)
+    x[:, -1] = 0
+    want = msr.msr_gated_recurrence_backward(x, g, r, dh, normalize=False, state_in=st, grad_state=st)
+    assert all(bool(torch.isfinite(t).all()) for t in want)
+    for bad in (float("nan"), float("inf")):
+        y = x.clone()
+        y[0, -1, 3] = bad
+        got = msr.msr_gated_recurrence_backward(y, g, r, dh, normalize=False, state_in=st, grad_state=st)
+        for name, a, b in zip(("dx", "dg", "drate", "dstate"), got, want):
+            assert torch.equal(a, b), (name, bad)
