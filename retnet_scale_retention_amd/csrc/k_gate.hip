@@ -63,7 +63,10 @@ struct GateArgs {
 // sign bit tells them apart), so that neither a state that hardly decays nor
 // one that is nearly gone loses accuracy.  -0 is f = 0.
 __device__ __forceinline__ bool far(float z) { return (int)__float_as_uint(z) < 0; }
-__device__ __forceinline__ float apply(float z, float p) { return fmaf(-z, p, far(z) ? 0.f : p); }
+__device__ __forceinline__ float apply(float z, float p) {
+    if (!far(z) && __builtin_isinf(p)) return p;  // not p - z p
+    return fmaf(-z, p, far(z) ? 0.f : p);
+}
 
 // Exponents are kept in base 2: k = q log2(e), with log2(e) in the channel's rate.
 constexpr float kLog2e = 1.44269504f;

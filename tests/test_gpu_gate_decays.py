@@ -191,3 +191,31 @@ def test_the_last_input_without_normalize_is_in_no_gradient(T, dtype):
         got = msr.msr_gated_recurrence_backward(y, g, r, dh, normalize=False, state_in=st, grad_state=st)
         for name, a, b in zip(("dx", "dg", "drate", "dstate"), got, want):
             assert torch.equal(a, b), (name, bad)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_an_infinity_stays_one(dtype):
+    # a inf + m x = inf while a is not 0: 700 tokens at 0.1 leave e^-70 at least
+    torch, dev = torch_dev()
+    msr = _msr()
+    kind = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    T, D, inf = 700, 40, float("inf")
+    gen = torch.Generator(device=dev).manual_seed(56)
+    x, g, dh = (torch.randn(2, T, D, generator=gen, device=dev).to(kind) for _ in range(3))
+    r, st = torch.full((D,), 0.1, device=dev), torch.randn(2, D, generator=gen, device=dev)
+    x[0, 10, ::2], st[1, 1::2] = inf, -inf
+    for normalize in (True, False):
+        h, last, carry = msr.msr_gated_recurrence(x, g, r, normalize=normalize, state_in=st, want_carry=True)
+        assert bool((h[0, 10:, ::2] == inf).all()) and bool((last[0, ::2] == inf).all()) and bool((carry[0, 1:, ::2] == inf).all())
+        assert bool((h[1, :, 1::2] == -inf).all()) and bool((last[1, 1::2] == -inf).all())
+        for t in (h[0, :10], h[0, :, 1::2], h[1, :, ::2], last[0, 1::2], last[1, ::2]):
+            assert bool(torch.isfinite(t).all())
+        s = st.clone()
+        for t in range(9, 14):
+            msr.msr_gated_recurrence_step(x[:, t].contiguous(), g[:, t].contiguous(), s, r, normalize=normalize)
+        assert bool((s[0, ::2] == inf).all()) and bool((s[1, 1::2] == -inf).all()) and bool(torch.isfinite(s[0, 1::2]).all())
+        x2, s2, d2 = torch.zeros_like(x), torch.zeros_like(st), dh.clone()
+        d2[0, 600, ::2] = inf
+        dx, _, _, ds = msr.msr_gated_recurrence_backward(x2, g, r, d2, normalize=normalize, state_in=s2)
+        assert bool((dx[0, :601, ::2] == inf).all()) and bool((ds[0, ::2] == inf).all())
+        assert bool(torch.isfinite(dx[0, 601:]).all()) and bool(torch.isfinite(dx[1]).all()) and bool(torch.isfinite(ds[1]).all())
