@@ -39,12 +39,11 @@
 
 #include "msr_quant.hpp"
 
+#include "msr_lookback.hpp"
+
 namespace {
 
 using namespace msr;
-
-// factor bits, of NaNs that no factor has, of a word that is not published yet and of one that holds a state
-constexpr uint32_t kUnset = 0xffffffffu, kState = 0xfffffffeu;
 
 struct GateArgs {
     const void *x, *g, *dh;         // dh: backward only
@@ -58,16 +57,7 @@ struct GateArgs {
     int B, T, D, tiles, cols, blocks, groups;
 };
 
-// ---- factors ----------------------------------------------------------------
-// A factor f in [0, 1] is held as 1 - f where f >= 1/2 and as -f below (the
-// sign bit tells them apart), so that neither a state that hardly decays nor
-// one that is nearly gone loses accuracy.  -0 is f = 0.
-__device__ __forceinline__ bool far(float z) { return (int)__float_as_uint(z) < 0; }
-__device__ __forceinline__ float apply(float z, float p) {
-    if (!far(z) && __builtin_isinf(p)) return p;  // not p - z p
-    return fmaf(-z, p, far(z) ? 0.f : p);
-}
-
+// ---- decays and gates -----------------------------------------------------------
 // Exponents are kept in base 2: k = q log2(e), with log2(e) in the channel's rate.
 constexpr float kLog2e = 1.44269504f;
 
@@ -140,53 +130,26 @@ __device__ __forceinline__ void close_gate(Raw8<float, ROWS> &r) {
     if constexpr (ROWS == kAny) r.down = 0;
 }
 
-// ---- words between tiles ------------------------------------------------------
-// Every tile has a word: its pair (f, h), which maps the state p before the tile to f p + h; then (kState) the state after
-// it.  A pair whose f is 0 is no state yet: 0 p is NaN where p is not finite.
-__device__ __forceinline__ void store(uint64_t *w, uint32_t u, float h) {
-    __hip_atomic_store(w, (uint64_t)u << 32 | __float_as_uint(h), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+// ---- words between tiles (msr_lookback.hpp) ---------------------------------------
+__device__ __forceinline__ void store(uint64_t *w, uint64_t v) {
+    __hip_atomic_store(w, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ void publish(uint64_t *w, float z, float h) {
-    store(w, z != z ? 0x7fc00000u : __float_as_uint(z), h);  // one NaN for all
-}
-__device__ __forceinline__ void publish(uint64_t *w, float state) { store(w, kState, state); }
-__device__ __forceinline__ uint64_t word(const uint64_t *w) {
-    return __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint32_t kind(uint64_t v) { return (uint32_t)(v >> 32); }
-__device__ __forceinline__ float value(uint64_t v) { return __uint_as_float((uint32_t)v); }
-__device__ __forceinline__ float after(uint64_t v, float p) {  // the state after its stretch
-    return kind(v) == kState ? value(v) : apply(__uint_as_float(kind(v)), p) + value(v);
-}
+__device__ __forceinline__ void publish(uint64_t *w, float z, float h) { store(w, pair_word(z, h)); }
+__device__ __forceinline__ void publish(uint64_t *w, float state) { store(w, pack(kState, state)); }
 
 constexpr int kSpins = 1 << 22;  // polls: seconds, far beyond any wait; an end for callers who share a workspace
 constexpr int kLook = 8;         // tiles looked at: 96 and 235 us (sizes above); with four 95 and 251, with 16 100 and 242
 constexpr int kSleep = 8;        // between polls, in 64 clocks: with two 97 and 236 us
 
-// The state that tile n of a chain starts from: that of the latest of the kLook tiles before it whose state is known, and
-// the pairs since (w: tile 0's word; a tile's words are CH apart).  Which one that is depends on how far the other
-// workgroups are; the result does not, since every tile's end state is formed from its start state by the same pair.
+// the state that tile n of a chain starts from (w: tile 0's word; a tile's words are CH apart)
 template <int CH>
-__device__ __forceinline__ float look_back(const uint64_t *w, int n) {
-    uint64_t v[kLook];
-    int from = -1;  // the latest state with no word missing after it
-    for (int spin = 0; spin < kSpins; ++spin) {
-#pragma unroll
-        for (int i = 0; i < kLook; ++i) v[i] = word(w + (int64_t)max(n - 1 - i, 0) * CH);
-        bool open = false;
-#pragma unroll
-        for (int i = 0; i < kLook; ++i) {
-            if (from < 0 && !open && kind(v[i]) == kState) from = i;
-            open = open || kind(v[i]) == kUnset;
-        }
-        if (from >= 0) break;
-        __builtin_amdgcn_s_sleep(kSleep);
-    }
-    float p = 0.f;
-#pragma unroll
-    for (int i = kLook - 1; i >= 0; --i)
-        if (i <= from) p = after(v[i], p);
-    return p;
+__device__ __forceinline__ float state_before(const uint64_t *w, int n) {
+    return look_back<kLook>(
+        kSpins,
+        [&](int i) {
+            return __hip_atomic_load(w + (int64_t)max(n - 1 - i, 0) * CH, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        },
+        [] { __builtin_amdgcn_s_sleep(kSleep); });
 }
 
 // The tiles are dealt out in order of time by `groups` counters: ticket q of a group's n chains is tile q / n of its chain
@@ -262,7 +225,7 @@ __device__ __forceinline__ void join_slices(const GateArgs &a, const Place &pl, 
         if (a.state_in && live) p = a.state_in[at];
     } else {
         if (pl.tile + 1 < a.tiles) publish(w + (int64_t)pl.tile * CH, z, h);
-        p = look_back<CH>(w, pl.tile);
+        p = state_before<CH>(w, pl.tile);
     }
     const float last = apply(z, p) + h;
     if (pl.tile + 1 < a.tiles)
@@ -437,7 +400,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
             if (a.state_in && live) p = a.state_in[(int64_t)b * a.D + c0 + c];
         } else {
             if (tile > 0) publish(w + (int64_t)n * CH, z, m);
-            p = look_back<CH>(w, n);
+            p = state_before<CH>(w, n);
         }
         const float last = apply(z, p) + m;
         if (tile > 0)
