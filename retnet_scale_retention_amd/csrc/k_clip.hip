@@ -123,8 +123,11 @@ __device__ __forceinline__ double squares(const T *p, int64_t left, bool tiny) {
 
 template <typename T>
 __device__ __forceinline__ void scale(const T *p, T *o, int64_t left, bool tiny, double f) {
-    // fp32: one rounding of the product with the fp64 factor; bf16: the fp32 product's rounding is far below its own
-    auto one = [&](float v) { return sizeof(T) == 4 ? (float)((double)v * f) : v * (float)f; };
+    // fp32: one rounding of the product with the fp64 factor; bf16: the fp32 product's rounding is far below its own.  The
+    // factor's exponent goes on afterwards, since large gradients and a small limit make factors that fp32 does not hold.
+    int e;
+    const float m = (float)frexp(f, &e);
+    auto one = [&](float v) { return sizeof(T) == 4 ? (float)((double)v * f) : ldexpf(v * m, e); };
     for_groups(p, left, tiny, [&](int at, float (&v)[8], int n) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = one(v[i]);
