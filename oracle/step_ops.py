@@ -134,5 +134,7 @@ def gate_backward(x, g, rate, state, dh, dstate, normalize=True):
 def clip(grads, max_norm):
     """([g f], norm) of float64 arrays; a norm beyond fp32 leaves them as they are."""
     norm = np.sqrt(sum(float((np.asarray(g, np.float64) ** 2).sum()) for g in grads))
-    f = max_norm / norm if max_norm < norm <= np.finfo(np.float32).max else 1.0
+    with np.errstate(over="ignore"):  # infinite as fp32
+        finite = np.isfinite(np.float32(norm))
+    f = max_norm / norm if max_norm < norm and finite else 1.0
     return [np.asarray(g, np.float64) * f for g in grads], norm

@@ -164,7 +164,7 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(ClipArgs a) {
     __shared__ double red[4];
     const double norm = a.norm ? (double)*a.norm : sqrt(total(a.sums, a.n_sums, red));
     if (a.norm_out && blockIdx.x == 0 && threadIdx.x == 0) *a.norm_out = (float)norm;
-    const bool clip = norm > (double)a.max_norm && norm <= 3.40282347e38;  // neither infinity, as fp32, nor NaN
+    const bool clip = norm > (double)a.max_norm && isfinite((float)norm);  // as the caller sees it
     const double f = clip ? (double)a.max_norm / norm : 1.0;
     const Find find(a);
     for (int c = a.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
