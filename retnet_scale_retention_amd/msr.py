@@ -951,7 +951,7 @@ def msr_gradient_norm(grads, *, out=None, workspace=None, stream=None):
 def msr_clip_gradients(grads, max_norm, *, norm=None, out=None, norm_out=None, workspace=None, stream=None):
     """g * min(1, max_norm / norm) for every tensor g of `grads` (contiguous, float32 and bfloat16), in place or to the
     tensors `out`.  norm: a float32 scalar on the device, e.g. one joined over processes; None: that of msr_gradient_norm,
-    formed here.  Where it is infinite or NaN the gradients stay as they are.  Returns (out or grads, norm)."""
+    formed here (norm_out: the scalar to write it to).  Where it is infinite or NaN the gradients stay as they are.  Returns (out or grads, norm)."""
     tc = _tc or _setup()
     grads = list(grads)
     if out is not None:
@@ -961,6 +961,8 @@ def msr_clip_gradients(grads, max_norm, *, norm=None, out=None, norm_out=None, w
     np_ = op = ws = None
     n = 0
     if norm is not None:
+        if norm_out is not None:
+            raise ValueError("norm_out is for the norm that the call forms; norm was given")
         np_ = _expect("norm", norm, (), tc.f32, dev)
     else:
         norm = _empty((), tc.f32, like.device, stream) if norm_out is None else norm_out

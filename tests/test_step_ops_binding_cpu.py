@@ -127,3 +127,12 @@ def test_tensors_that_do_not_fit_are_refused(world):
         with pytest.raises((ValueError, TypeError)):
             call()
         assert not world.lib.calls, i
+
+
+def test_a_norm_is_given_or_written(world):
+    g, scalar = on_device(4, dtype=F32), lambda: on_device(dtype=F32)
+    with pytest.raises(ValueError, match="norm_out"):
+        m.msr_clip_gradients([g], 1.0, norm=scalar(), norm_out=scalar())
+    assert not world.lib.calls
+    for kw in (dict(norm=scalar()), dict(norm_out=scalar())):
+        assert m.msr_clip_gradients([g], 1.0, **kw)[1] is list(kw.values())[0]
