@@ -55,11 +55,11 @@ def qk_norm_backward(x, w, dy, pos, theta, eps, s, rotate=True):
 def _parts(g, rate, normalize):
     s = 1.0 / (1.0 + np.exp(-np.asarray(g, np.float64)))
     q = np.asarray(rate, np.float64) * s
-    a, e = np.exp(-q), -np.expm1(-q)
+    a = np.exp(-q)
     m = np.sqrt(-np.expm1(-2 * q)) if normalize else np.ones_like(a)
-    # an fp32 sigmoid is off by its argument's rounding, g u, and a few u; 1 - exp(-q) follows it
+    # an fp32 sigmoid and 1 - s are off by their argument's rounding, g u, and a few u of themselves; q follows it
     es = (8 + 2 * np.abs(np.asarray(g, np.float64))) * U
-    return s, a, e, m, es
+    return s, q, a, m, es
 
 
 def _run(a, u, start):
@@ -71,34 +71,34 @@ def _run(a, u, start):
     return out
 
 
-def _bound(e, es, a, m, x, start):
-    """Magnitudes of the recurrence, and what its fp32 form is off by at most: each step adds e h with the relative
-    error of e, m x with that of m, and a few roundings of h."""
+def _bound(q, es, a, m, x, start):
+    """Magnitudes of the recurrence, and what its fp32 form is off by at most: each step's decay is off by q times the
+    relative error of q, relative to itself, m x by the error of m, and h by a few roundings."""
     size = _run(a, m * np.abs(x), np.abs(start))
     before = np.concatenate([np.abs(start)[:, None], size[:, :-1]], 1)
-    step = (es + 16 * U) * e * before + (es + 8 * U) * m * np.abs(x) + 8 * U * size
+    step = (es + 16 * U) * q * a * before + (es + 8 * U) * m * np.abs(x) + 8 * U * size
     return size, _run(a, step, np.zeros_like(start))
 
 
 def gate(x, g, rate, state, normalize=True):
     """(h, bound of its fp32 error), [B, T, D]; state [B, D] or None."""
     x = np.asarray(x, np.float64)
-    s, a, e, m, es = _parts(g, rate, normalize)
+    s, q, a, m, es = _parts(g, rate, normalize)
     start = np.zeros((x.shape[0], x.shape[2])) if state is None else np.asarray(state, np.float64)
-    return _run(a, m * x, start), _bound(e, es, a, m, x, start)[1]
+    return _run(a, m * x, start), _bound(q, es, a, m, x, start)[1]
 
 
 def gate_backward(x, g, rate, state, dh, dstate, normalize=True):
     """((dx, dg, drate, dstate_in), the bounds of their fp32 errors)."""
     x, dh, rate = np.asarray(x, np.float64), np.asarray(dh, np.float64), np.asarray(rate, np.float64)
-    s, a, e, m, es = _parts(g, rate, normalize)
+    s, q, a, m, es = _parts(g, rate, normalize)
     B, T, D = x.shape
     zero = np.zeros((B, D))
     start = zero if state is None else np.asarray(state, np.float64)
     last = zero if dstate is None else np.asarray(dstate, np.float64)
     before = lambda h, h0: np.concatenate([h0[:, None], h[:, :-1]], 1)
     h = _run(a, m * x, start)
-    hm, hb = _bound(e, es, a, m, x, start)
+    hm, hb = _bound(q, es, a, m, x, start)
     hp, hpm, hpb = before(h, start), before(hm, np.abs(start)), before(hb, zero)
     # mu_t = a_t (dh_t + mu_{t+1}), from the last token to the first
     rev = lambda z: z[:, ::-1]
@@ -106,7 +106,8 @@ def gate_backward(x, g, rate, state, dh, dstate, normalize=True):
     mum = rev(_run(rev(a), rev(a * np.abs(dh)), np.abs(last)))
     after = lambda z, z0: np.concatenate([z[:, 1:], z0[:, None]], 1)
     lam, lamm = dh + after(mu, last), np.abs(dh) + after(mum, np.abs(last))
-    mub = rev(_run(rev(a), rev(((es + 16 * U) * e + 8 * U) * lamm), zero))
+    ea = (es + 16 * U) * q + 8 * U  # of a, relative to it
+    mub = rev(_run(rev(a), rev(ea * a * lamm), zero))
     lamb = after(mub, zero) + U * lamm
     dx = m * lam
     dxb = m * lamb + (es + 8 * U) * m * lamm
@@ -114,14 +115,13 @@ def gate_backward(x, g, rate, state, dh, dstate, normalize=True):
     dlb = mub * hpm + mum * hpb + 4 * U * dlm
     if normalize:
         ratio = np.divide(a, m, out=np.zeros_like(a), where=m > 0)
-        ea = (es + 8 * U) * e + U  # of a = 1 - e, absolute
         dl = dl - mu * x * ratio
         t = mum * np.abs(x) * ratio
         dlm = dlm + t
-        dlb = dlb + mub * np.abs(x) * ratio + (es + 12 * U) * t + mum * np.abs(x) * np.divide(ea, m, out=np.zeros_like(a), where=m > 0)
-    k = rate * s * (1 - s)
+        dlb = dlb + mub * np.abs(x) * ratio + (ea + es + 12 * U) * t
+    k = rate * s / (1 + np.exp(np.asarray(g, np.float64)))  # 1 - s without its cancellation
     dg = -k * dl
-    dgb = k * dlb + (es + 8 * U) * k * dlm + rate * s * s * (es + 2 * U) * dlm
+    dgb = k * dlb + (2 * es + 16 * U) * k * dlm
     drate = -(s * dl).sum((0, 1))
     chain = 64 + B * T / 2048  # additions in a row: a slice, its tile's slices, a 64th of the tiles, six more
     drb = (s * dlb).sum((0, 1)) + ((es + (chain + 8) * U) * s * dlm).sum((0, 1))

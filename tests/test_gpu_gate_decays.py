@@ -10,7 +10,8 @@ square).  What a result is stored in adds 2^-8 (bf16) or u (fp32)."""
 import numpy as np
 import pytest
 
-from tests.gpu_util import down, torch_dev
+from oracle import step_ops as so
+from tests.gpu_util import down, note, torch_dev
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -219,3 +220,46 @@ def test_an_infinity_stays_one(dtype):
         dx, _, _, ds = msr.msr_gated_recurrence_backward(x2, g, r, d2, normalize=normalize, state_in=s2)
         assert bool((dx[0, :601, ::2] == inf).all()) and bool((ds[0, ::2] == inf).all())
         assert bool(torch.isfinite(dx[0, 601:]).all()) and bool(torch.isfinite(dx[1]).all()) and bool(torch.isfinite(ds[1]).all())
+
+
+def test_long_memory_around_where_a_decay_takes_its_series():
+    # the same gate at every token: a relative error of 1 - a moves the state 1 / (1 - a) by as much
+    torch, dev = torch_dev()
+    msr = _msr()
+    T, D = 3000, 128
+    x, g = torch.ones(1, T, D, device=dev), torch.zeros(1, T, D, device=dev)
+    r, rf = tensor(torch, dev, 2 * np.log(2) * np.linspace(0.02, 0.2, D))
+    q = 0.5 * rf
+    h, last, _ = msr.msr_gated_recurrence(x, g, r, normalize=False)
+    want = -np.expm1(-q * T) / -np.expm1(-q)
+    err = np.abs(down(last)[0] / want - 1).max()
+    note(f"largest {err:.1e}")
+    # 1 - a: 2.8e-6 of itself at most; q: 4 u; roundings of h, u of it at each of the 1 / (1 - a) = 72 tokens that it holds
+    assert err < 2.8e-6 + 4 * U + 72 * U
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,T,D", [(2, 1, 40), (1, 70, 24), (2, 300, 33), (1, 2000, 8)])
+def test_strong_decays_over_tiles(B, T, D, dtype):
+    # against the oracle's bounds, whose decays are off relative to themselves; twice them as in test_gpu_gate.py
+    torch, dev = torch_dev()
+    msr = _msr()
+    rng = np.random.default_rng([57, B, T, D])
+    some = lambda: rng.standard_normal((B, T, D)) * (rng.random((B, T, D)) < 0.7)
+    (x, xf), (dh, dhf) = tensor(torch, dev, some(), dtype), tensor(torch, dev, some(), dtype)
+    g, gf = tensor(torch, dev, 2 + 2 * rng.standard_normal((B, T, D)), dtype)
+    r, rf = tensor(torch, dev, np.exp(rng.uniform(np.log(2), np.log(40), D)))
+    (st, sf), (ds, dsf) = (tensor(torch, dev, rng.standard_normal((B, D))) for _ in range(2))
+    for normalize in (True, False):
+        want, bound = so.gate(xf, gf, rf, sf, normalize)
+        h, last, carry = msr.msr_gated_recurrence(x, g, r, normalize=normalize, state_in=st, want_carry=True)
+        near(h, want, 2 * bound, dtype, "h")
+        near(last, want[:, -1], 2 * bound[:, -1], "f32", "state")
+        s = st.clone()
+        for t in range(min(T, 20)):
+            one = msr.msr_gated_recurrence_step(x[:, t].contiguous(), g[:, t].contiguous(), s, r, normalize=normalize)
+            near(one, want[:, t], 2 * bound[:, t], dtype, "step")
+        got = msr.msr_gated_recurrence_backward(x, g, r, dh, normalize=normalize, state_in=st, carry=carry, grad_state=ds)
+        want, bound = so.gate_backward(xf, gf, rf, sf, dhf, dsf, normalize)
+        for name, a, b, c in zip(("dx", "dg", "drate", "dstate"), got, want, bound):
+            near(a, b, 2 * c, dtype if name in ("dx", "dg") else "f32", name)

@@ -104,6 +104,55 @@ def test_the_gate_bounds_hold_for_an_fp32_recurrence():
     assert np.all(run(-1) <= bound) and not np.all(run(100) <= 10 * bound)
 
 
+@pytest.mark.parametrize("lost", [False, True])
+def test_the_gate_bounds_hold_for_strong_decays_and_for_nothing_less(lost):
+    # fp32, token by token, rates up to 40, a third of the inputs 0: a decay as its exponential stays within the bounds, one
+    # as 1 - (1 - a), of which few digits are left, does not
+    rng = np.random.default_rng(4)
+    f = np.float32
+    B, T, D = 3, 60, 50
+    x, dh = ((rng.standard_normal((B, T, D)) * (rng.random((B, T, D)) < 0.7)).astype(f) for _ in range(2))
+    g = (2 + 2 * rng.standard_normal((B, T, D))).astype(f)
+    r = np.exp(rng.uniform(np.log(2), np.log(40), D)).astype(f)
+    st, ds = (rng.standard_normal((B, D)).astype(f) for _ in range(2))
+    t = np.exp(-np.abs(g))
+    c = t / (f(1) + t)
+    s, slope = np.where(g < 0, c, f(1) / (f(1) + t)), c * (f(1) - c)
+    q = r * s
+    e = -np.expm1(-q)
+    a, m = f(1) - e if lost else np.exp(-q), np.sqrt(e * (f(2) - e))
+    h, before = st, []
+    for i in range(T):
+        before.append(h)
+        h = a[:, i] * h + m[:, i] * x[:, i]
+    want, bound = so.gate(x, g, r, st)
+    inside = [np.abs(np.stack(before[1:] + [h], 1) - want) <= bound + 1e-37]  # below 2^-126 fp32 has no more digits
+    mu, dx, dg, dr = ds, np.empty_like(x), np.empty_like(x), np.zeros(D, f)
+    for i in reversed(range(T)):
+        lam = dh[:, i] + mu
+        mu = a[:, i] * lam
+        dl = mu * (before[i] - a[:, i] * x[:, i] / m[:, i])
+        dx[:, i], dg[:, i] = m[:, i] * lam, -(r * slope[:, i]) * dl
+        dr -= (s[:, i] * dl).sum(0, dtype=f)
+    want, bounds = so.gate_backward(x, g, r, st, dh, ds)
+    inside += [np.abs(z - w) <= b + 1e-37 for z, w, b in zip((dx, dg, dr, mu), want, bounds)]
+    if not lost:
+        assert all(i.all() for i in inside), [int((~i).sum()) for i in inside]
+    else:
+        assert not any(inside[i].all() for i in (0, 2, 3, 4)), [int((~i).sum()) for i in inside]
+
+
+def test_the_gate_bounds_reject_results_of_zero():
+    # one token without input, of q = 10, 20, 30 and 60: what is left of the state, and the gradients, are within 1% at most
+    g, one = np.full((1, 1, 4), 0.5), np.ones((1, 1, 4))
+    r = np.array([10.0, 20.0, 30.0, 60.0]) * (1 + np.exp(-0.5))
+    h, bound = so.gate(0 * one, g, r, one[0])
+    assert np.all(bound < 0.01 * h)
+    got, bounds = so.gate_backward(0 * one, g, r, one[0], one, one[0])
+    for i in (1, 2, 3):
+        assert np.all(bounds[i] < 0.01 * np.abs(got[i])), i
+
+
 def test_clip_definition():
     g = [np.array([3.0, 0.0]), np.array([[4.0]])]
     out, n = so.clip(g, 1.0)
