@@ -61,15 +61,25 @@ struct GateArgs {
 // Exponents are kept in base 2: k = q log2(e), with log2(e) in the channel's rate.
 constexpr float kLog2e = 1.44269504f;
 
-// a = 2^-k and e = 1 - a.  Where k is small, e is a series (the first term left out is 4e-7 of the sum at 1/32) and a is 1 -
-// e; elsewhere e is 1 - a, off by the exponential's error: 1.5e-6 of itself just above 1/32 as measured (by an ulp of a, that
-// is 2.8e-6, at most), and less above.
+// a = 2^-k and e = 1 - a.  Where k is small, e is a series and a is 1 - e; elsewhere e is 1 - a, off by the exponential's
+// error.  FINE: seven terms up to 1/2 (the first left out is 1.5e-8 of the sum); 1 - a is off by 2e-7 of itself there.  Else
+// three up to 1/32 (4e-7), and 1 - a is off by 1.5e-6 just above as measured (2.8e-6 by an ulp of a).  fp32 results, whose
+// kernels wait for memory, take the former at no cost (2 x 8192 x 2048 104 us with either; errors of the results 1.0e-7 to
+// 1.5e-7 of their norm with the latter, 0.6e-7 to 1.1e-7 with the former); bf16 ones, whose rounding is 4e-3, the latter.
+template <bool FINE>
 struct Decay {
     float e, a;
     __device__ __forceinline__ explicit Decay(float k) {
-        const float p = k * fmaf(k, fmaf(k, 0.0555041087f, -0.240226507f), 0.693147181f);
+        float p = 0.0555041087f;
+        if constexpr (FINE) {
+            p = fmaf(k, 1.52527338e-5f, -1.54035304e-4f);
+            p = fmaf(k, p, 1.33335581e-3f);
+            p = fmaf(k, p, -9.61812911e-3f);
+            p = fmaf(k, p, 0.0555041087f);
+        }
+        p = k * fmaf(k, fmaf(k, p, -0.240226507f), 0.693147181f);
         const float f = __builtin_amdgcn_exp2f(-k);
-        const bool small = k < 0.03125f;
+        const bool small = k < (FINE ? 0.5f : 0.03125f);
         e = small ? p : 1.f - f;
         a = small ? 1.f - p : f;
     }
@@ -77,7 +87,7 @@ struct Decay {
 
 __device__ __forceinline__ float factor(float k) {
     const float f = __builtin_amdgcn_exp2f(-k);
-    return f < 0.5f ? -f : Decay(k).e;
+    return f < 0.5f ? -f : Decay<true>(k).e;
 }
 
 __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * g)); }
@@ -185,7 +195,7 @@ struct Place {
 // ---- the forward pass -----------------------------------------------------------
 // a slice's tokens: a and m x of each, their sum of k, and the state that they make of 0.  raw(t, x, g) gives a
 // token's eight channels
-template <int S, bool NORM, typename Raw>
+template <bool FINE, int S, bool NORM, typename Raw>
 __device__ __forceinline__ void slice(const Raw &raw, const float (&rate)[8], float (&keep)[S][8], float (&u)[S][8],
                                       float (&k)[8], float (&h)[8]) {
 #pragma unroll
@@ -197,7 +207,7 @@ __device__ __forceinline__ void slice(const Raw &raw, const float (&rate)[8], fl
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float kt = rate[i] * sigmoid(g[i]);
-            const Decay d(kt);
+            const Decay<FINE> d(kt);
             if constexpr (NORM) u[t][i] *= __builtin_amdgcn_sqrtf(fmaf(-d.e, d.e, d.e + d.e));
             keep[t][i] = d.a;
             k[i] += kt;
@@ -281,7 +291,7 @@ __global__ __launch_bounds__(64 * W) void gate_kernel(GateArgs a) {
             for (int t = 0; t < S; ++t)
                 if (t >= mine) close_gate(rg[t]);
         }
-        slice<S, NORM>([&](int t, float (&x)[8], float (&g)[8]) { rx[t].get(x), rg[t].get(g); }, rate, keep, u, k, h);
+        slice<sizeof(T) == 4, S, NORM>([&](int t, float (&x)[8], float (&g)[8]) { rx[t].get(x), rg[t].get(g); }, rate, keep, u, k, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ks[sl][e0 + i] = k[i], hs[sl][e0 + i] = h[i];
     }
@@ -360,7 +370,7 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float kt = rate[i] * kLog2e * sg[t][i].set(g[i]);
-                const Decay d(kt);
+                const Decay<sizeof(T) == 4> d(kt);
                 if constexpr (NORM) {
                     m[t][i] = __builtin_amdgcn_sqrtf(fmaf(-d.e, d.e, d.e + d.e));
                     u[t][i] *= m[t][i];
@@ -500,7 +510,7 @@ __global__ __launch_bounds__(256) void gate_step_kernel(GateArgs a, int groups) 
     load8<ROWS>(a.rate + e0, left, rate);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const Decay d(kLog2e * rate[i] * sigmoid(g[i]));
+        const Decay<true> d(kLog2e * rate[i] * sigmoid(g[i]));
         const float e = d.e;
         const float m = NORM ? __builtin_amdgcn_sqrtf(fmaf(-e, e, e + e)) : 1.f, f = 1.f - e;
         const bool strong = e > 0.5f;

@@ -263,3 +263,22 @@ def test_strong_decays_over_tiles(B, T, D, dtype):
         want, bound = so.gate_backward(xf, gf, rf, sf, dhf, dsf, normalize)
         for name, a, b, c in zip(("dx", "dg", "drate", "dstate"), got, want, bound):
             near(a, b, 2 * c, dtype if name in ("dx", "dg") else "f32", name)
+
+
+def test_fp32_inputs_keep_their_accuracy_at_every_decay():
+    # h = m x of one token, dx = m lam.  A gate of 0 is 1/2 exactly; q is off by 3 u (two products, log2 e), 1 - a by that
+    # and 4 u (a series' roundings, or an ulp of a >= 1/2 in a difference >= 0.29), 1 - a^2 by 2 u more, m by half of
+    # these and 2 u (the root), the product by u: 8 u
+    torch, dev = torch_dev()
+    msr = _msr()
+    D = 20000
+    r, rf = tensor(torch, dev, 2 * np.log(2) * np.geomspace(1e-4, 3, D))
+    m = np.sqrt(-np.expm1(-rf))
+    x, g = torch.ones(1, 1, D, device=dev), torch.zeros(1, 1, D, device=dev)
+    h, last, _ = msr.msr_gated_recurrence(x, g, r)
+    step = msr.msr_gated_recurrence_step(x[0], g[0], torch.zeros(1, D, device=dev), r)
+    dx = msr.msr_gated_recurrence_backward(x, g, r, x)[0]
+    for name, t in (("h", h), ("state", last), ("step", step), ("dx", dx)):
+        err = np.abs(down(t).ravel() / m - 1).max()
+        note(f"{name} {err:.1e}")
+        assert err <= 8 * U, name
