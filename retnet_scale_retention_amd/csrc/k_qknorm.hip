@@ -141,7 +141,7 @@ __global__ __launch_bounds__(256) void qk_norm_backward_kernel(QkArgs a) {
     load_weight8<ROWS>(a.w[1], a.w_bf16, e0, left, w[1]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[0][i] = dw[1][i] = 0.f;
-    const float dims = (float)a.dk, root = sqrtf(dims);
+    const float dims = (float)a.dk;
     for (int64_t tok = (int64_t)blockIdx.x * 4 + wave; tok < a.tokens; tok += (int64_t)gridDim.x * 4) {
         float cs[4], sn[4];
         angles(a, tok, th, cs, sn);
@@ -178,8 +178,10 @@ __global__ __launch_bounds__(256) void qk_norm_backward_kernel(QkArgs a) {
                         ss = fmaf(v[i], v[i], ss);
                         gx = fmaf(v[i], g[i] * w[k][i], gx);
                     }
-                    // r^2 = d / (sum(x^2) + d eps); roots first: the quotient overflows where the sum is subnormal
-                    const float t2 = fmaf(a.eps, dims, group_sum<L>(ss)), r = t2 == 0.f ? 0.f : root / sqrtf(t2);
+                    // r^2 = d / (sum(x^2) + d eps), which overflows where the sum is subnormal: there it is scaled first
+                    const float t2 = fmaf(a.eps, dims, group_sum<L>(ss));
+                    const bool low = t2 < 0x1p-96f;
+                    const float root = sqrtf(dims / (low ? t2 * 0x1p64f : t2)), r = t2 == 0.f ? 0.f : low ? root * 0x1p32f : root;
                     gx = group_sum<L>(gx);
                     const float c = r == 0.f ? 0.f : gx / t2;  // squares past fp32: n is 0, whatever the sum came to
                     if (head < H) {
