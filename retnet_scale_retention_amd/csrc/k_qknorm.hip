@@ -259,17 +259,18 @@ Split split(int64_t tokens, int H, int Hk, int dk, int64_t most) {
 
 // Workgroups along the tokens.  Results: 4096 (16384 tokens of 2 x 16 heads of 256 bf16 84 us; 1024 85).  Gradients of short
 // tokens, which a wave has done after a few rows, three on a CU, of long ones two (more rows apart at a time cost more than
-// they hide): bf16, 16384 tokens of 2 x 16 heads of 256 153 us with 512 and 159 with 768, of 32 + 8 heads of 128 94 and 95,
-// of 2 x 16 heads of 128 76 and 73, of 2 x 4 of 64 28.5 and 24.3, 41725 of 2 x 4 of 96 59 and 49.
+// they hide), by the bytes of Q and K in a token.  With 768 and with 512, 16384 tokens: bf16 2 x 4 heads of 64 24.3 and 28.5
+// us, 2 x 16 of 128 73.4 and 73.9, 32 + 8 of 128 95 and 94, 2 x 16 of 256 159 and 153; fp32 2 x 4 of 128 38.2 and 39.1, 2 x 4
+// of 256 79.1 and 79.9, 32 + 8 of 64 100 and 99, 2 x 8 of 256 155.5 and 152.2.
 constexpr int kForward = 4096;
-int backward_groups(int H, int Hk, int dk) { return (H + Hk) * dk <= 4096 ? 768 : 512; }
+int backward_groups(int H, int Hk, int dk, size_t e) { return (H + Hk) * dk * e <= 8192 ? 768 : 512; }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
 
 size_t qk_norm_backward_workspace(int64_t tokens, int H, int Hk, int dk) {
-    const Split s = split(tokens, H, Hk, dk, backward_groups(H, Hk, dk));
+    const Split s = split(tokens, H, Hk, dk, backward_groups(H, Hk, dk, 2));  // of either type: fp32 takes no more
     return (size_t)2 * s.x * s.y * dk * sizeof(float);
 }
 
@@ -285,7 +286,7 @@ hipError_t launch_qk_norm(const QkNorm &q, bool backward, hipStream_t st) {
     a.pos_rows = q.pos_rows, a.pos0 = q.pos0, a.tokens = q.tokens;
     a.dk = q.dk, a.T = q.T, a.w_bf16 = q.w_dtype == MSR_BF16, a.rotate = q.rotate, a.scale = q.scale, a.eps = q.eps;
     for (int i = 0; i < q.dk / 2; ++i) a.theta[i] = q.theta[i];
-    const int most = backward ? backward_groups(q.H[0], q.H[1], q.dk) : kForward;
+    const int most = backward ? backward_groups(q.H[0], q.H[1], q.dk, e) : kForward;
     const Split s = split(q.tokens, q.H[0], q.H[1], q.dk, most);
     const int parts = s.x * s.y;
     a.per = s.per;
