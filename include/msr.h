@@ -506,12 +506,13 @@ msr_status msr_qk_norm_rotate_backward(const msr_problem *p, int32_t key_heads, 
  *   wanted; it may be state_in); h may be NULL;
  *   carry (NULL: not wanted) [B][ceil(T / 64)][D] fp32: the states before the
  *   tokens 0, 64, 128, ..., for the backward pass.
- * Everything between loads and stores is fp32.  T = 0 copies the state.
+ * Everything between loads and stores is fp32; a decay is as accurate where it
+ * nearly forgets the state as where it hardly does.  T = 0 copies the state.
  * B, T and D are at most 2^31 - 1, and B * ceil(T / 64) * ceil(D / 128) below
  * 2^24.  Outputs must not overlap anything else.  The workspace is that of
  * msr_gated_recurrence_workspace(B, T, D, 0).  Equal calls give equal
  * results.  A NaN reaches every later token of its channel, an infinity too,
- * as NaN where a decay since is 0 in fp32.
+ * as NaN once the decay since then is 0 in fp32.
  */
 #define MSR_GATE_BLOCK 64
 msr_status msr_gated_recurrence(int64_t B, int64_t T, int64_t D, int32_t dtype, int32_t normalize, const void *x,

@@ -9,8 +9,9 @@
 // the sums in the same order (no atomics, the same norm on every run).
 //
 // Bound by memory: two reads and a write where the gradients exceed the
-// caches.  Five fp32 tensors of 403 MB together: 220 us in a loop, 231 on
-// changing inputs (1.2 GB, 5.2 TB/s; a 1 GiB copy reaches 5.06).  60 bf16
+// caches.  Five fp32 tensors of 403 MB together: 222 us in a loop (206 in
+// place), 231 on changing inputs (1.2 GB, 5.2 TB/s; a 1 GiB copy reaches
+// 5.06); 300 bf16 tensors of 189 MB in place 106 in a loop.  60 bf16
 // tensors of 37.8 MB together: 23 us of kernels (8.8 and 15); the call takes
 // the host 30 us in place (16 to write the table, 9 the C call) and 41 with
 // tensors for the results.

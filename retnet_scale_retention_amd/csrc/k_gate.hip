@@ -27,14 +27,18 @@
 // way the first never waits, so every wait ends.
 //
 // Memory is the floor, and the arithmetic (two exponentials, a reciprocal and
-// a root per element) is not hidden behind it whole.  2 x 8192 x 4096 bf16:
-// 96 us (403 MB, 4.2 TB/s; a 1 GiB copy reaches 5.06): 89 without the waits,
-// 79 without the gate's arithmetic, 70 without both.  131072 x 1024: 235 us
-// (814 MB, 3.5 TB/s): 174, 240 and 165; its eight chains wait for states.
-// Gradients of 2 x 8192 x 4096: 187 us (675 MB, 3.6 TB/s).  Persistent
-// workgroups that load the next tile ahead took 118 and 305 us through
-// registers, 114 and 275 through LDS; tiles of 32 channels by 512 tokens 114
-// and 253.
+// a root per element) is not hidden behind it whole.  Ten calls over one set of
+// inputs in a graph, 2 x 8192 x 4096 bf16: 93 us (403 MB, 4.3 TB/s; a 1 GiB
+// copy reaches 5.06): 85 without the waits, 81 without the gate's arithmetic,
+// 75 without both; on changing inputs 103.  131072 x 1024: 239 us (814 MB,
+// 3.4 TB/s): 176, 228 and 164, its eight chains wait for states; on changing
+// inputs 235.  fp32 2 x 8192 x 4096: 190 us (805 MB, 4.2 TB/s).  Gradients of
+// 2 x 8192 x 4096 bf16: 184 us (675 MB, 3.7 TB/s), on changing inputs 180.
+// Persistent workgroups that load the next tile ahead took 118 and 305 us
+// through registers, 114 and 275 through LDS, where these kernels took 96 and
+// 235; tiles of 32 channels by 512 tokens 114 and 253.  Tiles in the order of
+// the workgroups' indexes, without tickets, take 90 and 226 (239 with), but
+// nothing says that workgroups start in that order, and the waits rest on it.
 #include <algorithm>
 
 #include "msr_quant.hpp"
@@ -63,9 +67,10 @@ constexpr float kLog2e = 1.44269504f;
 
 // a = 2^-k and e = 1 - a.  Where k is small, e is a series and a is 1 - e; elsewhere e is 1 - a, off by the exponential's
 // error.  FINE: seven terms up to 1/2 (the first left out is 1.5e-8 of the sum); 1 - a is off by 2e-7 of itself there.  Else
-// three up to 1/32 (4e-7), and 1 - a is off by 1.5e-6 just above as measured (2.8e-6 by an ulp of a).  fp32 results, whose
-// kernels wait for memory, take the former at no cost (2 x 8192 x 2048 104 us with either; errors of the results 1.0e-7 to
-// 1.5e-7 of their norm with the latter, 0.6e-7 to 1.1e-7 with the former); bf16 ones, whose rounding is 4e-3, the latter.
+// three up to 1/32 (4e-7), and 1 - a is off by 1.5e-6 just above as measured (2.8e-6 by an ulp of a).  fp32 results take the
+// former at no cost (2 x 8192 x 2048 103.5 us with either; errors 1.0e-7 to 1.5e-7 of the results' norm with the latter,
+// 0.6e-7 to 1.1e-7 with the former), bf16 ones, whose rounding is 4e-3, the latter (2 x 8192 x 4096: 93 us, with the former
+// 97; gradients 184 and 193).
 template <bool FINE>
 struct Decay {
     float e, a;
@@ -94,8 +99,8 @@ __device__ __forceinline__ float sigmoid(float g) { return __builtin_amdgcn_rcpf
 
 // The gradients need s (1 - s) too, and 1 - s formed of an s next to 1 has few digits (0.5% off at g = 12, none left from 17
 // on): with c the lesser of s and 1 - s, both formed of exp(-|g|), it is c (1 - c).  Where the registers allow (bf16 in rows
-// of aligned groups: 252 of them), s and s (1 - s) are kept from one pass over a tile to the other; elsewhere c is, with a
-// sign that says which it is (-0: s = 1), at five more operations.
+// of aligned groups: 252 of them), s and s (1 - s) are kept from one pass over a tile to the other (2 x 8192 x 4096: 184 us,
+// with c alone 196); elsewhere c is, with a sign that says which it is (-0: s = 1).
 template <bool BOTH>
 struct Gated;
 template <>
@@ -148,8 +153,8 @@ __device__ __forceinline__ void publish(uint64_t *w, float z, float h) { store(w
 __device__ __forceinline__ void publish(uint64_t *w, float state) { store(w, pack(kState, state)); }
 
 constexpr int kSpins = 1 << 22;  // polls: seconds, far beyond any wait; an end for callers who share a workspace
-constexpr int kLook = 8;         // tiles looked at: 96 and 235 us (sizes above); with four 95 and 251, with 16 100 and 242
-constexpr int kSleep = 8;        // between polls, in 64 clocks: with two 97 and 236 us
+constexpr int kLook = 8;         // tiles looked at: 93 and 239 us (loops as above); with four 89 and 257, with 16 98 and 246
+constexpr int kSleep = 8;        // between polls, in 64 clocks: with two 93.5 and 240 us
 
 // the state that tile n of a chain starts from (w: tile 0's word; a tile's words are CH apart)
 template <int CH>
@@ -291,7 +296,8 @@ __global__ __launch_bounds__(64 * W) void gate_kernel(GateArgs a) {
             for (int t = 0; t < S; ++t)
                 if (t >= mine) close_gate(rg[t]);
         }
-        slice<sizeof(T) == 4, S, NORM>([&](int t, float (&x)[8], float (&g)[8]) { rx[t].get(x), rg[t].get(g); }, rate, keep, u, k, h);
+        slice<sizeof(T) == 4, S, NORM>([&](int t, float (&x)[8], float (&g)[8]) { rx[t].get(x), rg[t].get(g); }, rate, keep, u,
+                                       k, h);
 #pragma unroll
         for (int i = 0; i < 8; ++i) ks[sl][e0 + i] = k[i], hs[sl][e0 + i] = h[i];
     }
@@ -494,7 +500,8 @@ __global__ __launch_bounds__(64 * W) void gate_backward_kernel(GateArgs a) {
     }
 }
 
-// One token: h = a state + m x.  Where a >= 1/2 it is taken as two numbers, 1 - e rounded and the rest that this left out,
+// One token: h = a state + m x, bound by its launch where it is small (64 x 4096 bf16 3.5 us in a graph) and by memory (512
+// x 8192 bf16 11 us, 5.3 TB/s).  Where a >= 1/2 it is taken as two numbers, 1 - e rounded and the rest that this left out,
 // so that the state's roundings are those of the two sums alone; below, where 1 - e has few digits or none, it is the
 // exponential itself.
 template <typename T, int ROWS, bool NORM>
@@ -552,8 +559,8 @@ hipError_t by_type(int dtype, int D, bool norm, F f) {
 
 constexpr int kWaves = 4, kLanes = 16, kChannels = 8 * kLanes;  // of a tile: lanes across, channels
 
-// Tokens of a lane.  bf16 forward: 96 us (2 x 8192 x 4096) and 235 (131072 x 1024) with eight, 103 and 366 with four.
-// Gradients, whose registers hold more of each token: 187 us with four, 215 with eight.  fp32 holds twice the bits.
+// Tokens of a lane.  bf16 forward: 93 us (2 x 8192 x 4096) and 239 (131072 x 1024) with eight, 101 and 386 with four.
+// Gradients, whose registers hold more of each token: 184 us with four, 224 with eight.  fp32 holds twice the bits.
 constexpr int tokens_of(int dtype, bool backward) { return dtype == MSR_BF16 && !backward ? 8 : 4; }
 constexpr int tile_of(int dtype, bool backward) { return 64 / kLanes * kWaves * tokens_of(dtype, backward); }
 

@@ -951,7 +951,8 @@ def msr_gradient_norm(grads, *, out=None, workspace=None, stream=None):
 def msr_clip_gradients(grads, max_norm, *, norm=None, out=None, norm_out=None, workspace=None, stream=None):
     """g * min(1, max_norm / norm) for every tensor g of `grads` (contiguous, float32 and bfloat16), in place or to the
     tensors `out`.  norm: a float32 scalar on the device, e.g. one joined over processes; None: that of msr_gradient_norm,
-    formed here (norm_out: the scalar to write it to).  Where it is infinite or NaN the gradients stay as they are.  Returns (out or grads, norm)."""
+    formed here (norm_out: the scalar to write it to).  Where it is infinite or NaN the gradients stay as they are.
+    Returns (out or grads, norm)."""
     tc = _tc or _setup()
     grads = list(grads)
     if out is not None:
